@@ -178,6 +178,45 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
                                        fs_stream_t stream);
 
 /*
+ * Windowed attention with a learned relative position bias by buckets (the
+ * additive bias of a Swin layer, which the FlashSwin pages replace by RoPE): per
+ * head h and pair of window positions
+ *   S_tu = q_t . k_u / sqrt(d) + table[h][b],
+ *   b = buckets[(i_t - i_u + M - 1) (2M - 1) + (j_t - j_u + M - 1)],
+ * (i, j) the row and column inside the window (rolled frame), the same for every
+ * window, added before the shift mask.  No rotation.
+ *
+ * Shapes: those of fs_winattn_check_shape with d == 32 (else FS_ERR_SHAPE).
+ * table: bf16 [heads][n_buckets], 2-byte aligned, 1 <= n_buckets <= 2^20.
+ * buckets: int32 [(2M-1)^2] in DEVICE memory, or NULL: the displacement index is
+ * the bucket and n_buckets must be (2M-1)^2 (else FS_ERR_SHAPE).  A bucket outside
+ * [0, n_buckets) adds no bias and takes no gradient.  An entry of -inf keeps its
+ * pairs apart; a query left without a key has o = 0, lse = -inf and no gradient.
+ * Finite entries beyond 8.5e37 in magnitude act as that value; a query whose
+ * log-sum-exp lies beyond 1e30 in magnitude takes part in no gradient.
+ *
+ * Forward: o and lse (lse may be NULL: inference), overwritten.
+ * Backward: dq, dk, dv and dtable (bf16 [heads][n_buckets]: the gradient summed in
+ * fp32 over every window of the batch and every pair of the bucket, in a fixed
+ * order), all overwritten.  At M >= 16 dq is accumulated in fp32 with bulk
+ * reductions whose order varies from run to run; everything else, and at M <= 8
+ * every output, is the same from run to run.  workspace: at least
+ * fs_winattn_relbias_bwd_workspace_bytes(shape) bytes, 256-byte aligned (M >= 16:
+ * 136 bytes per token-head on the padded grid; and 4 bytes a displacement for
+ * every head and CTA).  Other arguments, layouts, ownership and errors as
+ * fs_winattn_fwd / fs_winattn_bwd.  At M = 8 and M = 4, where windows share a
+ * tile, values that are not finite stay inside their own window.
+ */
+FS_API fs_status fs_winattn_relbias_fwd(const fs_winattn_shape* shape, const void* q, const void* k, const void* v,
+                                        const void* table, const int* buckets, int n_buckets, void* o, float* lse,
+                                        fs_stream_t stream);
+FS_API size_t fs_winattn_relbias_bwd_workspace_bytes(const fs_winattn_shape* shape);
+FS_API fs_status fs_winattn_relbias_bwd(const fs_winattn_shape* shape, const void* q, const void* k, const void* v,
+                                        const void* o, const void* dout, const float* lse, const void* table,
+                                        const int* buckets, int n_buckets, void* dq, void* dk, void* dv, void* dtable,
+                                        void* workspace, size_t workspace_bytes, fs_stream_t stream);
+
+/*
  * Training pair.  fs_winattn_fwd_train is fs_winattn_fwd (lse required) that
  * also leaves, in `workspace` (the backward's: at least
  * fs_winattn_bwd_workspace_bytes(shape) bytes, 256-byte aligned), the rotated

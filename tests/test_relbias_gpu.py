@@ -1,0 +1,202 @@
+"""GPU parity of the relative-position-bias attention against its fp64 oracle, element by element within the oracle's
+own error bounds; lse (fp32) within 2^-16 of the larger of 1 and its size (fp32 scores of a few tens, their sum and
+the logarithm's and exponential's few steps of 2^-22)."""
+import pytest
+import torch
+
+from oracle import relbias
+from vision_transformer_windowed_b200 import _lib, ops
+from vision_transformer_windowed_b200.inputs import make_inputs
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.fixture(autouse=True)
+def _device_status_clean():
+    _lib.fs_set_wait_limit_ns(4_000_000_000)
+    _lib.fs_device_status()
+    yield
+    torch.cuda.synchronize()
+    assert _lib.fs_device_status() == 0
+
+
+def draw(B, H, W, heads, M, n=None, qk_scale=1.0, std=0.7, seed=3):
+    inp = make_inputs(B, H, W, heads, 32, qk_scale=qk_scale)
+    inp.pop("theta")
+    g = torch.Generator().manual_seed(seed)
+    n = (2 * M - 1) ** 2 if n is None else n
+    inp["table"] = (torch.randn((heads, n), generator=g) * std).to(torch.bfloat16)
+    return inp
+
+
+def run(inp, M, s, buckets=None):
+    d = {k: t.cuda() for k, t in inp.items()}
+    bk = None if buckets is None else buckets.cuda()
+    o, lse = ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], M, s, buckets=bk)
+    dq, dk, dv, dt = ops.winattn_relbias_bwd(d["q"], d["k"], d["v"], o, d["dout"], lse, d["table"], M, s, buckets=bk)
+    torch.cuda.synchronize()
+    return dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv, dtable=dt)
+
+
+def compare(got, ref, err, keys=("o", "lse", "dq", "dk", "dv", "dtable")):
+    for key in keys:
+        a, b = got[key].double().cpu(), ref[key]
+        assert a.shape == b.shape, key
+        if key == "lse":
+            fine = torch.isfinite(b)
+            assert torch.equal(a[~fine], b[~fine])
+            assert ((a - b)[fine].abs() <= 2.0 ** -16 * b[fine].abs().clamp(min=1.0)).all(), key
+            continue
+        assert torch.isfinite(a).all(), f"{key}: non-finite values"
+        # 1e-6 of the largest: fp32 sums that cancel to near zero
+        over = (a - b).abs() - (err[key] * (1 + 1e-3) + 1e-6 * max(1.0, float(b.abs().max())))
+        assert over.max() <= 0, f"{key}: {float(over.max()):.3g} over its bound, error {float((a - b).abs().max()):.3g}"
+
+
+CASES = [  # (B, H, W, heads, M, s)
+    (1, 4, 4, 1, 4, 0),
+    (1, 8, 12, 2, 4, 0),      # 6 windows: a ragged tile
+    (2, 10, 6, 3, 4, 0),      # padded
+    (1, 8, 8, 1, 8, 0),       # one window: half a tile
+    (2, 16, 16, 2, 8, 0),
+    (2, 16, 16, 3, 8, 4),
+    (1, 8, 24, 1, 8, 4),      # three windows
+    (1, 20, 13, 2, 8, 4),     # padded, shifted
+    (1, 16, 16, 5, 16, 0),
+    (1, 32, 32, 2, 16, 8),
+    (1, 32, 48, 1, 16, 4),
+    (1, 40, 36, 2, 16, 12),   # padded
+    (1, 32, 32, 2, 32, 0),
+    (1, 64, 64, 1, 32, 16),
+    (1, 64, 40, 1, 32, 8),
+    (1, 33, 64, 1, 32, 20),
+    (1, 64, 64, 1, 64, 0),
+    (1, 64, 64, 1, 64, 32),
+    (1, 64, 70, 1, 64, 16),
+    (1, 64, 64, 1, 64, 24),
+    (1, 64, 64, 1, 64, 4),
+]
+
+
+@pytest.mark.parametrize("cfg", CASES)
+def test_parity(cfg):
+    inp = draw(*cfg[:5])
+    compare(run(inp, *cfg[4:]), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], *cfg[4:], dout=inp["dout"]))
+
+
+@pytest.mark.parametrize("cfg", [(1, 8, 12, 2, 4, 0), (2, 16, 16, 3, 8, 4), (1, 32, 32, 2, 16, 8), (1, 32, 32, 40, 16, 0),
+                                 (1, 64, 64, 1, 32, 16)])
+def test_parity_by_buckets(cfg):
+    """Shared buckets, with some displacements outside the table on either side."""
+    B, H, W, heads, M, s = cfg
+    buckets, n = ops.log_distance_buckets(M, exact=2, device="cpu")
+    buckets[0, 0], buckets[-1, -1], buckets[M - 1, 0] = -1, n, 2 ** 31 - 1
+    inp = draw(B, H, W, heads, M, n)
+    compare(run(inp, M, s, buckets), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, buckets=buckets,
+                                                  dout=inp["dout"]))
+
+
+@pytest.mark.parametrize("cfg", [(1, 8, 8, 2, 4, 0), (2, 16, 16, 3, 8, 4), (1, 32, 32, 2, 16, 8), (1, 64, 64, 1, 32, 16)])
+def test_sharp_softmax_and_masked_displacements(cfg):
+    """Peaked rows, a wide bias, entries of -inf and of the type's lowest value."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(B, H, W, heads, M, qk_scale=3.0, std=4.0)
+    n = inp["table"].shape[1]
+    inp["table"][:, 1] = -INF
+    inp["table"][0, n // 2 + 1] = -INF
+    inp["table"][0, 2:n // 3] = torch.finfo(torch.bfloat16).min
+    compare(run(inp, M, s), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"]))
+
+
+@pytest.mark.parametrize("M", [4, 8, 16, 32])
+def test_rows_without_a_key(M):
+    """Head 0 attends nothing, head 1 only one displacement that the window's last rows lack."""
+    inp = draw(1, M, M, 2, M)
+    inp["table"][:] = -INF
+    inp["table"][1, (M - 2) * (2 * M - 1) + M - 1] = 0.25  # the key one row below
+    got = run(inp, M, 0)
+    ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, 0, dout=inp["dout"])
+    assert (ref["lse"][..., 0] == -INF).all() and torch.isfinite(ref["lse"][0, :-1, :, 1]).all()
+    compare(got, ref, err)
+    assert (got["o"][..., 0, :] == 0).all() and (got["dq"][..., 0, :] == 0).all()
+
+
+@pytest.mark.parametrize("M", [4, 8, 16])
+def test_every_entry_of_the_lowest_value_is_the_uniform_row(M):
+    inp = draw(1, M, M, 1, M)
+    inp["table"][:] = torch.finfo(torch.bfloat16).min
+    o, _ = ops.winattn_relbias_fwd(*(inp[k].cuda() for k in ("q", "k", "v", "table")), M, 0, need_lse=False)
+    mean = inp["v"].double().reshape(-1, 32).mean(0)
+    bound = 2.0 ** -7 * inp["v"].double().abs().reshape(-1, 32).mean(0)  # P's rounding and o's
+    assert ((o.double().cpu() - mean).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M", [4, 8])
+def test_values_that_are_not_finite_stay_in_their_window(M):
+    """Small windows share a tile with their neighbours."""
+    inp = draw(1, M, 4 * M, 1, M)
+    clean = run(inp, M, 0)
+    for name in ("q", "k", "v", "dout"):
+        inp[name][:, :, M:2 * M] = INF if name == "v" else float("nan")
+    got = run(inp, M, 0)
+    for key in ("o", "lse", "dq", "dk", "dv"):
+        for part in (slice(0, M), slice(2 * M, 4 * M)):
+            assert torch.equal(got[key][:, :, part], clean[key][:, :, part]), key
+
+
+def test_inference_forward_repeats_and_leaves_nothing_else_written():
+    inp = draw(2, 40, 36, 2, 16)
+    d = {k: t.cuda() for k, t in inp.items()}
+    a = run(inp, 16, 8)
+    b = run(inp, 16, 8)
+    o, none = ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], 16, 8, need_lse=False)
+    assert none is None and torch.equal(o, a["o"])
+    for key in ("o", "lse", "dk", "dv", "dtable"):
+        assert torch.equal(a[key], b[key]), key
+    # outputs inside larger buffers: the bytes around them stay
+    big = torch.full((o.numel() + 64,), 7.0, device="cuda", dtype=torch.bfloat16)
+    view = big[32:-32].view(o.shape)
+    ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], 16, 8, o=view, need_lse=False)
+    assert torch.equal(view, o) and (big[:32] == 7).all() and (big[-32:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [8, 16])
+def test_autograd_other_stream_and_graph(M):
+    inp = draw(1, 32, 32, 2, M)
+    want = run(inp, M, 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        leaves = [inp[k].cuda().requires_grad_() for k in ("q", "k", "v", "table")]
+        o = ops.window_attention_relbias(*leaves, M, 0)
+        grads = torch.autograd.grad(o, leaves, inp["dout"].cuda())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(o.detach(), want["o"])
+    for t, key in zip(grads, ("dq", "dk", "dv", "dtable")):
+        if key == "dq" and M >= 16:  # two fp32 sums in either order: commutative, equal up to the zero they start from
+            assert (t.float() - want[key].float()).abs().max() <= 2.0 ** -7 * want[key].float().abs().max()
+        else:
+            assert torch.equal(t, want[key]), key
+    d = {k: t.cuda() for k, t in inp.items()}
+    ws = ops.alloc_relbias_workspace(d["q"], M, 0)
+    out, lse = ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], M, 0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], M, 0, o=out, lse=lse)
+        dq, dk, dv, dt = ops.winattn_relbias_bwd(d["q"], d["k"], d["v"], out, d["dout"], lse, d["table"], M, 0,
+                                                 workspace=ws)
+    new = draw(1, 32, 32, 2, M, seed=9)
+    d["table"].copy_(new["table"])
+    inp["table"] = new["table"]
+    g.replay()
+    torch.cuda.synchronize()
+    again = run(inp, M, 0)
+    assert torch.equal(out, again["o"]) and torch.equal(dt, again["dtable"]) and torch.equal(dk, again["dk"])
+
+
+def test_empty_batch_zeroes_the_table_gradient():
+    inp = draw(0, 16, 16, 2, 8)
+    got = run(inp, 8, 0)
+    assert got["o"].numel() == 0 and (got["dtable"] == 0).all()

@@ -81,6 +81,12 @@ def load(build_if_missing: bool = True):
         lib.fs_winattn_lrbias_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.fs_winattn_lrbias_bwd.argtypes = [P] + [vp] * 9 + [ctypes.c_int] + [vp] * 7 + [ctypes.c_size_t, vp]
         lib.fs_winattn_lrbias_bwd.restype = st
+        lib.fs_winattn_relbias_fwd.argtypes = [P] + [vp] * 5 + [ctypes.c_int] + [vp] * 3
+        lib.fs_winattn_relbias_fwd.restype = st
+        lib.fs_winattn_relbias_bwd_workspace_bytes.argtypes = [P]
+        lib.fs_winattn_relbias_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.fs_winattn_relbias_bwd.argtypes = [P] + [vp] * 8 + [ctypes.c_int] + [vp] * 5 + [ctypes.c_size_t, vp]
+        lib.fs_winattn_relbias_bwd.restype = st
         _lib = lib
         return lib
 
@@ -162,6 +168,24 @@ def fs_winattn_lrbias_bwd(shape: Shape, q: int, k: int, v: int, o: int, dout: in
     _check(load().fs_winattn_lrbias_bwd(ctypes.byref(shape), q, k, v, o, dout, lse, theta, u, w, int(rank), dq, dk,
                                         dv, dtheta, du, dw, workspace, workspace_bytes, stream),
            "fs_winattn_lrbias_bwd")
+
+
+def fs_winattn_relbias_fwd(shape: Shape, q: int, k: int, v: int, table: int, buckets: int, n_buckets: int, o: int,
+                           lse: int, stream: int) -> None:
+    _check(load().fs_winattn_relbias_fwd(ctypes.byref(shape), q, k, v, table, buckets, int(n_buckets), o, lse, stream),
+           "fs_winattn_relbias_fwd")
+
+
+def fs_winattn_relbias_bwd_workspace_bytes(shape: Shape) -> int:
+    return int(load().fs_winattn_relbias_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def fs_winattn_relbias_bwd(shape: Shape, q: int, k: int, v: int, o: int, dout: int, lse: int, table: int,
+                           buckets: int, n_buckets: int, dq: int, dk: int, dv: int, dtable: int, workspace: int,
+                           workspace_bytes: int, stream: int) -> None:
+    _check(load().fs_winattn_relbias_bwd(ctypes.byref(shape), q, k, v, o, dout, lse, table, buckets, int(n_buckets),
+                                         dq, dk, dv, dtable, workspace, workspace_bytes, stream),
+           "fs_winattn_relbias_bwd")
 
 
 def fs_device_status() -> int:

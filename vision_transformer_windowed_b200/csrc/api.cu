@@ -86,6 +86,21 @@ fs_status encode_box_map(CUtensorMap* m, const void* base, const Geo& g) {
     return r == CUDA_SUCCESS ? FS_OK : FS_ERR_CUDA;
 }
 
+// Geometry of a call with a relative position bias: heads of 32 channels; without
+// a bucket map the table has one entry a displacement.
+fs_status relbias_geo(const fs_winattn_shape* shape, const int* buckets, int n_buckets, Geo* g) {
+    const fs_status st = make_geo(shape, g);
+    if (st != FS_OK) return st;
+    const int nd = (2 * g->M - 1) * (2 * g->M - 1);
+    if (g->d != 32 || n_buckets < 1 || n_buckets > (1 << 20) || (!buckets && n_buckets != nd)) return FS_ERR_SHAPE;
+    return FS_OK;
+}
+
+bool relbias_aligned(const void* table, const int* buckets, const float* lse) {
+    return !(reinterpret_cast<uintptr_t>(table) & 1u) && !(reinterpret_cast<uintptr_t>(buckets) & 3u) &&
+           !(reinterpret_cast<uintptr_t>(lse) & 3u);
+}
+
 __global__ void bounded_wait_selftest_kernel(unsigned int* status, unsigned long long limit_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -407,6 +422,100 @@ fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void* q, co
     p.dw = dw;
     p.ws = static_cast<uint8_t*>(workspace);
     const cudaError_t e = launch_lrbias_bwd(g, p, status, lim, sms, cs, g_phase_n >= 5 ? g_phase_events : nullptr);
+    return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+fs_status fs_winattn_relbias_fwd(const fs_winattn_shape* shape, const void* q, const void* k, const void* v,
+                                 const void* table, const int* buckets, int n_buckets, void* o, float* lse,
+                                 fs_stream_t stream) {
+    Geo g;
+    fs_status st = relbias_geo(shape, buckets, n_buckets, &g);
+    if (st != FS_OK) return st;
+    if (g.B == 0) return FS_OK;
+    if (!q || !k || !v || !table || !o) return FS_ERR_NULL;  // buckets and lse may be NULL
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !relbias_aligned(table, buckets, lse))
+        return FS_ERR_ALIGN;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    RelbMaps maps{};
+    if (g.N >= kTile &&
+        (encode_box_map(&maps.q, q, g) || encode_box_map(&maps.k, k, g) || encode_box_map(&maps.v, v, g)))
+        return FS_ERR_CUDA;
+    unsigned long long lim;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        lim = g_limit_ns;
+    }
+    RelbPtrs p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.table = table;
+    p.buckets = buckets;
+    p.n_buckets = n_buckets;
+    p.o_out = o;
+    p.lse_out = lse;
+    const cudaError_t e = launch_relbias_fwd(g, p, maps, status, lim, sms, reinterpret_cast<cudaStream_t>(stream),
+                                             g_phase_n >= 2 ? g_phase_events : nullptr);
+    return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+size_t fs_winattn_relbias_bwd_workspace_bytes(const fs_winattn_shape* shape) {
+    Geo g;
+    if (make_geo(shape, &g) != FS_OK || g.d != 32) return 0;
+    return relbias_bwd_workspace_bytes(g);
+}
+
+fs_status fs_winattn_relbias_bwd(const fs_winattn_shape* shape, const void* q, const void* k, const void* v,
+                                 const void* o, const void* dout, const float* lse, const void* table,
+                                 const int* buckets, int n_buckets, void* dq, void* dk, void* dv, void* dtable,
+                                 void* workspace, size_t workspace_bytes, fs_stream_t stream) {
+    Geo g;
+    fs_status st = relbias_geo(shape, buckets, n_buckets, &g);
+    if (st != FS_OK) return st;
+    if (!dtable) return FS_ERR_NULL;
+    if (!relbias_aligned(dtable, nullptr, nullptr)) return FS_ERR_ALIGN;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (g.B == 0) {  // empty batch: the table gradient is an empty sum
+        if ((st = device_state(&status, &sms)) != FS_OK) return st;
+        return cudaMemsetAsync(dtable, 0, 2ull * g.heads * n_buckets, cs) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+    }
+    if (!q || !k || !v || !o || !dout || !lse || !table || !dq || !dk || !dv) return FS_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned16(dq) ||
+        !aligned16(dk) || !aligned16(dv) || !relbias_aligned(table, buckets, lse))
+        return FS_ERR_ALIGN;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < relbias_bwd_workspace_bytes(g))
+        return FS_ERR_WORKSPACE;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    RelbMaps maps{};
+    if (g.N >= kTile && (encode_box_map(&maps.q, q, g) || encode_box_map(&maps.k, k, g) ||
+                         encode_box_map(&maps.v, v, g) || encode_box_map(&maps.dout, dout, g)))
+        return FS_ERR_CUDA;
+    unsigned long long lim;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        lim = g_limit_ns;
+    }
+    RelbPtrs p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.o = o;
+    p.dout = dout;
+    p.table = table;
+    p.buckets = buckets;
+    p.n_buckets = n_buckets;
+    p.lse = lse;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dtable = dtable;
+    p.ws = static_cast<uint8_t*>(workspace);
+    const cudaError_t e = launch_relbias_bwd(g, p, maps, status, lim, cs, g_phase_n >= 5 ? g_phase_events : nullptr);
     return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
 }
 

@@ -123,6 +123,32 @@ cudaError_t launch_lrbias_fwd(const Geo& g, const LrbPtrs& p, unsigned int* stat
 cudaError_t launch_lrbias_bwd(const Geo& g, const LrbPtrs& p, unsigned int* status, unsigned long long limit_ns,
                               int num_sms, cudaStream_t stream, cudaEvent_t const* events);
 
+// Windowed attention with a learned relative position bias by buckets (heads of
+// 32 channels, every window size).
+struct RelbPtrs {
+    const void *q, *k, *v, *o, *dout;  // bf16 [B, H, W, heads, 32]
+    const void* table;                 // bf16 [heads][n_buckets]
+    const int* buckets;                // [(2M-1)^2] displacement -> bucket, or null: the displacement is the bucket
+    int n_buckets;
+    const float* lse;
+    void *o_out, *dq, *dk, *dv, *dtable;  // o_out: the forward's O; dtable: bf16 [heads][n_buckets]
+    float* lse_out;
+    uint8_t* ws;
+};
+size_t relbias_bwd_workspace_bytes(const Geo& g);
+// events as for the 64-channel kernels (the backward's last mark follows the
+// table gradient's sum; windows of fewer than 128 tokens run one kernel in the
+// place of prep, main and post).
+// TMA maps of the token tensors, read by windows of 128 tokens or more.
+struct RelbMaps {
+    CUtensorMap q, k, v, dout;
+};
+cudaError_t launch_relbias_fwd(const Geo& g, const RelbPtrs& p, const RelbMaps& maps, unsigned int* status,
+                               unsigned long long limit_ns, int num_sms, cudaStream_t stream,
+                               cudaEvent_t const* events);
+cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& maps, unsigned int* status,
+                               unsigned long long limit_ns, cudaStream_t stream, cudaEvent_t const* events);
+
 // Fixed-order d theta sum: part [heads][per_head][16] -> dtheta [heads][16] (one
 // launch; cnt: heads counters that are zero when it starts).
 namespace bwdk {

@@ -1,0 +1,936 @@
+// Attention with a learned relative position bias, windows of fewer than 128
+// tokens: M = 8 on the tensor cores (two windows to a 128-slot tile), M = 4 on
+// the CUDA cores (a half warp is a window).  A work item is one (tile, head); all
+// of its attention, and every gradient of its tokens, stays inside it.
+//
+// Windows that share a tile must not reach each other, not even through a
+// product 0 x inf.  At M = 8 a row therefore keeps only the 64 columns of its own
+// window: the probabilities are a compact [128 rows x 64] operand, multiplied once
+// with each window's 64 value rows into an accumulator of its own, and a row reads
+// its own window's.  That is the same tensor work as one 128-column product, half
+// the TMEM traffic, and nothing has to be filled with zeros.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "dgeo.cuh"
+#include "geometry.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "relbias.cuh"
+#include "rows.cuh"
+
+namespace fswin {
+
+namespace relb {
+
+constexpr float kScale = 0.17677669529663688f;  // 1 / sqrt(32)
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kM8 = 8, kP8 = bias_pitch(8, 8);  // window side, table pitch (the same for boxes of 8 and of 4)
+static_assert(bias_pitch(8, 4) == kP8, "one pitch for both shifts");
+
+// Window position of local slot e of an 8 x 8 window stored in boxes of kBW x kBW.
+template <int kBW>
+__host__ __device__ constexpr int slot_i(int e) {
+    return kBW == 8 ? e >> 3 : ((e >> 5) << 2) + ((e >> 2) & 3);
+}
+template <int kBW>
+__host__ __device__ constexpr int slot_j(int e) {
+    return kBW == 8 ? e & 7 : (((e >> 4) & 1) << 2) + (e & 3);
+}
+// Table offset of local slot e relative to window position (0, 0).
+template <int kBW>
+__host__ __device__ constexpr int slot_off(int e) {
+    return slot_i<kBW>(e) * kP8 + slot_j<kBW>(e);
+}
+
+// cp.async copies of a warp's 32 rows: lane l moves 16-byte chunk l % 4 of rows
+// l / 4 + 8 i, eight whole 64-byte rows an instruction.
+__device__ __forceinline__ void load_rows(uint8_t* tile, const uint8_t* src, long long tok, bool valid, int warp,
+                                          int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rl = (lane >> 2) + 8 * i, c = lane & 3;
+        const long long tk = __shfl_sync(0xFFFFFFFFu, tok, rl);
+        const bool vd = __shfl_sync(0xFFFFFFFFu, valid ? 1 : 0, rl) != 0;
+        const int row = warp * 32 + rl;
+        cp_async16(smem_u32(tile + row * kRowBytes + ((c ^ ((row >> 1) & 3)) << 4)),
+                   vd ? src + tk * kRowBytes + 16 * c : src, vd ? 16u : 0u);
+    }
+}
+
+__device__ __forceinline__ void save_rows(uint8_t* dst, const uint8_t* tile, long long tok, bool valid, int warp,
+                                          int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rl = (lane >> 2) + 8 * i, c = lane & 3;
+        const long long tk = __shfl_sync(0xFFFFFFFFu, tok, rl);
+        const bool vd = __shfl_sync(0xFFFFFFFFu, valid ? 1 : 0, rl) != 0;
+        const int row = warp * 32 + rl;
+        if (vd)
+            *reinterpret_cast<uint4*>(dst + tk * kRowBytes + 16 * c) =
+                *reinterpret_cast<const uint4*>(tile + row * kRowBytes + ((c ^ ((row >> 1) & 3)) << 4));
+    }
+}
+
+// The 16-column groups of its own window that row r attends (bit b: local slots
+// [16 b, 16 b + 16)), from the tile's segment bytes.
+__device__ __forceinline__ uint32_t own_groups(const Geo& g, long long X, int r) {
+    if (!g.s) return 0xFu;
+    const uint64_t segs = d_tile_segs(g, X, d_tile_win(g, X));
+    return (allow16(g, seg_at(segs, r >> g.lBT), segs) >> (4 * (r >> 6))) & 0xFu;
+}
+
+// ------------------------------------------------------------------ M = 8 forward
+namespace fwd8 {
+
+constexpr int kThreads = 128;
+constexpr int kSlotBytes = 3 * kTileBytes;  // q, k, v tiles of one item
+constexpr int kTabOff = 2 * kSlotBytes;     // two slots
+constexpr int kTabBytes = 15 * kP8 * 4;
+constexpr int kBarOff = (kTabOff + kTabBytes + 15) / 16 * 16;
+constexpr int kSmemBytes = kBarOff + 64 + 1024;  // + alignment of the base
+constexpr uint32_t kTmemCols = 128;
+// S [0, 128); compact P (bf16) [0, 32); the two windows' O [64, 96), [96, 128).
+// P and O only take columns whose scores have been read.
+constexpr uint32_t kColP = 0, kColO = 64;
+
+struct Bars {
+    uint64_t s_full, p_ready, o_full, grp, done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Bars) <= 64, "barrier block overflows its slot");
+
+struct Params {
+    Geo g;
+    const uint8_t *q, *k, *v;
+    uint8_t* o;
+    const __nv_bfloat16* table;
+    const int* buckets;
+    int n_buckets;
+    float* lse;
+    unsigned int* status;
+    unsigned long long limit_ns;
+    int streams;
+};
+
+// Four CTAs an SM, each one row a thread: the chain copy -> S -> softmax -> O of
+// an item is latency-bound, so other CTAs' items fill the gaps.
+template <int kBW>
+__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant__ Params prm) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
+    float* tab = reinterpret_cast<float*>(smem + kTabOff);
+    const Geo& g = prm.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = tid, wi = warp >> 1;
+    const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
+
+    if (tid == 0) {
+        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->p_ready, 4);
+        mbar_init(&bars->o_full, 1);
+        mbar_init(&bars->grp, 4);
+        mbar_init(&bars->done, 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&bars->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    auto row_tok = [&](long long X, long long* tok) {
+        int pi, pj;
+        return slot_token(g, X, r, h, &pi, &pj, tok);
+    };
+    auto copy_item = [&](int slot, long long tok, bool valid) {
+        uint8_t* sl = smem + slot * kSlotBytes;
+        load_rows(sl, prm.q, tok, valid, warp, lane);
+        load_rows(sl + kTileBytes, prm.k, tok, valid, warp, lane);
+        load_rows(sl + 2 * kTileBytes, prm.v, tok, valid, warp, lane);
+    };
+    long long X = stream, tok = 0, tok_n = 0;
+    bool valid = X < g.tiles && row_tok(X, &tok), valid_n = false;
+    if (X < g.tiles) copy_item(0, tok, valid);
+    cp_async_commit();
+    long long Xn = X + prm.streams;
+    if (Xn < g.tiles) {
+        valid_n = row_tok(Xn, &tok_n);
+        copy_item(1, tok_n, valid_n);
+    }
+    cp_async_commit();
+    build_bias(tab, kP8, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, kM8, tid,
+               kThreads);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
+    const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+    const uint32_t id_pv = make_idesc_bf16(kTile, kHeadDim, false, true);  // P (TMEM) x V
+    const uint32_t sbase = smem_u32(smem);
+    const uint64_t dK0 = make_sdesc(sbase, 16, 512, kSw64);     // K-major, 64-byte rows
+    const uint64_t dMN0 = make_sdesc(sbase, 8192, 512, kSw64);  // MN-major, 64-byte rows
+    const float sl2 = g.scale_log2;
+    const int e_r = r & 63;  // local slot: its window position does not depend on the item
+    const float* brow = tab + (slot_i<kBW>(e_r) + kM8 - 1) * kP8 + slot_j<kBW>(e_r) + kM8 - 1;
+    uint32_t gph = 0, ph = 0;
+    auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
+    };
+    for (int j = 0; X < g.tiles; ++j) {
+        uint8_t* sl = smem + (j & 1) * kSlotBytes;
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->grp);
+        if (!wwait(&bars->grp, gph, 0x7301)) break;  // every row's copies landed; the previous item's O was read
+        gph ^= 1;
+        const uint64_t qo = static_cast<uint64_t>(((j & 1) * kSlotBytes) >> 4);
+        if (r == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 16; ++k)
+                umma_ss(tmem, dK0 + qo + 2 * k, dK0 + qo + (kTileBytes >> 4) + 2 * k, id_s, k > 0);
+            umma_commit(&bars->s_full);
+        }
+        const uint32_t grp4 = own_groups(g, X, r);
+        if (!wwait(&bars->s_full, ph, 0x7302)) break;
+        tc_fence_after();
+        float t[64];
+        {
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                tmem_ld32(trow + 64 * wi + 32 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const int a = 32 * c + e;
+                    ffma2(t[a], t[a + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2,
+                          brow[-slot_off<kBW>(a)], brow[-slot_off<kBW>(a + 1)]);
+                }
+            }
+        }
+        if (grp4 != 0xFu) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+                if (!((grp4 >> (e >> 4)) & 1u)) t[e] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], t[e], t[e + 1]);
+        const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+        const float mu = m == -INFINITY ? 0.f : m;  // a row whose every key is masked: P = 0
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int a = 32 * c + 2 * e;
+                float t0, t1;
+                fadd2(t0, t1, t[a], t[a + 1], -mu, -mu);
+                const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                const int s = (e & 1) * 2;
+                fadd2(l4[s], l4[s + 1], l4[s], l4[s + 1], p0, p1);
+                w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
+            }
+            tmem_st16(trow + kColP + 16 * c, w);
+        }
+        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_ready);
+        if (r == 0 && mbar_wait(&bars->p_ready, ph, ctl, 0x7203)) {
+            tc_fence_after();
+            const uint64_t vo = qo + (2 * kTileBytes >> 4);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_ts(tmem + kColO + 32 * w, tmem + kColP + 8 * k, dMN0 + vo + 256 * w + 64 * k, id_pv, k > 0);
+            umma_commit(&bars->o_full);
+        }
+        if (!wwait(&bars->o_full, ph, 0x7304)) break;
+        tc_fence_after();
+        {
+            uint32_t v[32];
+            tmem_ld32(trow + kColO + 32 * wi, v);
+            tmem_wait_ld();
+            tc_fence_before();  // ordered before the next item's products by its group barrier
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: O = 0; a NaN stays one
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(v[e]) * inv;
+            store_row_swz(sl, r, x);  // over q
+        }
+        if (valid && prm.lse != nullptr) prm.lse[tok] = (m + lg2_approx(l)) * kLn2;
+        __syncwarp();
+        save_rows(prm.o, sl, tok, valid, warp, lane);
+        __syncwarp();  // the staged rows are read: the slot takes the rows of the item after the next
+        X = Xn;
+        tok = tok_n;
+        valid = valid_n;
+        Xn += prm.streams;
+        if (Xn < g.tiles) {
+            valid_n = row_tok(Xn, &tok_n);
+            copy_item(j & 1, tok_n, valid_n);
+        }
+        cp_async_commit();
+        ph ^= 1;
+    }
+    cp_async_wait<0>();
+    if (r == 0) {  // every product issued here has completed before the columns are freed
+        umma_commit(&bars->done);
+        mbar_wait(&bars->done, 0, ctl, 0x72ff);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace fwd8
+
+// ------------------------------------------------------------------ M = 8 backward
+namespace bwd8 {
+
+constexpr int kThreads = 160;  // four row warps, one mover warp
+constexpr int kWarpMover = 4;
+constexpr int kSlotBytes = 4 * kTileBytes;          // q, k, v, dO tiles of one item
+constexpr int kOOff = 2 * kSlotBytes;               // o tile
+constexpr int kDSOff = kOOff + kTileBytes;          // dS: per window 64 keys x 64 queries, 128-byte swizzle
+constexpr int kVecOff = kDSOff + 2 * kTileBytes;    // lse2[128], D[128]
+constexpr int kTabOff = kVecOff + 2 * kTile * 4;
+constexpr int kBarOff = (kTabOff + 15 * kP8 * 4 + 15) / 16 * 16;
+constexpr int kSmemBytes = kBarOff + 128 + 1024;
+static_assert(kDSOff % 1024 == 0, "128-byte swizzled operand must be 1024-byte aligned");
+static_assert(64 * kTile * 4 <= 2 * kSlotBytes, "the table gradient's staging takes the slots");
+constexpr uint32_t kTmemCols = 256;
+// S^T [0,128), dP^T [128,256); compact P^T and dS^T (bf16, the 64 queries of the
+// key's window) over columns already read, and per window dV, dK, dQ over the rest
+constexpr uint32_t kColS = 0, kColDP = 128, kColP = 0, kColDS = 128;
+constexpr uint32_t kColDV = 64, kColDK = 192;
+__device__ __forceinline__ uint32_t col_dq(int w) { return w ? 160u : 32u; }
+
+struct Bars {
+    uint64_t s_full, p_ready, mma2_done, grp, done;
+    uint64_t slot_full[2], o_full, o_free, staged;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Bars) <= 128, "barrier block overflows its slot");
+
+struct Params {
+    Geo g;
+    const uint8_t *q, *k, *v, *o, *dout;
+    uint8_t *dq, *dk, *dv;
+    const __nv_bfloat16* table;
+    const int* buckets;
+    int n_buckets;
+    const float* lse;
+    float* part;  // [streams][heads][225]
+    unsigned int* status;
+    unsigned long long limit_ns;
+    int streams;
+};
+
+// Thread = key row: its 64 scores and dP against the queries of its window, P^T
+// and dS^T back to TMEM, dS to shared memory for dQ = dS K.  dS also adds up in 64
+// fp32 registers a thread over all the items of the CTA (one head): the table
+// gradient costs one addition a pair, and its sum over equal displacements is
+// taken once, at the end.
+template <int kBW>
+__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant__ Params prm) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
+    float* tab = reinterpret_cast<float*>(smem + kTabOff);
+    const Geo& g = prm.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
+    const long long n = g.tiles > stream ? (g.tiles - stream + prm.streams - 1) / prm.streams : 0;
+    auto tile_at = [&](long long j) { return stream + j * prm.streams; };
+
+    if (tid == 0) {
+        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->p_ready, 4);
+        mbar_init(&bars->mma2_done, 1);
+        mbar_init(&bars->grp, 4);
+        mbar_init(&bars->done, 1);
+        mbar_init(&bars->slot_full[0], 32);  // one cp.async arrival per mover lane
+        mbar_init(&bars->slot_full[1], 32);
+        mbar_init(&bars->o_full, 32);
+        mbar_init(&bars->o_free, 4);
+        mbar_init(&bars->staged, 4);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&bars->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    build_bias(tab, kP8, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, kM8, tid,
+               kThreads);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
+    auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
+    };
+    float dacc[64];  // row warps: sum over the items of dS of (this key slot, query slot e)
+#pragma unroll
+    for (int e = 0; e < 64; ++e) dacc[e] = 0.f;
+
+    if (warp == kWarpMover) {
+        // rows of each item one item ahead, and the stores of the staged gradients
+        long long tok[2][4];
+        bool valid[2][4];
+        auto geo = [&](long long j, int b) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                int pi, pj;
+                valid[b][q] = slot_token(g, tile_at(j), lane + 32 * q, h, &pi, &pj, &tok[b][q]);
+            }
+        };
+        auto load = [&](uint8_t* tile, const uint8_t* src, int b) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_rows(tile, src, tok[b][q], valid[b][q], q, lane);
+        };
+        auto load_slot = [&](int b) {
+            uint8_t* sl = smem + b * kSlotBytes;
+            load(sl, prm.q, b);
+            load(sl + kTileBytes, prm.k, b);
+            load(sl + 2 * kTileBytes, prm.v, b);
+            load(sl + 3 * kTileBytes, prm.dout, b);
+            cp_async_mbar_arrive(&bars->slot_full[b]);
+        };
+        auto load_o = [&](int b) {
+            load(smem + kOOff, prm.o, b);
+            cp_async_mbar_arrive(&bars->o_full);
+        };
+        if (n > 0) {
+            geo(0, 0);
+            load_slot(0);
+            load_o(0);
+        }
+        if (n > 1) {
+            geo(1, 1);
+            load_slot(1);
+        }
+        for (long long j = 0; j < n; j += 2) {
+            bool stop = false;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {  // item j + b lives in slot b: constant indices, registers
+                const long long jj = j + b;
+                if (stop || jj >= n) break;
+                const uint32_t ph = static_cast<uint32_t>(b);
+                if (jj + 1 < n) {
+                    if (!wwait(&bars->o_free, ph, 0x7401)) { stop = true; break; }
+                    load_o(b ^ 1);
+                }
+                if (!wwait(&bars->staged, ph, 0x7402)) { stop = true; break; }
+                uint8_t* sl = smem + b * kSlotBytes;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    save_rows(prm.dq, sl, tok[b][q], valid[b][q], q, lane);
+                    save_rows(prm.dk, sl + kTileBytes, tok[b][q], valid[b][q], q, lane);
+                    save_rows(prm.dv, sl + 2 * kTileBytes, tok[b][q], valid[b][q], q, lane);
+                }
+                __syncwarp();  // the staged rows are read: the slot takes item jj + 2's rows
+                if (jj + 2 < n) {
+                    geo(jj + 2, b);
+                    load_slot(b);
+                }
+            }
+            if (stop) break;
+        }
+        cp_async_wait<0>();
+    } else {
+        const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+        const uint32_t id_dv = make_idesc_bf16(kTile, kHeadDim, false, true);  // P^T or dS^T (TMEM) x dO or Q
+        const uint32_t id_dq = make_idesc_bf16(kTile, kHeadDim, true, true);   // dS (smem) x K
+        const uint32_t sbase = smem_u32(smem);
+        const uint64_t dK0 = make_sdesc(sbase, 16, 512, kSw64);
+        const uint64_t dMN0 = make_sdesc(sbase, 8192, 512, kSw64);
+        const uint64_t dDS = make_sdesc(sbase + kDSOff, 8192, 1024, kSw128);  // the windows' blocks are the two halves of M
+        const int r = tid, wi = warp >> 1;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const float sl2 = g.scale_log2;
+        float* lse2v = reinterpret_cast<float*>(smem + kVecOff);
+        float* dvec = lse2v + kTile;
+        const int e_r = r & 63;
+        const float* brow = tab + (kM8 - 1 - slot_i<kBW>(e_r)) * kP8 + kM8 - 1 - slot_j<kBW>(e_r);
+        uint8_t* dsrow = smem + kDSOff + wi * 8192 + (e_r >> 3) * 1024 + (r & 7) * 128;
+        uint32_t gph = 0;
+        long long tok = 0;
+        bool valid = false;
+        auto lse2_of = [&](long long j) {
+            int pi, pj;
+            valid = slot_token(g, tile_at(j), r, h, &pi, &pj, &tok);
+            return valid ? grad_lse2(__ldg(prm.lse + tok)) : INFINITY;  // outside the grid: no probability
+        };
+        float lse2 = n > 0 ? lse2_of(0) : 0.f;
+        for (long long j = 0; j < n; ++j) {
+            const uint32_t ph = static_cast<uint32_t>(j & 1);
+            uint8_t* sl = smem + (j & 1) * kSlotBytes;
+            if (!wwait(&bars->slot_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), 0x7304) ||
+                !wwait(&bars->o_full, ph, 0x7305))
+                break;
+            {
+                float a[32], b[32];
+                load_row_swz(smem + kOOff, r, a, false);
+                load_row_swz(sl + 3 * kTileBytes, r, b, false);
+                float d4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    ffma2(d4[0], d4[1], a[e], a[e + 1], b[e], b[e + 1], d4[0], d4[1]);
+                    ffma2(d4[2], d4[3], a[e + 2], a[e + 3], b[e + 2], b[e + 3], d4[2], d4[3]);
+                }
+                dvec[r] = (d4[0] + d4[1]) + (d4[2] + d4[3]);
+            }
+            lse2v[r] = lse2;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_free);
+            fence_proxy_async_smem();
+            if (lane == 0) mbar_arrive(&bars->grp);
+            if (!wwait(&bars->grp, gph, 0x7306)) break;  // rows landed, D and lse2 in place, the last item's products read
+            gph ^= 1;
+            const uint64_t qo = static_cast<uint64_t>(((j & 1) * kSlotBytes) >> 4);
+            const uint64_t ko = qo + (kTileBytes >> 4), vo = qo + (2 * kTileBytes >> 4), dof = qo + (3 * kTileBytes >> 4);
+            if (r == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) {
+                    umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
+                    umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+                }
+                umma_commit(&bars->s_full);
+            }
+            const uint32_t grp4 = own_groups(g, tile_at(j), r);
+            if (j + 1 < n) lse2 = lse2_of(j + 1);
+            if (!wwait(&bars->s_full, ph, 0x7307)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t sv[32], pv[32];
+                tmem_ld32(trow + kColS + 64 * wi + 32 * c, sv);
+                tmem_ld32(trow + kColDP + 64 * wi + 32 * c, pv);
+                tmem_wait_ld();
+                uint32_t wp[16], wd[16];
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const int a = 32 * c + 4 * e4, e = 4 * e4;
+                    const bool on = (grp4 >> (a >> 4)) & 1u;
+                    const float4 L4 = *reinterpret_cast<const float4*>(lse2v + 64 * wi + a);
+                    const float4 D4 = *reinterpret_cast<const float4*>(dvec + 64 * wi + a);
+                    float t0, t1, t2, t3;
+                    fadd2(t0, t1, brow[slot_off<kBW>(a)], brow[slot_off<kBW>(a + 1)], -L4.x, -L4.y);
+                    fadd2(t2, t3, brow[slot_off<kBW>(a + 2)], brow[slot_off<kBW>(a + 3)], -L4.z, -L4.w);
+                    ffma2(t0, t1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, sl2, t0, t1);
+                    ffma2(t2, t3, __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), sl2, sl2, t2, t3);
+                    float p0 = ex2_approx(t0), p1 = ex2_approx(t1), p2 = ex2_approx(t2), p3 = ex2_approx(t3);
+                    float d0, d1, d2, d3;
+                    fadd2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), -D4.x, -D4.y);
+                    fadd2(d2, d3, __uint_as_float(pv[e + 2]), __uint_as_float(pv[e + 3]), -D4.z, -D4.w);
+                    fmul2(d0, d1, d0, d1, p0, p1);
+                    fmul2(d2, d3, d2, d3, p2, p3);
+                    if (!on) p0 = p1 = p2 = p3 = d0 = d1 = d2 = d3 = 0.f;
+                    fadd2(dacc[a], dacc[a + 1], dacc[a], dacc[a + 1], d0, d1);
+                    fadd2(dacc[a + 2], dacc[a + 3], dacc[a + 2], dacc[a + 3], d2, d3);
+                    wp[2 * e4] = pack_bf16x2(p0, p1);  // P and dS join their products in bf16, the operands' type
+                    wp[2 * e4 + 1] = pack_bf16x2(p2, p3);
+                    wd[2 * e4] = pack_bf16x2(d0, d1);
+                    wd[2 * e4 + 1] = pack_bf16x2(d2, d3);
+                }
+                tmem_st16(trow + kColP + 16 * c, wp);
+                tmem_st16(trow + kColDS + 16 * c, wd);
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+                    *reinterpret_cast<uint4*>(dsrow + (((4 * c + q4) ^ (r & 7)) << 4)) =
+                        make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
+            }
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_ready);
+            if (r == 0 && mbar_wait(&bars->p_ready, ph, ctl, 0x7203)) {
+                tc_fence_after();
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ts(tmem + kColDV + 32 * w, tmem + kColP + 8 * k, dMN0 + dof + 256 * w + 64 * k, id_dv, k > 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ts(tmem + kColDK + 32 * w, tmem + kColDS + 8 * k, dMN0 + qo + 256 * w + 64 * k, id_dv, k > 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ss(tmem + col_dq(w), dDS + 128 * k, dMN0 + ko + 256 * w + 64 * k, id_dq, k > 0);
+                }
+                umma_commit(&bars->mma2_done);
+            }
+            if (!wwait(&bars->mma2_done, ph, 0x7308)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int which = 0; which < 3; ++which) {  // dq, dk, dv staged over q, k, v
+                const uint32_t col = which == 0 ? col_dq(wi) : (which == 1 ? kColDK : kColDV) + 32 * wi;
+                uint32_t v[32];
+                tmem_ld32(trow + col, v);
+                tmem_wait_ld();
+                const float sc = which < 2 ? kScale : 1.f;
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]) * sc;
+                store_row_swz(sl + which * kTileBytes, r, x);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->staged);
+        }
+        if (r == 0) {
+            umma_commit(&bars->done);
+            mbar_wait(&bars->done, 0, ctl, 0x72ff);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();  // every copy into and out of the slots is done
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+    // table gradient of this CTA: stage [query slot][row], then sum the pairs of
+    // each displacement in a fixed order
+    float* st = reinterpret_cast<float*>(smem);
+    if (warp < 4) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) st[e * kTile + tid] = dacc[e];
+    }
+    __syncthreads();
+    for (int d = tid; d < 225; d += kThreads) {
+        const int di = d / 15 - 7, dj = d % 15 - 7;
+        float sum = 0.f;
+        for (int iu = di < 0 ? -di : 0; iu < (di > 0 ? 8 - di : 8); ++iu)
+            for (int ju = dj < 0 ? -dj : 0; ju < (dj > 0 ? 8 - dj : 8); ++ju) {
+                const int it = iu + di, jt = ju + dj;
+                const int u = kBW == 8 ? iu * 8 + ju : ((iu >> 2) * 2 + (ju >> 2)) * 16 + (iu & 3) * 4 + (ju & 3);
+                const int t = kBW == 8 ? it * 8 + jt : ((it >> 2) * 2 + (jt >> 2)) * 16 + (it & 3) * 4 + (jt & 3);
+                sum += st[t * kTile + u] + st[t * kTile + u + 64];
+            }
+        prm.part[static_cast<size_t>(blockIdx.x) * 225 + d] = sum;
+    }
+}
+
+}  // namespace bwd8
+
+// ------------------------------------------------------------------ M = 4
+// Windows of 16 tokens: a 128-row tensor tile would use one score in eight, so
+// each thread computes its row with fp32 multiply-adds from shared memory (a half
+// warp is a window, all of whose threads read the same key row: a broadcast).
+// The two windows of a warp read key rows whose numbers differ in bit 1, so that
+// the 64-byte swizzle puts them into different banks.  No shift fits M = 4.
+namespace m4 {
+
+constexpr int kThreads = 128, kP4 = bias_pitch(4, 4);
+
+struct Params {
+    Geo g;
+    const uint8_t *q, *k, *v, *o, *dout;
+    uint8_t *o_out, *dq, *dk, *dv;
+    const __nv_bfloat16* table;
+    const int* buckets;
+    int n_buckets;
+    const float* lse;
+    float* lse_out;
+    float* part;  // [streams][heads][49]
+    int streams;
+};
+
+// Row of a tile through loads that stay in program order: with all sixteen key
+// rows of a window hoisted to the front the registers would not hold them.
+__device__ __forceinline__ void load_row_ordered(const uint8_t* tile, int row, float (&x)[32]) {
+    const uint32_t base = smem_u32(tile + row * kRowBytes);
+    const uint32_t sw = (row >> 1) & 3;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v = ld_shared_v4(base + ((c ^ sw) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[8 * c + 2 * e] = bf16lo_to_f32(w[e]);
+            x[8 * c + 2 * e + 1] = bf16hi_to_f32(w[e]);
+        }
+    }
+}
+
+__device__ __forceinline__ float dot_row(const uint8_t* tile, int row, const float (&a)[32]) {
+    float b[32], s[4] = {0.f, 0.f, 0.f, 0.f};
+    load_row_ordered(tile, row, b);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        ffma2(s[0], s[1], a[e], a[e + 1], b[e], b[e + 1], s[0], s[1]);
+        ffma2(s[2], s[3], a[e + 2], a[e + 3], b[e + 2], b[e + 3], s[2], s[3]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ void axpy_row(const uint8_t* tile, int row, float f, float (&acc)[32]) {
+    float b[32];
+    load_row_ordered(tile, row, b);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) ffma2(acc[e], acc[e + 1], b[e], b[e + 1], f, f, acc[e], acc[e + 1]);
+}
+
+__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant__ Params prm) {
+    __shared__ __align__(128) uint8_t smem[3 * kTileBytes];
+    __shared__ float tab[7 * kP4];
+    const Geo& g = prm.g;
+    const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+    const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
+    build_bias(tab, kP4, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, 4, r,
+               kThreads);
+    __syncthreads();
+    const int e_r = r & 15, flip = (lane >> 4) << 1, w0 = r & ~15;
+    const float* brow = tab + ((e_r >> 2) + 3) * kP4 + (e_r & 3) + 3;
+    for (long long X = stream; X < g.tiles; X += prm.streams) {
+        int pi, pj;
+        long long tok;
+        const bool valid = slot_token(g, X, r, h, &pi, &pj, &tok);
+        load_rows(smem, prm.q, tok, valid, warp, lane);
+        load_rows(smem + kTileBytes, prm.k, tok, valid, warp, lane);
+        load_rows(smem + 2 * kTileBytes, prm.v, tok, valid, warp, lane);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();  // a warp reads only the rows that it copied
+        float a[32], s[16];
+        load_row_swz(smem, r, a, false);
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int uu = u ^ flip;
+            s[u] = fmaf(dot_row(smem + kTileBytes, w0 + uu, a), g.scale_log2, brow[-((uu >> 2) * kP4 + (uu & 3))]);
+            m = fmaxf(m, s[u]);
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        float l = 0.f, acc[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const float p = ex2_approx(s[u] - mu);
+            l += p;
+            axpy_row(smem + 2 * kTileBytes, w0 + (u ^ flip), p, acc);
+        }
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
+        if (valid && prm.lse_out != nullptr) prm.lse_out[tok] = (m + lg2_approx(l)) * kLn2;
+        store_row_swz(smem, r, acc);  // over this thread's own q row
+        __syncwarp();
+        save_rows(prm.o_out, smem, tok, valid, warp, lane);
+        __syncwarp();
+    }
+}
+
+constexpr int kXPitch = 17;  // exchange of P and dS inside a window: [query][key] with a padded pitch
+constexpr int kBwdSmem = 5 * kTileBytes + 2 * 8 * 16 * kXPitch * 4;
+
+__global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant__ Params prm) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float tab[7 * kP4];
+    float* xp = reinterpret_cast<float*>(smem + 5 * kTileBytes);  // P of the tile's 8 windows
+    float* xd = xp + 8 * 16 * kXPitch;                            // dS
+    const Geo& g = prm.g;
+    const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+    const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
+    build_bias(tab, kP4, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, 4, r,
+               kThreads);
+    __syncthreads();
+    const int e_r = r & 15, flip = (lane >> 4) << 1, w0 = r & ~15;
+    const float* brow = tab + ((e_r >> 2) + 3) * kP4 + (e_r & 3) + 3;
+    uint8_t *tq = smem, *tk = smem + kTileBytes, *tv = smem + 2 * kTileBytes, *tdo = smem + 3 * kTileBytes,
+            *to = smem + 4 * kTileBytes;
+    float* myp = xp + (r >> 4) * 16 * kXPitch;
+    float* myd = xd + (r >> 4) * 16 * kXPitch;
+    float dacc[16];  // sum over the items of dS of (this query slot, key slot u ^ flip)
+#pragma unroll
+    for (int u = 0; u < 16; ++u) dacc[u] = 0.f;
+    for (long long X = stream; X < g.tiles; X += prm.streams) {
+        int pi, pj;
+        long long tok;
+        const bool valid = slot_token(g, X, r, h, &pi, &pj, &tok);
+        load_rows(tq, prm.q, tok, valid, warp, lane);
+        load_rows(tk, prm.k, tok, valid, warp, lane);
+        load_rows(tv, prm.v, tok, valid, warp, lane);
+        load_rows(tdo, prm.dout, tok, valid, warp, lane);
+        load_rows(to, prm.o, tok, valid, warp, lane);
+        cp_async_commit();
+        const float lse2 = valid ? grad_lse2(__ldg(prm.lse + tok)) : INFINITY;
+        cp_async_wait<0>();
+        __syncwarp();
+        float p[16];
+        {
+            float a[32];
+            load_row_swz(tq, r, a, false);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int uu = u ^ flip;
+                p[u] = ex2_approx(fmaf(dot_row(tk, w0 + uu, a), g.scale_log2,
+                                       brow[-((uu >> 2) * kP4 + (uu & 3))] - lse2));
+                myp[e_r * kXPitch + uu] = p[u];
+            }
+        }
+        float acc[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+        {
+            float a[32];
+            load_row_swz(tdo, r, a, false);
+            const float D = dot_row(to, r, a);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int uu = u ^ flip;
+                const float d = p[u] * (dot_row(tv, w0 + uu, a) - D);
+                dacc[u] += d;
+                myd[e_r * kXPitch + uu] = d;
+                axpy_row(tk, w0 + uu, d, acc);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] *= kScale;
+        store_row_swz(to, r, acc);  // dq, over this thread's own o row
+        __syncwarp();               // the windows' P and dS are in place
+        float acv[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = acv[e] = 0.f;
+#pragma unroll 4
+        for (int t = 0; t < 16; ++t) {  // as key row: the queries of its window
+            const int tt = t ^ flip;
+            axpy_row(tq, w0 + tt, myd[tt * kXPitch + e_r], acc);
+            axpy_row(tdo, w0 + tt, myp[tt * kXPitch + e_r], acv);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] *= kScale;
+        __syncwarp();  // every thread of the warp has read the k and v rows
+        store_row_swz(tk, r, acc);
+        store_row_swz(tv, r, acv);
+        __syncwarp();
+        save_rows(prm.dq, to, tok, valid, warp, lane);
+        save_rows(prm.dk, tk, tok, valid, warp, lane);
+        save_rows(prm.dv, tv, tok, valid, warp, lane);
+        __syncwarp();
+    }
+    __syncthreads();
+    float* st = reinterpret_cast<float*>(smem);  // [key slot][row]
+#pragma unroll
+    for (int u = 0; u < 16; ++u) st[(u ^ flip) * kThreads + r] = dacc[u];
+    __syncthreads();
+    if (r < 49) {
+        const int di = r / 7 - 3, dj = r % 7 - 3;
+        float sum = 0.f;
+        for (int iu = di < 0 ? -di : 0; iu < (di > 0 ? 4 - di : 4); ++iu)
+            for (int ju = dj < 0 ? -dj : 0; ju < (dj > 0 ? 4 - dj : 4); ++ju)
+                for (int w = 0; w < 8; ++w) sum += st[(iu * 4 + ju) * kThreads + w * 16 + (iu + di) * 4 + ju + dj];
+        prm.part[static_cast<size_t>(blockIdx.x) * 49 + r] = sum;
+    }
+}
+
+}  // namespace m4
+
+// ------------------------------------------------------------------ launches
+cudaError_t launch_small_fwd(const Geo& g, const RelbPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                             int num_sms, cudaStream_t stream) {
+    if (g.M == 4) {
+        m4::Params prm{};
+        prm.g = g;
+        prm.q = static_cast<const uint8_t*>(p.q);
+        prm.k = static_cast<const uint8_t*>(p.k);
+        prm.v = static_cast<const uint8_t*>(p.v);
+        prm.o_out = static_cast<uint8_t*>(p.o_out);
+        prm.lse_out = p.lse_out;
+        prm.table = static_cast<const __nv_bfloat16*>(p.table);
+        prm.buckets = p.buckets;
+        prm.n_buckets = p.n_buckets;
+        prm.streams = streams_per_head(g.tiles, g.heads, 4 * num_sms);
+        m4::fwd_kernel<<<static_cast<unsigned>(prm.streams) * g.heads, m4::kThreads, 0, stream>>>(prm);
+        return cudaGetLastError();
+    }
+    static SmemOptIn optin8, optin4;
+    const bool b8 = g.bw == 8;
+    auto* kern = b8 ? fwd8::fwd_kernel<8> : fwd8::fwd_kernel<4>;
+    if (cudaError_t e = (b8 ? optin8 : optin4).ensure(reinterpret_cast<const void*>(kern), fwd8::kSmemBytes)) return e;
+    fwd8::Params prm{};
+    prm.g = g;
+    prm.q = static_cast<const uint8_t*>(p.q);
+    prm.k = static_cast<const uint8_t*>(p.k);
+    prm.v = static_cast<const uint8_t*>(p.v);
+    prm.o = static_cast<uint8_t*>(p.o_out);
+    prm.lse = p.lse_out;
+    prm.table = static_cast<const __nv_bfloat16*>(p.table);
+    prm.buckets = p.buckets;
+    prm.n_buckets = p.n_buckets;
+    prm.status = status;
+    prm.limit_ns = limit_ns;
+    prm.streams = streams_per_head(g.tiles, g.heads, 4 * num_sms);
+    kern<<<static_cast<unsigned>(prm.streams) * g.heads, fwd8::kThreads, fwd8::kSmemBytes, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_small_bwd(const Geo& g, const RelbPtrs& p, float* part, int streams, unsigned int* status,
+                             unsigned long long limit_ns, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>(streams) * g.heads;
+    if (g.M == 4) {
+        static SmemOptIn optin;
+        if (cudaError_t e = optin.ensure(reinterpret_cast<const void*>(m4::bwd_kernel), m4::kBwdSmem)) return e;
+        m4::Params prm{};
+        prm.g = g;
+        prm.q = static_cast<const uint8_t*>(p.q);
+        prm.k = static_cast<const uint8_t*>(p.k);
+        prm.v = static_cast<const uint8_t*>(p.v);
+        prm.o = static_cast<const uint8_t*>(p.o);
+        prm.dout = static_cast<const uint8_t*>(p.dout);
+        prm.dq = static_cast<uint8_t*>(p.dq);
+        prm.dk = static_cast<uint8_t*>(p.dk);
+        prm.dv = static_cast<uint8_t*>(p.dv);
+        prm.lse = p.lse;
+        prm.table = static_cast<const __nv_bfloat16*>(p.table);
+        prm.buckets = p.buckets;
+        prm.n_buckets = p.n_buckets;
+        prm.part = part;
+        prm.streams = streams;
+        m4::bwd_kernel<<<grid, m4::kThreads, m4::kBwdSmem, stream>>>(prm);
+        return cudaGetLastError();
+    }
+    static SmemOptIn optin8, optin4;
+    const bool b8 = g.bw == 8;
+    auto* kern = b8 ? bwd8::bwd_kernel<8> : bwd8::bwd_kernel<4>;
+    if (cudaError_t e = (b8 ? optin8 : optin4).ensure(reinterpret_cast<const void*>(kern), bwd8::kSmemBytes)) return e;
+    bwd8::Params prm{};
+    prm.g = g;
+    prm.q = static_cast<const uint8_t*>(p.q);
+    prm.k = static_cast<const uint8_t*>(p.k);
+    prm.v = static_cast<const uint8_t*>(p.v);
+    prm.o = static_cast<const uint8_t*>(p.o);
+    prm.dout = static_cast<const uint8_t*>(p.dout);
+    prm.dq = static_cast<uint8_t*>(p.dq);
+    prm.dk = static_cast<uint8_t*>(p.dk);
+    prm.dv = static_cast<uint8_t*>(p.dv);
+    prm.lse = p.lse;
+    prm.table = static_cast<const __nv_bfloat16*>(p.table);
+    prm.buckets = p.buckets;
+    prm.n_buckets = p.n_buckets;
+    prm.part = part;
+    prm.status = status;
+    prm.limit_ns = limit_ns;
+    prm.streams = streams;
+    kern<<<grid, bwd8::kThreads, bwd8::kSmemBytes, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+}  // namespace relb
+
+}  // namespace fswin

@@ -259,3 +259,140 @@ class WindowAttentionLowRankBias(torch.autograd.Function):
 
 def window_attention_lrbias(q, k, v, theta, u, w, M: int, s: int):
     return WindowAttentionLowRankBias.apply(q, k, v, theta, u, w, M, s)
+
+
+# ------------------------------------------------- learned relative position bias
+# The additive bias of a Swin layer, by buckets: S_tu = q_t . k_u / sqrt(d) +
+# table[h][b(i_t - i_u, j_t - j_u)].  Without a bucket map every displacement has
+# an entry of its own, in the order of Swin's relative_position_index (Swin's
+# [(2M-1)^2, heads] table transposed).  Heads of 32 channels, no rotation.
+def log_distance_buckets(M: int, exact: int = 4, device="cuda"):
+    """(buckets int32 [2M-1, 2M-1], their number): per axis, signed distances below `exact` keep a bucket each and
+    longer ones share one an octave; the two axes' buckets multiply."""
+    if M < 1 or exact < 1:
+        raise ValueError("M and exact must be positive")
+
+    def axis(x):
+        a = abs(x)
+        b = a if a < exact else exact + (a // exact).bit_length() - 1
+        return b if x >= 0 else -b
+
+    one = torch.tensor([axis(x) for x in range(-(M - 1), M)], dtype=torch.int32)
+    one = one - one.min()
+    n = int(one.max()) + 1
+    return (one[:, None] * n + one[None, :]).contiguous().to(device), n * n
+
+
+def _check_on(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class _on:
+    """Makes the tensors' device current for the launches (a no-op when it is)."""
+
+    def __init__(self, device):
+        self.index = device.index if device.index != torch.cuda.current_device() else -1
+
+    def __enter__(self):
+        if self.index >= 0:
+            self.prev = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.index >= 0:
+            torch.cuda.set_device(self.prev)
+
+
+def _check_relbias(q, k, v, table, M: int, buckets) -> None:
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_tensor(name, t, q.shape, torch.bfloat16)
+    if table.dim() != 2:
+        raise ValueError("table must be [heads, buckets]")
+    _check_tensor("table", table, (q.shape[3], table.shape[1]), torch.bfloat16)
+    if buckets is not None:
+        _check_tensor("buckets", buckets, (2 * M - 1, 2 * M - 1), torch.int32)
+    elif table.shape[1] != (2 * M - 1) ** 2:
+        raise ValueError(f"without a bucket map the table has {(2 * M - 1) ** 2} entries a head, got {table.shape[1]}")
+    _check_on(q.device, k=k, v=v, table=table, buckets=buckets)
+
+
+def winattn_relbias_fwd(q, k, v, table, M: int, s: int, buckets=None, o=None, lse=None, need_lse: bool = True):
+    """O, LSE of windowed attention with the bias table[h][bucket of the displacement] (bf16 in/out, fp32 LSE).
+
+    table: bf16 [heads, n]; buckets: int32 [2M-1, 2M-1] (query minus key, row then column, each plus M-1), or None:
+    n = (2M-1)^2.  A bucket outside [0, n) adds no bias.  need_lse=False: inference, LSE is returned as None."""
+    sh = _shape(q, M, s)
+    B, H, W, heads, d = q.shape
+    _check_relbias(q, k, v, table, M, buckets)
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None and need_lse:
+        lse = torch.empty((B, H, W, heads), device=q.device, dtype=torch.float32)
+    _check_tensor("o", o, q.shape, torch.bfloat16)
+    if lse is not None:
+        _check_tensor("lse", lse, (B, H, W, heads), torch.float32)
+    _check_on(q.device, o=o, lse=lse)
+    with _on(q.device):
+        _lib.fs_winattn_relbias_fwd(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                                    buckets.data_ptr() if buckets is not None else 0, table.shape[1], o.data_ptr(),
+                                    lse.data_ptr() if lse is not None else 0, _stream(q.device))
+    return o, lse
+
+
+def alloc_relbias_workspace(q: torch.Tensor, M: int, s: int) -> torch.Tensor:
+    n = _lib.fs_winattn_relbias_bwd_workspace_bytes(_shape(q, M, s))
+    return torch.empty(max(n, 256), device=q.device, dtype=torch.uint8)
+
+
+def winattn_relbias_bwd(q, k, v, o, dout, lse, table, M: int, s: int, buckets=None, workspace=None, dq=None, dk=None,
+                        dv=None, dtable=None):
+    """dQ, dK, dV, dtable (bf16, like the table) of sum(O * dout)."""
+    sh = _shape(q, M, s)
+    B, H, W, heads, d = q.shape
+    _check_relbias(q, k, v, table, M, buckets)
+    for name, t in (("o", o), ("dout", dout)):
+        _check_tensor(name, t, q.shape, torch.bfloat16)
+    _check_tensor("lse", lse, (B, H, W, heads), torch.float32)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(q) if dk is None else dk
+    dv = torch.empty_like(q) if dv is None else dv
+    dtable = torch.empty_like(table) if dtable is None else dtable
+    for name, t, ref in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("dtable", dtable, table)):
+        _check_tensor(name, t, ref.shape, torch.bfloat16)
+    if workspace is None:
+        workspace = alloc_relbias_workspace(q, M, s)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _check_on(q.device, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, dtable=dtable, workspace=workspace)
+    with _on(q.device):
+        _lib.fs_winattn_relbias_bwd(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                                    lse.data_ptr(), table.data_ptr(),
+                                    buckets.data_ptr() if buckets is not None else 0, table.shape[1], dq.data_ptr(),
+                                    dk.data_ptr(), dv.data_ptr(), dtable.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel(), _stream(q.device))
+    return dq, dk, dv, dtable
+
+
+class WindowAttentionRelativeBias(torch.autograd.Function):
+    """Autograd wrapper of the relative-position-bias attention (forward and backward in libfswin.so)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, table, M: int, s: int, buckets=None):
+        o, lse = winattn_relbias_fwd(q, k, v, table, M, s, buckets=buckets)
+        ctx.save_for_backward(q, k, v, o, lse, table, *(() if buckets is None else (buckets,)))
+        ctx.M, ctx.s = M, s
+        return o
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, o, lse, table, *rest = ctx.saved_tensors
+        dq, dk, dv, dtable = winattn_relbias_bwd(q, k, v, o, dout.contiguous(), lse, table, ctx.M, ctx.s,
+                                                 buckets=rest[0] if rest else None)
+        return dq, dk, dv, dtable, None, None, None
+
+
+def window_attention_relbias(q, k, v, table, M: int, s: int, buckets=None):
+    """Autograd windowed attention with a learned relative position bias by buckets."""
+    return WindowAttentionRelativeBias.apply(q, k, v, table, M, s, buckets)
