@@ -217,6 +217,60 @@ FS_API fs_status fs_winattn_relbias_bwd(const fs_winattn_shape* shape, const voi
                                         void* workspace, size_t workspace_bytes, fs_stream_t stream);
 
 /*
+ * The residual step between the blocks of a Swin layer, row by row over the
+ * channels (a row is a token):
+ *   y = post(f);  r = x + gate[b] * (scale o drop(y));  n = pre(r)
+ * post and pre: FS_NORM_NONE, FS_NORM_LAYER ((v - mean) / sqrt(var + eps), times
+ * weight, plus bias) or FS_NORM_RMS (v / sqrt(mean(v^2) + eps), times weight, plus
+ * bias).  A pre-norm layer has pre, a post-norm layer (Swin V2) post.
+ *  - gate: one value a sample (stochastic depth, or a learned gate).  A sample whose
+ *    gate is zero takes nothing from f, whatever f holds, and gives it no gradient;
+ *  - scale: one value a channel (layer scale);
+ *  - drop: element e of the whole tensor is kept, times 1 / (1 - drop_p), when word
+ *    e mod 4 of Philox4x32-10 with counter (e / 4, rng[1]) and key rng[0] is at least
+ *    floor(drop_p 2^32), else replaced by zero.  The mask is never stored: the
+ *    backward draws it again from the same rng.
+ * Types: x, r, dr, dx and every parameter and parameter gradient are of the stream
+ * type (bf16, or fp32 with stream_f32); f, n, dn, df are bf16.  Sums, means and
+ * deviations are fp32; n is the norm of r before r is rounded, and the backward
+ * forms it again from the stored r.
+ * Layout: x, f, r, n and their gradients [samples, tokens, channels], contiguous,
+ * any alignment of their element (16-byte aligned tensors with channels a multiple
+ * of 8 take 16-byte accesses); gate [samples]; parameters [channels]; rng: int64
+ * [2] in DEVICE memory, read when the kernel runs.  r may be x, n may be f, dx may
+ * be dr, df may be dn (the same buffer, not a shifted one).
+ * Shapes: 1 <= channels <= 8192, samples * tokens < 2^31 (both >= 0), eps >= 0 and
+ * finite, 0 <= drop_p < 1; else FS_ERR_SHAPE, as for the weight or bias of a norm
+ * that is FS_NORM_NONE.  gate, scale, weights and biases may be NULL; rng may be
+ * NULL when drop_p == 0; n is required with pre and not written without.
+ *
+ * Backward: gradients of sum(r * dr) + sum(n * dn); dr or dn may be NULL (zero).  f is
+ * required; dgate, dscale and the parameter gradients may each be NULL (not
+ * wanted), and are ignored where their parameter is NULL.  Results do not vary from
+ * run to run.  workspace: at least fs_resnorm_bwd_workspace_bytes(shape) bytes,
+ * 256-byte aligned.
+ */
+typedef enum { FS_NORM_NONE = 0, FS_NORM_LAYER = 1, FS_NORM_RMS = 2 } fs_norm;
+typedef struct {
+    long long samples, tokens;
+    int channels;
+    int stream_f32; /* 0: bf16 stream, 1: fp32 */
+    int pre, post;  /* fs_norm */
+    float eps;
+    double drop_p;
+} fs_resnorm_shape;
+FS_API fs_status fs_resnorm_fwd(const fs_resnorm_shape* shape, const void* x, const void* f, const void* gate,
+                                const void* scale, const void* post_w, const void* post_b, const void* pre_w,
+                                const void* pre_b, const long long* rng, void* r, void* n, fs_stream_t stream);
+FS_API size_t fs_resnorm_bwd_workspace_bytes(const fs_resnorm_shape* shape);
+FS_API fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, const void* dn, const void* r,
+                                const void* f, const void* gate, const void* scale, const void* post_w,
+                                const void* post_b, const void* pre_w, const void* pre_b, const long long* rng,
+                                void* dx, void* df, void* dgate, void* dscale, void* dpost_w, void* dpost_b,
+                                void* dpre_w, void* dpre_b, void* workspace, size_t workspace_bytes,
+                                fs_stream_t stream);
+
+/*
  * Training pair.  fs_winattn_fwd_train is fs_winattn_fwd (lse required) that
  * also leaves, in `workspace` (the backward's: at least
  * fs_winattn_bwd_workspace_bytes(shape) bytes, 256-byte aligned), the rotated

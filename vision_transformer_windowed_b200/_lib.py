@@ -30,6 +30,13 @@ class Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "W", "heads", "d", "M", "s")]
 
 
+class ResnormShape(ctypes.Structure):
+    """fs_resnorm_shape"""
+    _fields_ = [("samples", ctypes.c_longlong), ("tokens", ctypes.c_longlong)] + \
+        [(n, ctypes.c_int) for n in ("channels", "stream_f32", "pre", "post")] + \
+        [("eps", ctypes.c_float), ("drop_p", ctypes.c_double)]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -87,6 +94,13 @@ def load(build_if_missing: bool = True):
         lib.fs_winattn_relbias_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.fs_winattn_relbias_bwd.argtypes = [P] + [vp] * 8 + [ctypes.c_int] + [vp] * 5 + [ctypes.c_size_t, vp]
         lib.fs_winattn_relbias_bwd.restype = st
+        R = ctypes.POINTER(ResnormShape)
+        lib.fs_resnorm_fwd.argtypes = [R] + [vp] * 12
+        lib.fs_resnorm_fwd.restype = st
+        lib.fs_resnorm_bwd_workspace_bytes.argtypes = [R]
+        lib.fs_resnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.fs_resnorm_bwd.argtypes = [R] + [vp] * 20 + [ctypes.c_size_t, vp]
+        lib.fs_resnorm_bwd.restype = st
         _lib = lib
         return lib
 
@@ -186,6 +200,21 @@ def fs_winattn_relbias_bwd(shape: Shape, q: int, k: int, v: int, o: int, dout: i
     _check(load().fs_winattn_relbias_bwd(ctypes.byref(shape), q, k, v, o, dout, lse, table, buckets, int(n_buckets),
                                          dq, dk, dv, dtable, workspace, workspace_bytes, stream),
            "fs_winattn_relbias_bwd")
+
+
+def fs_resnorm_fwd(shape: ResnormShape, *pointers_and_stream: int) -> None:
+    """x, f, gate, scale, post_w, post_b, pre_w, pre_b, rng, r, n, stream (0 for an absent tensor)"""
+    _check(load().fs_resnorm_fwd(ctypes.byref(shape), *pointers_and_stream), "fs_resnorm_fwd")
+
+
+def fs_resnorm_bwd_workspace_bytes(shape: ResnormShape) -> int:
+    return int(load().fs_resnorm_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def fs_resnorm_bwd(shape: ResnormShape, *pointers_and_stream: int) -> None:
+    """dr, dn, r, f, gate, scale, post_w, post_b, pre_w, pre_b, rng, dx, df, dgate, dscale, dpost_w, dpost_b, dpre_w,
+    dpre_b, workspace, workspace_bytes, stream (0 for an absent tensor)"""
+    _check(load().fs_resnorm_bwd(ctypes.byref(shape), *pointers_and_stream), "fs_resnorm_bwd")
 
 
 def fs_device_status() -> int:

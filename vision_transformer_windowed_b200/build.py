@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -11,8 +12,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfswin.so")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "small.cu", "block.cu", "noalloc.cu", "wide.cu", "lrbias.cu", "relbias.cu",
-           "relbias_small.cu"]
-HEADERS = ["dgeo.cuh", "geometry.cuh", "kernels.cuh", "ptx.cuh", "relbias.cuh", "rows.cuh", "schedule.cuh", "tile_io.cuh"]
+           "relbias_small.cu", "resnorm.cu", "resnorm_bwd.cu"]
+HEADERS = ["dgeo.cuh", "geometry.cuh", "kernels.cuh", "ptx.cuh", "relbias.cuh", "resnorm.cuh",
+           "rows.cuh", "schedule.cuh", "tile_io.cuh"]
 
 
 def nvcc_path() -> str:
@@ -41,12 +43,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
              "-I", os.path.join(ROOT, "include")]
     if verbose:
         flags += ["-Xptxas", "-v"]
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
-        subprocess.check_call(cmd)
-        objs.append(obj)
+    objs = [os.path.join(BUILD, src.replace(".cu", ".o")) for src in SOURCES]
+
+    def compile_one(src: str, obj: str) -> None:
+        subprocess.check_call([nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj])
+
+    with ThreadPoolExecutor(max_workers=max(1, min(len(SOURCES), os.cpu_count() or 1))) as pool:
+        for done in [pool.submit(compile_one, src, obj) for src, obj in zip(SOURCES, objs)]:
+            done.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", tmp,
                            "-lcudart"])

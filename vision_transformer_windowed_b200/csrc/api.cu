@@ -101,6 +101,36 @@ bool relbias_aligned(const void* table, const int* buckets, const float* lse) {
            !(reinterpret_cast<uintptr_t>(lse) & 3u);
 }
 
+fs_status resnorm_shape(const fs_resnorm_shape* sh, ResnormShape* out) {
+    if (!sh) return FS_ERR_NULL;
+    if (sh->samples < 0 || sh->tokens < 0 || sh->channels < 1 || sh->channels > 8192) return FS_ERR_SHAPE;
+    if (sh->samples > 0x7FFFFFFFll || sh->tokens > 0x7FFFFFFFll || sh->samples * sh->tokens > 0x7FFFFFFFll)
+        return FS_ERR_SHAPE;
+    if ((sh->stream_f32 != 0 && sh->stream_f32 != 1) || sh->pre < 0 || sh->pre > 2 || sh->post < 0 || sh->post > 2)
+        return FS_ERR_SHAPE;
+    if (!(sh->eps >= 0.f) || std::isinf(sh->eps) || !(sh->drop_p >= 0.0 && sh->drop_p < 1.0)) return FS_ERR_SHAPE;
+    *out = ResnormShape{sh->samples, sh->tokens, sh->channels, sh->stream_f32 == 1, sh->pre, sh->post, sh->eps,
+                        sh->drop_p};
+    return FS_OK;
+}
+
+// Parameters of a residual step: none for a norm that is not there, element-aligned.
+fs_status resnorm_params(const ResnormShape& sh, const ResnormPtrs& p) {
+    if ((!sh.pre && (p.pre_w || p.pre_b)) || (!sh.post && (p.post_w || p.post_b))) return FS_ERR_SHAPE;
+    uintptr_t stream = 0, half = 0;
+    for (const void* q : {p.x, p.gate, p.scale, p.post_w, p.post_b, p.pre_w, p.pre_b, static_cast<const void*>(p.r), p.dr,
+                          static_cast<const void*>(p.dx), static_cast<const void*>(p.dgate),
+                          static_cast<const void*>(p.dscale), static_cast<const void*>(p.dpost_w),
+                          static_cast<const void*>(p.dpost_b), static_cast<const void*>(p.dpre_w),
+                          static_cast<const void*>(p.dpre_b)})
+        stream |= reinterpret_cast<uintptr_t>(q);
+    for (const void* q : {p.f, static_cast<const void*>(p.n), p.dn, static_cast<const void*>(p.df)})
+        half |= reinterpret_cast<uintptr_t>(q);
+    if ((stream & (sh.stream_f32 ? 3u : 1u)) || (half & 1u) || (reinterpret_cast<uintptr_t>(p.rng) & 7u))
+        return FS_ERR_ALIGN;
+    return FS_OK;
+}
+
 __global__ void bounded_wait_selftest_kernel(unsigned int* status, unsigned long long limit_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -517,6 +547,81 @@ fs_status fs_winattn_relbias_bwd(const fs_winattn_shape* shape, const void* q, c
     p.ws = static_cast<uint8_t*>(workspace);
     const cudaError_t e = launch_relbias_bwd(g, p, maps, status, lim, cs, g_phase_n >= 5 ? g_phase_events : nullptr);
     return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+fs_status fs_resnorm_fwd(const fs_resnorm_shape* shape, const void* x, const void* f, const void* gate,
+                         const void* scale, const void* post_w, const void* post_b, const void* pre_w,
+                         const void* pre_b, const long long* rng, void* r, void* n, fs_stream_t stream) {
+    ResnormShape sh;
+    fs_status st = resnorm_shape(shape, &sh);
+    if (st != FS_OK) return st;
+    ResnormPtrs p{};
+    p.x = x;
+    p.f = f;
+    p.gate = gate;
+    p.scale = scale;
+    p.post_w = post_w;
+    p.post_b = post_b;
+    p.pre_w = pre_w;
+    p.pre_b = pre_b;
+    p.rng = rng;
+    p.r = r;
+    p.n = sh.pre ? n : nullptr;
+    if ((st = resnorm_params(sh, p)) != FS_OK) return st;
+    if (sh.samples * sh.tokens == 0) return FS_OK;
+    if (!x || !f || !r || (sh.pre && !n) || (sh.drop_p > 0.0 && !rng)) return FS_ERR_NULL;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    return launch_resnorm_fwd(sh, p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+size_t fs_resnorm_bwd_workspace_bytes(const fs_resnorm_shape* shape) {
+    ResnormShape sh;
+    if (resnorm_shape(shape, &sh) != FS_OK) return 0;
+    return resnorm_bwd_workspace_bytes(sh);
+}
+
+fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, const void* dn, const void* r, const void* f,
+                         const void* gate, const void* scale, const void* post_w, const void* post_b,
+                         const void* pre_w, const void* pre_b, const long long* rng, void* dx, void* df, void* dgate,
+                         void* dscale, void* dpost_w, void* dpost_b, void* dpre_w, void* dpre_b, void* workspace,
+                         size_t workspace_bytes, fs_stream_t stream) {
+    ResnormShape sh;
+    fs_status st = resnorm_shape(shape, &sh);
+    if (st != FS_OK) return st;
+    ResnormPtrs p{};
+    p.dr = dr;
+    p.dn = sh.pre ? dn : nullptr;
+    p.r = const_cast<void*>(r);
+    p.f = f;
+    p.gate = gate;
+    p.scale = scale;
+    p.post_w = post_w;
+    p.post_b = post_b;
+    p.pre_w = pre_w;
+    p.pre_b = pre_b;
+    p.rng = rng;
+    p.dx = dx;
+    p.df = df;
+    p.dgate = gate ? dgate : nullptr;
+    p.dscale = scale ? dscale : nullptr;
+    p.dpost_w = post_w ? dpost_w : nullptr;
+    p.dpost_b = post_b ? dpost_b : nullptr;
+    p.dpre_w = pre_w ? dpre_w : nullptr;
+    p.dpre_b = pre_b ? dpre_b : nullptr;
+    p.ws = static_cast<uint8_t*>(workspace);
+    if ((st = resnorm_params(sh, p)) != FS_OK) return st;
+    if (sh.samples * sh.tokens > 0 &&
+        (!f || !dx || !df || (sh.pre && dn && !r) || (sh.drop_p > 0.0 && !rng)))
+        return FS_ERR_NULL;
+    if (resnorm_bwd_workspace_bytes(sh) > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                                                workspace_bytes < resnorm_bwd_workspace_bytes(sh)))
+        return FS_ERR_WORKSPACE;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    return launch_resnorm_bwd(sh, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
 }
 
 fs_status fs_device_status(unsigned int* code) {

@@ -149,6 +149,38 @@ cudaError_t launch_relbias_fwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
 cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& maps, unsigned int* status,
                                unsigned long long limit_ns, cudaStream_t stream, cudaEvent_t const* events);
 
+// The residual step of a layer with its norms: r = x + g_b gamma o drop(post(f)),
+// n = pre(r), and its backward.
+struct ResnormPtrs {
+    const void *x, *f;                                       // forward: stream type, bf16
+    const void *gate, *scale, *post_w, *post_b, *pre_w, *pre_b;  // stream type, each may be null
+    const long long* rng;                                    // (seed, offset), read when elements are dropped
+    void *r, *n;                                             // r: the backward reads it
+    const void *dr, *dn;                                     // either may be null
+    void *dx, *df, *dgate, *dscale, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+    uint8_t* ws;
+    long long samples;
+};
+struct ResnormShape {
+    long long samples, tokens;
+    int channels;
+    bool stream_f32;
+    int pre, post;  // 0 none, 1 layer norm, 2 rms norm
+    float eps;
+    double drop_p;
+    // Sixteen-byte accesses: the channel count divides by 8 and every tensor is aligned.
+    bool wide(const ResnormPtrs& p) const {
+        const void* all[] = {p.x,  p.f,  p.scale, p.post_w, p.post_b, p.pre_w, p.pre_b,
+                             p.r,  p.n,  p.dr,    p.dn,     p.dx,     p.df};
+        uintptr_t bits = 0;
+        for (const void* q : all) bits |= reinterpret_cast<uintptr_t>(q);
+        return channels % 8 == 0 && (bits & 15u) == 0;
+    }
+};
+size_t resnorm_bwd_workspace_bytes(const ResnormShape& sh);
+cudaError_t launch_resnorm_fwd(const ResnormShape& sh, const ResnormPtrs& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_resnorm_bwd(const ResnormShape& sh, const ResnormPtrs& p, cudaStream_t stream);
+
 // Fixed-order d theta sum: part [heads][per_head][16] -> dtheta [heads][16] (one
 // launch; cnt: heads counters that are zero when it starts).
 namespace bwdk {

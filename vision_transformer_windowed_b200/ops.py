@@ -15,6 +15,8 @@ padding), and only the H x W real tokens are read and written.
 """
 from __future__ import annotations
 
+from collections import namedtuple
+
 import torch
 
 from . import _lib
@@ -396,3 +398,136 @@ class WindowAttentionRelativeBias(torch.autograd.Function):
 def window_attention_relbias(q, k, v, table, M: int, s: int, buckets=None):
     """Autograd windowed attention with a learned relative position bias by buckets."""
     return WindowAttentionRelativeBias.apply(q, k, v, table, M, s, buckets)
+
+
+# --------------------------------------------------------- residual step and norms
+# What stands between the blocks of a Swin layer: the branch's post norm, dropout,
+# layer scale and gate, the residual sum, and the next block's pre norm, in one pass
+# over the rows.
+_NORMS = {None: 0, "layer": 1, "rms": 2}
+_STEP_PARAMS = ("gate", "scale", "post_weight", "post_bias", "pre_weight", "pre_bias")
+ResidualNormGrads = namedtuple("ResidualNormGrads", ("dx", "df") + tuple("d" + n for n in _STEP_PARAMS))
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _resnorm_shape(stream, f, params, pre, post, eps: float, p: float, rng):
+    """Checks a residual step's arguments; `stream`: x, or r in the backward."""
+    if pre not in _NORMS or post not in _NORMS:
+        raise ValueError("pre and post must be None, 'layer' or 'rms'")
+    if stream.dim() < 2:
+        raise ValueError("expected a [samples, ..., channels] tensor")
+    if stream.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"the residual stream must be bfloat16 or float32, got {stream.dtype}")
+    B, C = stream.shape[0], stream.shape[-1]
+    _check_tensor("x", stream, stream.shape, stream.dtype)
+    _check_tensor("f", f, stream.shape, torch.bfloat16)
+    for name, t in params.items():
+        if t is not None:
+            _check_tensor(name, t, (B,) if name == "gate" else (C,), stream.dtype)
+    for kind, which in ((pre, "pre"), (post, "post")):
+        if kind is None and (params[which + "_weight"] is not None or params[which + "_bias"] is not None):
+            raise ValueError(f"{which}_weight and {which}_bias need {which}='layer' or 'rms'")
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must lie in [0, 1)")
+    if p > 0.0:
+        if rng is None:
+            raise ValueError("dropout needs rng, an int64 tensor (seed, offset)")
+        _check_tensor("rng", rng, (2,), torch.int64)
+    _check_on(stream.device, f=f, rng=rng, **params)
+    tokens = stream.numel() // (B * C) if B and C else 0
+    return _lib.ResnormShape(B, tokens, C, int(stream.dtype == torch.float32), _NORMS[pre], _NORMS[post], eps, p)
+
+
+def residual_norm_fwd(x, f, gate=None, scale=None, post=None, post_weight=None, post_bias=None, pre="layer",
+                      pre_weight=None, pre_bias=None, eps: float = 1e-5, p: float = 0.0, rng=None, r=None, n=None):
+    """r = x + gate[b] * scale * dropout(post(f)), n = pre(r) (None without pre).
+
+    x: the residual stream [B, ..., C], bf16 or fp32; f: a block's output, bf16.  gate: one value a sample (stochastic
+    depth or learned; a zero gate takes nothing from f); scale: one a channel (layer scale); post, pre: None, "layer"
+    or "rms", with weight and bias or without.  Parameters are of x's type, n is bf16.  p: dropout probability, drawn
+    from rng, an int64 CUDA tensor (seed, offset) that the kernel reads when it runs; advance the offset between
+    steps.  r may be x and n may be f, to work in place."""
+    params = dict(gate=gate, scale=scale, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
+                  pre_bias=pre_bias)
+    sh = _resnorm_shape(x, f, params, pre, post, eps, p, rng)
+    r = torch.empty_like(x) if r is None else r
+    n = torch.empty_like(f) if n is None and pre is not None else n
+    _check_tensor("r", r, x.shape, x.dtype)
+    if pre is not None:
+        _check_tensor("n", n, x.shape, torch.bfloat16)
+    _check_on(x.device, r=r, n=n)
+    with _on(x.device):
+        _lib.fs_resnorm_fwd(sh, x.data_ptr(), f.data_ptr(), _ptr(gate), _ptr(scale), _ptr(post_weight), _ptr(post_bias),
+                            _ptr(pre_weight), _ptr(pre_bias), _ptr(rng) if p > 0.0 else 0, r.data_ptr(), _ptr(n),
+                            _stream(x.device))
+    return r, n if pre is not None else None
+
+
+def residual_norm_bwd(dr, dn, r, f, gate=None, scale=None, post=None, post_weight=None, post_bias=None, pre="layer",
+                      pre_weight=None, pre_bias=None, eps: float = 1e-5, p: float = 0.0, rng=None, workspace=None,
+                      skip=()):
+    """Gradients of sum(r * dr) + sum(n * dn) as ResidualNormGrads; None for an absent parameter and for the names in
+    `skip` ("gate", "scale", ...).  dr or dn may be None (zero); r is the forward's, rng as the forward read it."""
+    params = dict(gate=gate, scale=scale, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
+                  pre_bias=pre_bias)
+    sh = _resnorm_shape(r, f, params, pre, post, eps, p, rng)
+    if dr is not None:
+        _check_tensor("dr", dr, r.shape, r.dtype)
+    if dn is not None:
+        if pre is None:
+            raise ValueError("dn without a pre norm")
+        _check_tensor("dn", dn, r.shape, torch.bfloat16)
+    need = _lib.fs_resnorm_bwd_workspace_bytes(sh)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), device=r.device, dtype=torch.uint8)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _check_on(r.device, dr=dr, dn=dn, workspace=workspace)
+    out = {name: None if t is None or name in skip else torch.empty_like(t) for name, t in params.items()}
+    dx, df = torch.empty_like(r), torch.empty_like(f)
+    with _on(r.device):
+        _lib.fs_resnorm_bwd(sh, _ptr(dr), _ptr(dn), r.data_ptr(), f.data_ptr(), _ptr(gate), _ptr(scale),
+                            _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias),
+                            _ptr(rng) if p > 0.0 else 0, dx.data_ptr(), df.data_ptr(),
+                            *(_ptr(out[name]) for name in _STEP_PARAMS), workspace.data_ptr(), workspace.numel(),
+                            _stream(r.device))
+    return ResidualNormGrads(dx, df, *(out[name] for name in _STEP_PARAMS))
+
+
+class ResidualNorm(torch.autograd.Function):
+    """Autograd wrapper of the residual step (forward and backward in libfswin.so)."""
+
+    @staticmethod
+    def forward(ctx, x, f, gate, scale, post_weight, post_bias, pre_weight, pre_bias, rng, pre, post, eps, p):
+        params = (gate, scale, post_weight, post_bias, pre_weight, pre_bias)
+        if p > 0.0:
+            rng = rng.clone()  # the caller may advance its own before the backward
+        kw = dict(zip(_STEP_PARAMS, params), pre=pre, post=post, eps=eps, p=p, rng=rng)
+        r, n = residual_norm_fwd(x, f, **kw)
+        ctx.set_materialize_grads(False)
+        tensors = params + (rng if p > 0.0 else None,)
+        ctx.present = [t is not None for t in tensors]
+        ctx.save_for_backward(r, f, *(t for t in tensors if t is not None))
+        ctx.options = dict(pre=pre, post=post, eps=eps, p=p)
+        return r, n
+
+    @staticmethod
+    def backward(ctx, dr, dn):
+        if dr is None and dn is None:
+            return (None,) * 13
+        r, f, *rest = ctx.saved_tensors
+        tensors = [rest.pop(0) if there else None for there in ctx.present]
+        needs = dict(zip(_STEP_PARAMS, ctx.needs_input_grad[2:8]))
+        g = residual_norm_bwd(None if dr is None else dr.contiguous(), None if dn is None else dn.contiguous(), r, f,
+                              **dict(zip(_STEP_PARAMS, tensors)), rng=tensors[-1], **ctx.options,
+                              skip=[name for name, wanted in needs.items() if not wanted])
+        return (*g, None, None, None, None, None)
+
+
+def residual_norm(x, f, gate=None, scale=None, post=None, post_weight=None, post_bias=None, pre="layer",
+                  pre_weight=None, pre_bias=None, eps: float = 1e-5, p: float = 0.0, rng=None):
+    """Autograd residual step; arguments and results as residual_norm_fwd."""
+    return ResidualNorm.apply(x, f, gate, scale, post_weight, post_bias, pre_weight, pre_bias, rng, pre, post, eps, p)
