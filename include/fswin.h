@@ -271,6 +271,39 @@ FS_API fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, c
                                 fs_stream_t stream);
 
 /*
+ * Gated feed-forward block of a layer:
+ *   h = act(x W_gate^T + b_gate) o (x W_up^T + b_up);  y = h W_down^T + b_down
+ * act: FS_ACT_SILU (g sigmoid(g)) or FS_ACT_GELU (g Phi(g), the exact one).  All bf16:
+ * x, y [tokens, channels]; w_gate, w_up [hidden, channels]; w_down [channels, hidden];
+ * b_gate, b_up [hidden] and b_down [channels], each of which may be NULL.  Products and
+ * the activation are fp32; h is rounded to bf16 between the two products.
+ * Shapes: 0 <= tokens < 2^31 - 256, channels 8 .. 16384 and hidden 8 .. 65536, both
+ * multiples of 8 (else FS_ERR_SHAPE); every pointer 16-byte aligned (FS_ERR_ALIGN).
+ *
+ * Backward: gradients of sum(y * dy), from x and the weights (h is formed again).  dx and
+ * the weight gradients are bf16 like what they belong to; a NULL bias gradient is not
+ * computed.  Weight and bias gradients are summed over the tokens in fp32 in a fixed
+ * order: results do not vary from run to run.
+ * workspace: at least fs_gated_mlp_{fwd,bwd}_workspace_bytes(shape) bytes, 256-byte
+ * aligned (2 bytes forward and 6 backward a token and hidden channel, and backward 192
+ * bytes a weight of one matrix).
+ */
+typedef enum { FS_ACT_SILU = 0, FS_ACT_GELU = 1 } fs_act;
+typedef struct {
+    long long tokens;
+    int channels, hidden, act; /* act: fs_act */
+} fs_mlp_shape;
+FS_API size_t fs_gated_mlp_fwd_workspace_bytes(const fs_mlp_shape* shape);
+FS_API fs_status fs_gated_mlp_fwd(const fs_mlp_shape* shape, const void* x, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* b_gate, const void* b_up, const void* b_down, void* y,
+                                  void* workspace, size_t workspace_bytes, fs_stream_t stream);
+FS_API size_t fs_gated_mlp_bwd_workspace_bytes(const fs_mlp_shape* shape);
+FS_API fs_status fs_gated_mlp_bwd(const fs_mlp_shape* shape, const void* dy, const void* x, const void* w_gate,
+                                  const void* w_up, const void* w_down, const void* b_gate, const void* b_up, void* dx,
+                                  void* dw_gate, void* dw_up, void* dw_down, void* db_gate, void* db_up, void* db_down,
+                                  void* workspace, size_t workspace_bytes, fs_stream_t stream);
+
+/*
  * Training pair.  fs_winattn_fwd_train is fs_winattn_fwd (lse required) that
  * also leaves, in `workspace` (the backward's: at least
  * fs_winattn_bwd_workspace_bytes(shape) bytes, 256-byte aligned), the rotated

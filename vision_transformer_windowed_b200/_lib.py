@@ -37,6 +37,11 @@ class ResnormShape(ctypes.Structure):
         [("eps", ctypes.c_float), ("drop_p", ctypes.c_double)]
 
 
+class MlpShape(ctypes.Structure):
+    """fs_mlp_shape"""
+    _fields_ = [("tokens", ctypes.c_longlong)] + [(n, ctypes.c_int) for n in ("channels", "hidden", "act")]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -101,6 +106,14 @@ def load(build_if_missing: bool = True):
         lib.fs_resnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.fs_resnorm_bwd.argtypes = [R] + [vp] * 20 + [ctypes.c_size_t, vp]
         lib.fs_resnorm_bwd.restype = st
+        L = ctypes.POINTER(MlpShape)
+        for name in ("fs_gated_mlp_fwd_workspace_bytes", "fs_gated_mlp_bwd_workspace_bytes"):
+            getattr(lib, name).argtypes = [L]
+            getattr(lib, name).restype = ctypes.c_size_t
+        lib.fs_gated_mlp_fwd.argtypes = [L] + [vp] * 9 + [ctypes.c_size_t, vp]
+        lib.fs_gated_mlp_fwd.restype = st
+        lib.fs_gated_mlp_bwd.argtypes = [L] + [vp] * 15 + [ctypes.c_size_t, vp]
+        lib.fs_gated_mlp_bwd.restype = st
         _lib = lib
         return lib
 
@@ -215,6 +228,25 @@ def fs_resnorm_bwd(shape: ResnormShape, *pointers_and_stream: int) -> None:
     """dr, dn, r, f, gate, scale, post_w, post_b, pre_w, pre_b, rng, dx, df, dgate, dscale, dpost_w, dpost_b, dpre_w,
     dpre_b, workspace, workspace_bytes, stream (0 for an absent tensor)"""
     _check(load().fs_resnorm_bwd(ctypes.byref(shape), *pointers_and_stream), "fs_resnorm_bwd")
+
+
+def fs_gated_mlp_fwd_workspace_bytes(shape: MlpShape) -> int:
+    return int(load().fs_gated_mlp_fwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def fs_gated_mlp_fwd(shape: MlpShape, *pointers_and_stream: int) -> None:
+    """x, w_gate, w_up, w_down, b_gate, b_up, b_down, y, workspace, workspace_bytes, stream (0 for an absent bias)"""
+    _check(load().fs_gated_mlp_fwd(ctypes.byref(shape), *pointers_and_stream), "fs_gated_mlp_fwd")
+
+
+def fs_gated_mlp_bwd_workspace_bytes(shape: MlpShape) -> int:
+    return int(load().fs_gated_mlp_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def fs_gated_mlp_bwd(shape: MlpShape, *pointers_and_stream: int) -> None:
+    """dy, x, w_gate, w_up, w_down, b_gate, b_up, dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down, workspace,
+    workspace_bytes, stream (0 for an absent bias)"""
+    _check(load().fs_gated_mlp_bwd(ctypes.byref(shape), *pointers_and_stream), "fs_gated_mlp_bwd")
 
 
 def fs_device_status() -> int:

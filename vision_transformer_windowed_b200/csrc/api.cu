@@ -131,6 +131,15 @@ fs_status resnorm_params(const ResnormShape& sh, const ResnormPtrs& p) {
     return FS_OK;
 }
 
+fs_status mlp_shape(const fs_mlp_shape* sh, MlpShape* out) {
+    if (!sh) return FS_ERR_NULL;
+    if (sh->tokens < 0 || sh->tokens > 0x7FFFFF00ll || sh->channels < 8 || sh->channels > 16384 || sh->channels % 8 ||
+        sh->hidden < 8 || sh->hidden > 65536 || sh->hidden % 8 || sh->act < 0 || sh->act > 1)
+        return FS_ERR_SHAPE;
+    *out = MlpShape{sh->tokens, sh->channels, sh->hidden, sh->act};
+    return FS_OK;
+}
+
 __global__ void bounded_wait_selftest_kernel(unsigned int* status, unsigned long long limit_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -153,6 +162,19 @@ __global__ void zero_f32_kernel(float* p, int n) {
 }
 
 }  // namespace
+
+int fswin::encode_matrix(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows, int box_cols,
+                         bool swizzle128) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : 1;
+}
 
 int fswin::device_ready() {
     unsigned int* status = nullptr;
@@ -622,6 +644,103 @@ fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, const vo
     int sms = 0;
     if ((st = device_state(&status, &sms)) != FS_OK) return st;
     return launch_resnorm_bwd(sh, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+size_t fs_gated_mlp_fwd_workspace_bytes(const fs_mlp_shape* shape) {
+    MlpShape sh;
+    return mlp_shape(shape, &sh) == FS_OK ? mlp_fwd_workspace_bytes(sh) : 0;
+}
+
+fs_status fs_gated_mlp_fwd(const fs_mlp_shape* shape, const void* x, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* b_gate, const void* b_up, const void* b_down, void* y,
+                           void* workspace, size_t workspace_bytes, fs_stream_t stream) {
+    MlpShape sh;
+    fs_status st = mlp_shape(shape, &sh);
+    if (st != FS_OK) return st;
+    if (sh.tokens == 0) return FS_OK;
+    if (!x || !w_gate || !w_up || !w_down || !y) return FS_ERR_NULL;  // biases may be NULL
+    for (const void* q : {x, w_gate, w_up, w_down, b_gate, b_up, b_down, static_cast<const void*>(y)})
+        if (!aligned16(q)) return FS_ERR_ALIGN;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < mlp_fwd_workspace_bytes(sh))
+        return FS_ERR_WORKSPACE;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    unsigned long long lim;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        lim = g_limit_ns;
+    }
+    MlpPtrs p{};
+    p.x = x;
+    p.w_gate = w_gate;
+    p.w_up = w_up;
+    p.w_down = w_down;
+    p.b_gate = b_gate;
+    p.b_up = b_up;
+    p.b_down = b_down;
+    p.y = y;
+    p.ws = static_cast<uint8_t*>(workspace);
+    return launch_mlp_fwd(sh, p, status, lim, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FS_OK
+                                                                                                        : FS_ERR_CUDA;
+}
+
+size_t fs_gated_mlp_bwd_workspace_bytes(const fs_mlp_shape* shape) {
+    MlpShape sh;
+    return mlp_shape(shape, &sh) == FS_OK ? mlp_bwd_workspace_bytes(sh) : 0;
+}
+
+fs_status fs_gated_mlp_bwd(const fs_mlp_shape* shape, const void* dy, const void* x, const void* w_gate,
+                           const void* w_up, const void* w_down, const void* b_gate, const void* b_up, void* dx,
+                           void* dw_gate, void* dw_up, void* dw_down, void* db_gate, void* db_up, void* db_down,
+                           void* workspace, size_t workspace_bytes, fs_stream_t stream) {
+    MlpShape sh;
+    fs_status st = mlp_shape(shape, &sh);
+    if (st != FS_OK) return st;
+    if (!dw_gate || !dw_up || !dw_down) return FS_ERR_NULL;  // bias gradients may be NULL
+    for (const void* q : {dy, x, w_gate, w_up, w_down, b_gate, b_up, static_cast<const void*>(dx),
+                          static_cast<const void*>(dw_gate), static_cast<const void*>(dw_up),
+                          static_cast<const void*>(dw_down), static_cast<const void*>(db_gate),
+                          static_cast<const void*>(db_up), static_cast<const void*>(db_down)})
+        if (!aligned16(q)) return FS_ERR_ALIGN;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (sh.tokens == 0) {  // no token: the parameter gradients are empty sums
+        if ((st = device_state(&status, &sms)) != FS_OK) return st;
+        const size_t cf = 2ull * sh.channels * sh.hidden;
+        const struct { void* p; size_t n; } all[] = {{dw_gate, cf}, {dw_up, cf}, {dw_down, cf}, {db_gate, 2ull * sh.hidden},
+                                                     {db_up, 2ull * sh.hidden}, {db_down, 2ull * sh.channels}};
+        for (const auto& a : all)
+            if (a.p && cudaMemsetAsync(a.p, 0, a.n, cs) != cudaSuccess) return FS_ERR_CUDA;
+        return FS_OK;
+    }
+    if (!dy || !x || !w_gate || !w_up || !w_down || !dx) return FS_ERR_NULL;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < mlp_bwd_workspace_bytes(sh))
+        return FS_ERR_WORKSPACE;
+    if ((st = device_state(&status, &sms)) != FS_OK) return st;
+    unsigned long long lim;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        lim = g_limit_ns;
+    }
+    MlpPtrs p{};
+    p.dy = dy;
+    p.x = x;
+    p.w_gate = w_gate;
+    p.w_up = w_up;
+    p.w_down = w_down;
+    p.b_gate = b_gate;
+    p.b_up = b_up;
+    p.dx = dx;
+    p.dw_gate = dw_gate;
+    p.dw_up = dw_up;
+    p.dw_down = dw_down;
+    p.db_gate = db_gate;
+    p.db_up = db_up;
+    p.db_down = db_down;
+    p.ws = static_cast<uint8_t*>(workspace);
+    return launch_mlp_bwd(sh, p, status, lim, sms, cs) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
 }
 
 fs_status fs_device_status(unsigned int* code) {

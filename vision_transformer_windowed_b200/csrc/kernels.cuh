@@ -181,6 +181,31 @@ size_t resnorm_bwd_workspace_bytes(const ResnormShape& sh);
 cudaError_t launch_resnorm_fwd(const ResnormShape& sh, const ResnormPtrs& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_resnorm_bwd(const ResnormShape& sh, const ResnormPtrs& p, cudaStream_t stream);
 
+// The gated feed-forward block y = (act(x Wg^T + bg) o (x Wu^T + bu)) Wd^T + bd and
+// its backward, all bf16: x, y, dy, dx [tokens, channels], w_gate, w_up [hidden,
+// channels], w_down [channels, hidden].
+struct MlpShape {
+    long long tokens;
+    int channels, hidden, act;  // act: 0 silu, 1 gelu
+};
+struct MlpPtrs {
+    const void *x, *dy, *w_gate, *w_up, *w_down, *b_gate, *b_up, *b_down;
+    void *y, *dx, *dw_gate, *dw_up, *dw_down, *db_gate, *db_up, *db_down;
+    uint8_t* ws;
+};
+size_t mlp_fwd_workspace_bytes(const MlpShape& sh);
+size_t mlp_bwd_workspace_bytes(const MlpShape& sh);
+cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                           int num_sms, cudaStream_t stream);
+cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                           int num_sms, cudaStream_t stream);
+
+// TMA map of a row-major bf16 matrix: box of box_rows x box_cols (box_cols 64 with
+// the 128-byte swizzle, 32 with the 64-byte one).  0 on success.  Needs the
+// library's per-device state (device_ready).
+int encode_matrix(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows, int box_cols,
+                  bool swizzle128);
+
 // Fixed-order d theta sum: part [heads][per_head][16] -> dtheta [heads][16] (one
 // launch; cnt: heads counters that are zero when it starts).
 namespace bwdk {

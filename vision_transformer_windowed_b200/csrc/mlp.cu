@@ -1,0 +1,645 @@
+// Gated feed-forward block: y = h W_down^T + b_down, h = act(x W_gate^T + b_gate) o (x W_up^T + b_up),
+// and its backward, as persistent tensor-core kernels over one pipeline.
+//
+// Pipeline (one CTA an SM, 12 warps): warp 0 copies operand blocks of 64
+// contraction channels into a ring with TMA (128-byte swizzle), warp 1 issues
+// tcgen05 products into one of two 256-column TMEM accumulators, warps 4-11 turn
+// the other accumulator into the result.  Operands are taken as they lie in memory:
+// contraction-major, or (weights and activations of the gradient products)
+// row-major with the contraction over rows, which the matrix descriptors express.
+// A contraction that does not fill its last block ends at its last 16 channels.
+//
+//   kGate:   h = act(x Wg^T + bg) o (x Wu^T + bu): the two weight tiles lie one after
+//            the other in a stage, so one product of up to 256 columns makes both
+//   kLinear: y = h Wd^T + bd
+//   kGrad:   g, u again, dh = dy Wd; h, dg = dh o u o act'(g), du = dh o act(g)
+//   kDx:     dx = dg Wg + du Wu, one contraction over both
+//   kDw:     dWg = dg^T x, dWu = du^T x, dWd = dy^T h, the tokens split over CTAs with
+//            fp32 partial results that a second kernel adds in order; a 16-column
+//            product with a tile of ones gives the bias gradients
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace fswin {
+
+namespace mlp {
+
+enum : int { kGate, kLinear, kGrad, kDx, kDw };
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kBlockK = 64;
+constexpr int kBlockM = 128;
+constexpr int kABytes = kBlockM * kBlockK * 2;
+constexpr int kStages = 4;                        // at most
+constexpr int kDwMaxN = 192;
+// A stage: A, and B of up to 256 rows; kGrad: x, three times 64 weight rows, dy; kDw:
+// A and up to 192 columns.
+__host__ __device__ constexpr int stage_bytes(int op) {
+    return op == kGrad ? 2 * kABytes + 3 * 8192 : (op == kDw ? kABytes + kDwMaxN * 128 : 3 * kABytes);
+}
+__host__ __device__ constexpr int stages_of(int op) { return op == kGrad ? 3 : kStages; }
+constexpr int kStoreBytes = 32 * 64;              // a warp's 32 rows x 32 bf16 columns
+constexpr int kRingBytes = 12 * kABytes;
+constexpr int kOnesOff = kStages * (kABytes + kDwMaxN * 128);  // kDw: 16 rows x 64 of 1.0 behind its ring
+constexpr int kOnesBytes = 2048;
+constexpr int kStoreOff = kRingBytes;
+constexpr int kBarOff = kStoreOff + kEpiWarps * 2 * kStoreBytes;
+constexpr uint32_t kColOnes = 240;                 // bias gradient columns of kDw
+
+struct Bars {
+    uint64_t full[kStages], free_[kStages], acc_full[2], acc_free[2], done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr int kSmemBytes = kBarOff + 256 + 1024;
+static_assert(stages_of(kGate) * stage_bytes(kGate) <= kRingBytes && stages_of(kGrad) * stage_bytes(kGrad) <= kRingBytes &&
+                  kOnesOff + kOnesBytes <= kRingBytes,
+              "the ring overflows its place");
+static_assert(stage_bytes(kGrad) % 1024 == 0 && stage_bytes(kDw) % 1024 == 0 && kOnesOff % 1024 == 0, "tile alignment");
+static_assert(sizeof(Bars) <= 256, "barrier block overflows its slot");
+static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may have");
+
+struct Maps {
+    CUtensorMap a[3], b[3], out[3];
+};
+
+struct Problem {       // kDw: one of the three weight gradients
+    int m, n, tiles_n, tiles, first;  // first: its first tile in the launch
+    float* part;       // [splits][m][n]
+    float* bias_part;  // [splits][m], or null
+};
+
+struct Params {
+    int m, n, k;       // result rows and columns, contraction length (of one segment)
+    int segments;      // kDx: 2
+    int bn;            // columns of a tile
+    int tiles_n;
+    long long tiles;
+    int act;           // 0 silu, 1 gelu
+    const __nv_bfloat16 *bias0, *bias1;
+    Problem pr[3];
+    int splits, blocks_per_split;  // kDw, in blocks of 64 tokens
+    unsigned int* status;
+    unsigned long long limit_ns;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// act(g) and act'(g).  silu: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).  gelu: g
+// Phi(g), Phi(g) + g phi(g), Phi from the error function's approximation 7.1.26 of
+// M. Abramowitz and I. A. Stegun, "Handbook of Mathematical Functions" (absolute
+// error 1.5e-7, far below the result's bf16 step; on the negative side the small tail
+// is the computed term itself, so nothing cancels).
+template <bool kSlope>
+__device__ __forceinline__ void activate(float g, int act, float& a, float& slope) {
+    if (act == 0) {
+        const float s = __fdividef(1.f, 1.f + ex2_approx(-1.4426950408889634f * g));
+        a = g * s;
+        if (kSlope) slope = fmaf(a, 1.f - s, s);
+        return;
+    }
+    const float z = fabsf(g) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+    const float e = ex2_approx(-0.72134752044448170f * g * g);  // e^(-g^2 / 2)
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float tail = 0.5f * p * t * e;  // Phi(-|g|)
+    const float cdf = g < 0.f ? tail : 1.f - tail;
+    a = g * cdf;
+    if (kSlope) slope = fmaf(g * 0.39894228040143268f, e, cdf);
+}
+
+// 32 columns of a bias row from column c (a multiple of 8) on; zero beyond n.
+__device__ __forceinline__ void add_bias(float (&x)[32], const __nv_bfloat16* bias, int c, int n) {
+    if (!bias) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (c + 8 * q >= n) break;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(bias + c + 8 * q));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[8 * q + 2 * e] += bf16lo_to_f32(w[e]);
+            x[8 * q + 2 * e + 1] += bf16hi_to_f32(w[e]);
+        }
+    }
+}
+
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&x)[32]) {
+    uint32_t v[32];
+    tmem_ld32(taddr, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
+    constexpr int stages = stages_of(OP), kStageBytes = stage_bytes(OP);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t* ones = smem + kOnesOff;  // kDw only
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->free_[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->acc_full[i], 1);
+            mbar_init(&bars->acc_free[i], kEpiWarps);
+        }
+        mbar_init(&bars->done, 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars->tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (OP == kDw) {
+        for (int i = tid; i < kOnesBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const uint32_t sbase = smem_u32(smem);
+    const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
+
+    // A tile of the launch: its problem (kDw), first row and column, first block and
+    // number of blocks of its contraction.
+    struct Tile {
+        int pr, m0, n0, kb0, nkb, split;
+    };
+    const int kblocks = (prm.k + kBlockK - 1) / kBlockK;
+    auto tile_of = [&](long long t) {
+        Tile x{0, 0, 0, 0, kblocks * (OP == kDx ? prm.segments : 1), 0};
+        if (OP == kDw) {
+            x.split = static_cast<int>(t % prm.splits);
+            const int q = static_cast<int>(t / prm.splits);
+            x.pr = q >= prm.pr[2].first ? 2 : (q >= prm.pr[1].first ? 1 : 0);
+            const Problem& p = prm.pr[x.pr];
+            const int i = q - p.first;
+            x.m0 = i / p.tiles_n * kBlockM;
+            x.n0 = i % p.tiles_n * prm.bn;
+            x.kb0 = x.split * prm.blocks_per_split;
+            x.nkb = min(prm.blocks_per_split, kblocks - x.kb0);
+        } else {
+            const long long mt = t / prm.tiles_n;
+            x.m0 = static_cast<int>(mt) * kBlockM;
+            x.n0 = static_cast<int>(t - mt * prm.tiles_n) * prm.bn;
+        }
+        return x;
+    };
+    // Columns that a tile's products make: the tile's width, or what is left of the
+    // result, in steps of 16.
+    auto width_of = [&](const Tile& x) {
+        const int left = (OP == kDw ? prm.pr[x.pr].n : prm.n) - x.n0;
+        const int w = left < prm.bn ? left : prm.bn;
+        return (w + 15) & ~15;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0;
+            bool ok = true;
+            for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x) {
+                const Tile x = tile_of(t);
+                for (int i = 0; i < x.nkb; ++i) {
+                    if (!(ok = mbar_wait(&bars->free_[st], ph ^ 1u, ctl, 0x8101))) break;
+                    uint64_t* bar = &bars->full[st];
+                    const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
+                    const int k0 = (x.kb0 + i) * kBlockK;
+                    if (OP == kGate) {
+                        mbar_arrive_expect_tx(bar, kABytes + 2 * prm.bn * 128);
+                        tma_load_2d(s, &maps.a[0], bar, k0, x.m0);
+                        tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
+                        tma_load_2d(sb + prm.bn * 128, &maps.b[1], bar, k0, x.n0);
+                    } else if (OP == kLinear) {
+                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
+                        tma_load_2d(s, &maps.a[0], bar, k0, x.m0);
+                        tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
+                    } else if (OP == kGrad) {
+                        mbar_arrive_expect_tx(bar, 2 * kABytes + 3 * 64 * 128);
+                        tma_load_2d(s, &maps.a[0], bar, k0, x.m0);
+                        tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
+                        tma_load_2d(sb + 64 * 128, &maps.b[1], bar, k0, x.n0);
+                        tma_load_2d(sb + 2 * 64 * 128, &maps.b[2], bar, x.n0, k0);
+                        tma_load_2d(s + kABytes + 3 * 8192, &maps.a[1], bar, k0, x.m0);
+                    } else if (OP == kDx) {
+                        const int seg = i >= kblocks ? 1 : 0, kk = k0 - seg * kblocks * kBlockK;
+                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
+                        tma_load_2d(s, &maps.a[seg], bar, kk, x.m0);
+                        for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[seg], bar, x.n0 + 64 * b, kk);
+                    } else {
+                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
+                        for (int b = 0; b < 2; ++b) tma_load_2d(s + b * 8192, &maps.a[x.pr], bar, x.m0 + 64 * b, k0);
+                        for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
+                    }
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0, n = 0;
+            bool ok = true;
+            for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
+                const Tile x = tile_of(t);
+                const uint32_t acc = tmem + 256 * (n & 1u);
+                if (!mbar_wait(&bars->acc_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8102)) break;
+                tc_fence_after();
+                const int width = width_of(x);
+                const uint32_t id = OP == kGate   ? make_idesc_bf16(kBlockM, 2 * prm.bn, false, false)
+                                    : OP == kGrad ? make_idesc_bf16(kBlockM, 128, false, false)
+                                    : OP == kDw   ? make_idesc_bf16(kBlockM, width, true, true)
+                                                  : make_idesc_bf16(kBlockM, width, false, OP == kDx);
+                const uint32_t id_dh = make_idesc_bf16(kBlockM, 64, false, true);
+                const uint32_t id_ones = make_idesc_bf16(kBlockM, 16, true, false);
+                const bool bias = OP == kDw && x.n0 == 0 && prm.pr[x.pr].bias_part != nullptr;
+                for (int i = 0; i < x.nkb; ++i) {
+                    if (!(ok = mbar_wait(&bars->full[st], ph, ctl, 0x8103))) break;
+                    tc_fence_after();
+                    const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
+                    const int kb = OP == kDx && i >= kblocks ? i - kblocks : x.kb0 + i;
+                    const int left = prm.k - kb * kBlockK;
+                    const int steps = left >= kBlockK ? kBlockK / 16 : (left + 15) / 16;
+                    for (int k = 0; k < steps; ++k) {
+                        const uint32_t more = i > 0 || k > 0;
+                        if (OP == kDw) {
+                            const uint64_t da = make_sdesc(s, 8192, 1024, kSw128) + 128 * k;
+                            umma_ss(acc, da, make_sdesc(sb, 8192, 1024, kSw128) + 128 * k, id, more);
+                            if (bias) umma_ss(acc + kColOnes, da, make_sdesc(smem_u32(ones), 16, 1024, kSw128) + 2 * k, id_ones, more);
+                        } else {
+                            const uint64_t da = make_sdesc(s, 16, 1024, kSw128) + 2 * k;
+                            const uint64_t db = OP == kDx ? make_sdesc(sb, 8192, 1024, kSw128) + 128 * k
+                                                          : make_sdesc(sb, 16, 1024, kSw128) + 2 * k;
+                            umma_ss(acc, da, db, id, more);
+                            if (OP == kGrad)
+                                umma_ss(acc + 128, make_sdesc(s + kABytes + 3 * 8192, 16, 1024, kSw128) + 2 * k,
+                                        make_sdesc(sb + 2 * 64 * 128, 8192, 1024, kSw128) + 128 * k, id_dh, more);
+                        }
+                    }
+                    umma_commit(&bars->free_[st]);
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) umma_commit(&bars->acc_full[n & 1u]);
+            }
+            umma_commit(&bars->done);  // every product issued here has completed before the columns are freed
+            mbar_wait(&bars->done, 0, ctl, 0x81ff);
+        }
+    } else if (warp >= 4) {
+        const int ew = warp - 4, quad = ew & 3, half = ew >> 2;
+        const int row_in = quad * 32 + lane;
+        const uint32_t store = sbase + kStoreOff + ew * 2 * kStoreBytes;
+        uint32_t n = 0, sbuf = 0;
+        // A warp's 32 x 32 block of results: staged in bf16, stored by TMA (which leaves
+        // out what lies outside the result).  Two buffers: the store before the last has
+        // read its buffer.
+        auto put = [&](const CUtensorMap* m, const float (&x)[32], int col, int row0) {
+            bulk_wait_read_but1();
+            __syncwarp();
+            const uint32_t dst = store + (sbuf & 1u) * kStoreBytes + lane * 64;
+            const int sw = (lane >> 1) & 3;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 v = pack_chunk(x, c);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ sw) << 4)), "r"(v.x), "r"(v.y),
+                             "r"(v.z), "r"(v.w)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(m, store + (sbuf & 1u) * kStoreBytes, col, row0);
+                bulk_commit();
+            }
+            ++sbuf;
+        };
+        for (long long t = blockIdx.x; t < prm.tiles; t += gridDim.x, ++n) {
+            const Tile x = tile_of(t);
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[n & 1u], (n >> 1) & 1u, ctl, 0x8104));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + 256 * (n & 1u) + (static_cast<uint32_t>(quad * 32) << 16);
+            const int row0 = x.m0 + quad * 32;
+            if (OP == kDw) {
+                const Problem& p = prm.pr[x.pr];
+                const int row = x.m0 + row_in, width = width_of(x);
+                float* dst = p.part + (static_cast<long long>(x.split) * p.m + row) * p.n + x.n0;
+                for (int c = 32 * half; c < width; c += 64) {
+                    float v[32];
+                    load_cols(acc + c, v);
+                    if (row < p.m) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (x.n0 + c + e < p.n)
+                                *reinterpret_cast<float4*>(dst + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                }
+                if (half == 0 && x.n0 == 0 && p.bias_part) {
+                    uint32_t v[16];
+                    tmem_ld16(acc + kColOnes, v);
+                    tmem_wait_ld();
+                    if (row < p.m) p.bias_part[static_cast<long long>(x.split) * p.m + row] = __uint_as_float(v[0]);
+                }
+            } else {
+                const int left = prm.n - x.n0, width = left < prm.bn ? left : prm.bn;
+                for (int c = 32 * half; c < width; c += 64) {
+                    const int col = x.n0 + c;
+                    float a[32];
+                    load_cols(acc + c, a);
+                    if (OP == kLinear || OP == kDx) {
+                        if (OP == kLinear) add_bias(a, prm.bias0, col, prm.n);
+                    } else {
+                        float u[32];
+                        load_cols(acc + prm.bn + c, u);
+                        add_bias(a, prm.bias0, col, prm.n);
+                        add_bias(u, prm.bias1, col, prm.n);
+                        if (OP == kGate) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float f, s;
+                                activate<false>(a[e], prm.act, f, s);
+                                a[e] = f * u[e];
+                            }
+                        } else {
+                            float dh[32], du[32];
+                            load_cols(acc + 128 + c, dh);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float f, s;
+                                activate<true>(a[e], prm.act, f, s);
+                                du[e] = dh[e] * f;
+                                a[e] = f * u[e];
+                                dh[e] *= u[e] * s;
+                            }
+                            put(&maps.out[1], dh, col, row0);
+                            put(&maps.out[2], du, col, row0);
+                        }
+                    }
+                    put(&maps.out[0], a, col, row0);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->acc_free[n & 1u]);
+        }
+        bulk_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Weight and bias gradients: the splits' partial results added in order.
+struct SumParams {
+    const float* part[6];
+    __nv_bfloat16* out[6];
+    long long size[6];
+    long long blocks[7];  // first block of each result
+    int splits;
+};
+__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumParams p) {
+    int i = 0;
+    while (blockIdx.x >= p.blocks[i + 1]) ++i;
+    const long long e = ((blockIdx.x - p.blocks[i]) * 256 + threadIdx.x) * 4;
+    if (e >= p.size[i]) return;  // sizes are multiples of 8
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < p.splits; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part[i] + k * p.size[i] + e);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(p.out[i] + e) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
+template <int OP>
+cudaError_t launch(const Maps& maps, const Params& prm, int num_sms, cudaStream_t stream) {
+    static SmemOptIn optin;
+    if (cudaError_t e = optin.ensure(reinterpret_cast<const void*>(mlp_kernel<OP>), kSmemBytes)) return e;
+    const long long grid = prm.tiles < num_sms ? prm.tiles : num_sms;
+    mlp_kernel<OP><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(maps, prm);
+    return cudaGetLastError();
+}
+
+// The equal tiles of at most `most` columns (a multiple of `step`) that cover n.
+inline int tile_width(int n, int most, int step) {
+    const int tiles = (n + most - 1) / most;
+    return ((n + tiles - 1) / tiles + step - 1) / step * step;
+}
+
+// Splits of the tokens for the weight gradients: of 1 .. 16 the one with the least
+// work on the busiest SM (waves / splits), more splits costing 1 % each for their
+// partial results; no split shorter than four blocks.
+inline int pick_splits(int tiles, int kblocks, int num_sms) {
+    int best = 1;
+    double cost = 1e30;
+    for (int s = 1; s <= 16; ++s) {
+        const int per = (kblocks + s - 1) / s;
+        if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;
+        const double waves = static_cast<double>((static_cast<long long>(tiles) * s + num_sms - 1) / num_sms);
+        const double c = waves * per * (1.0 + 0.01 * s);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+constexpr int kMaxSplits = 16;
+
+}  // namespace mlp
+
+// ------------------------------------------------------------------ host
+namespace {
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct BwdLayout {
+    size_t h, dg, du, part[3], bias[3], total;
+};
+BwdLayout bwd_layout(const MlpShape& sh) {
+    const size_t tf = round256(static_cast<size_t>(sh.tokens) * sh.hidden * 2);
+    const size_t cf = static_cast<size_t>(sh.channels) * sh.hidden * 4 * mlp::kMaxSplits;
+    BwdLayout L{};
+    size_t o = 0;
+    L.h = o;  o += tf;
+    L.dg = o; o += tf;
+    L.du = o; o += tf;
+    for (int i = 0; i < 3; ++i) {
+        L.part[i] = o;
+        o += round256(cf);
+        L.bias[i] = o;
+        o += round256(static_cast<size_t>(i == 2 ? sh.channels : sh.hidden) * 4 * mlp::kMaxSplits);
+    }
+    L.total = o;
+    return L;
+}
+
+}  // namespace
+
+size_t mlp_fwd_workspace_bytes(const MlpShape& sh) {
+    return round256(static_cast<size_t>(sh.tokens) * sh.hidden * 2);
+}
+size_t mlp_bwd_workspace_bytes(const MlpShape& sh) { return bwd_layout(sh).total; }
+
+cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                           int num_sms, cudaStream_t stream) {
+    using namespace mlp;
+    const int T = static_cast<int>(sh.tokens), C = sh.channels, F = sh.hidden;
+    const int rows_m = (T + kBlockM - 1) / kBlockM;
+    Maps maps{};
+    Params prm{};
+    prm.status = status;
+    prm.limit_ns = limit_ns;
+    prm.act = sh.act;
+    prm.m = T;
+    prm.n = F;
+    prm.k = C;
+    prm.bn = tile_width(F, 128, 32);
+    prm.tiles_n = (F + prm.bn - 1) / prm.bn;
+    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_gate);
+    prm.bias1 = static_cast<const __nv_bfloat16*>(p.b_up);
+    if (encode_matrix(&maps.a[0], p.x, T, C, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.b[0], p.w_gate, F, C, prm.bn, kBlockK, true) ||
+        encode_matrix(&maps.b[1], p.w_up, F, C, prm.bn, kBlockK, true) ||
+        encode_matrix(&maps.out[0], p.ws, T, F, 32, 32, false))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch<kGate>(maps, prm, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    prm.n = C;
+    prm.k = F;
+    prm.bn = tile_width(C, 256, 32);
+    prm.tiles_n = (C + prm.bn - 1) / prm.bn;
+    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_down);
+    if (encode_matrix(&maps.a[0], p.ws, T, F, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.b[0], p.w_down, C, F, prm.bn, kBlockK, true) ||
+        encode_matrix(&maps.out[0], p.y, T, C, 32, 32, false))
+        return cudaErrorInvalidValue;
+    return launch<kLinear>(maps, prm, num_sms, stream);
+}
+
+cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                           int num_sms, cudaStream_t stream) {
+    using namespace mlp;
+    const int T = static_cast<int>(sh.tokens), C = sh.channels, F = sh.hidden;
+    const int rows_m = (T + kBlockM - 1) / kBlockM;
+    const BwdLayout L = bwd_layout(sh);
+    uint8_t *h = p.ws + L.h, *dg = p.ws + L.dg, *du = p.ws + L.du;
+    Maps maps{};
+    Params prm{};
+    prm.status = status;
+    prm.limit_ns = limit_ns;
+    prm.act = sh.act;
+    // h, dg, du
+    prm.m = T;
+    prm.n = F;
+    prm.k = C;
+    prm.bn = 64;
+    prm.tiles_n = (F + 63) / 64;
+    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_gate);
+    prm.bias1 = static_cast<const __nv_bfloat16*>(p.b_up);
+    if (encode_matrix(&maps.a[0], p.x, T, C, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.a[1], p.dy, T, C, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.b[0], p.w_gate, F, C, 64, kBlockK, true) ||
+        encode_matrix(&maps.b[1], p.w_up, F, C, 64, kBlockK, true) ||
+        encode_matrix(&maps.b[2], p.w_down, C, F, kBlockK, 64, true) ||
+        encode_matrix(&maps.out[0], h, T, F, 32, 32, false) || encode_matrix(&maps.out[1], dg, T, F, 32, 32, false) ||
+        encode_matrix(&maps.out[2], du, T, F, 32, 32, false))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch<kGrad>(maps, prm, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    // dx
+    prm.n = C;
+    prm.k = F;
+    prm.segments = 2;
+    prm.bn = tile_width(C, 256, 64);
+    prm.tiles_n = (C + prm.bn - 1) / prm.bn;
+    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    if (encode_matrix(&maps.a[0], dg, T, F, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.a[1], du, T, F, kBlockM, kBlockK, true) ||
+        encode_matrix(&maps.b[0], p.w_gate, F, C, kBlockK, 64, true) ||
+        encode_matrix(&maps.b[1], p.w_up, F, C, kBlockK, 64, true) ||
+        encode_matrix(&maps.out[0], p.dx, T, C, 32, 32, false))
+        return cudaErrorInvalidValue;
+    if ((e = launch<kDx>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
+    // weights and biases
+    prm.k = T;
+    prm.bn = kDwMaxN;
+    const void *as[3] = {dg, du, p.dy}, *bs[3] = {p.x, p.x, h};
+    void* const outs[6] = {p.dw_gate, p.dw_up, p.dw_down, p.db_gate, p.db_up, p.db_down};
+    int first = 0;
+    for (int i = 0; i < 3; ++i) {
+        Problem& q = prm.pr[i];
+        q.m = i == 2 ? C : F;
+        q.n = i == 2 ? F : C;
+        q.tiles_n = (q.n + prm.bn - 1) / prm.bn;
+        q.tiles = (q.m + kBlockM - 1) / kBlockM * q.tiles_n;
+        q.first = first;
+        first += q.tiles;
+        q.part = reinterpret_cast<float*>(p.ws + L.part[i]);
+        q.bias_part = outs[3 + i] ? reinterpret_cast<float*>(p.ws + L.bias[i]) : nullptr;
+        if (encode_matrix(&maps.a[i], as[i], T, q.m, kBlockK, 64, true) ||
+            encode_matrix(&maps.b[i], bs[i], T, q.n, kBlockK, 64, true))
+            return cudaErrorInvalidValue;
+    }
+    const int kblocks = (T + kBlockK - 1) / kBlockK;
+    prm.splits = pick_splits(first, kblocks, num_sms);
+    prm.blocks_per_split = (kblocks + prm.splits - 1) / prm.splits;
+    prm.tiles = static_cast<long long>(first) * prm.splits;
+    if ((e = launch<kDw>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
+    SumParams sum{};
+    sum.splits = prm.splits;
+    int count = 0;
+    long long blocks = 0;
+    for (int i = 0; i < 6; ++i) {
+        if (!outs[i]) continue;
+        sum.part[count] = i < 3 ? prm.pr[i].part : prm.pr[i - 3].bias_part;
+        sum.out[count] = static_cast<__nv_bfloat16*>(outs[i]);
+        sum.size[count] = i < 3 ? static_cast<long long>(C) * F : prm.pr[i - 3].m;
+        sum.blocks[count] = blocks;
+        blocks += (sum.size[count] / 4 + 255) / 256;
+        ++count;
+    }
+    for (int i = count; i < 7; ++i) sum.blocks[i] = blocks;
+    sum_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(sum);
+    return cudaGetLastError();
+}
+
+}  // namespace fswin

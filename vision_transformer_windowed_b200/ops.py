@@ -531,3 +531,86 @@ def residual_norm(x, f, gate=None, scale=None, post=None, post_weight=None, post
                   pre_weight=None, pre_bias=None, eps: float = 1e-5, p: float = 0.0, rng=None):
     """Autograd residual step; arguments and results as residual_norm_fwd."""
     return ResidualNorm.apply(x, f, gate, scale, post_weight, post_bias, pre_weight, pre_bias, rng, pre, post, eps, p)
+
+
+# ------------------------------------------------------------- gated feed-forward
+_ACTS = {"silu": 0, "gelu": 1}
+_MLP_PARAMS = ("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down")
+GatedMlpGrads = namedtuple("GatedMlpGrads", ("dx",) + tuple("d" + n for n in _MLP_PARAMS))
+
+
+def _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act: str):
+    if act not in _ACTS:
+        raise ValueError("act must be 'silu' or 'gelu'")
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise ValueError("expected x [..., channels] and w_gate [hidden, channels]")
+    C, F = x.shape[-1], w_gate.shape[0]
+    _check_tensor("x", x, x.shape, torch.bfloat16)
+    for name, t, shape in (("w_gate", w_gate, (F, C)), ("w_up", w_up, (F, C)), ("w_down", w_down, (C, F)),
+                           ("b_gate", b_gate, (F,)), ("b_up", b_up, (F,)), ("b_down", b_down, (C,))):
+        if t is not None or name[0] == "w":
+            _check_tensor(name, t, shape, torch.bfloat16)
+    _check_on(x.device, w_gate=w_gate, w_up=w_up, w_down=w_down, b_gate=b_gate, b_up=b_up, b_down=b_down)
+    return _lib.MlpShape(x.numel() // C if C else 0, C, F, _ACTS[act])
+
+
+def _mlp_workspace(need: int, workspace, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), device=device, dtype=torch.uint8)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _check_on(device, workspace=workspace)
+    return workspace
+
+
+def gated_mlp_fwd(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, act: str = "silu", y=None,
+                  workspace=None):
+    """y = (act(x w_gate^T + b_gate) * (x w_up^T + b_up)) w_down^T + b_down, all bf16.
+
+    x [..., C]; w_gate, w_up [F, C]; w_down [C, F]; C and F multiples of 8; act "silu" or "gelu"."""
+    sh = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
+    y = torch.empty_like(x) if y is None else y
+    _check_tensor("y", y, x.shape, torch.bfloat16)
+    _check_on(x.device, y=y)
+    ws = _mlp_workspace(_lib.fs_gated_mlp_fwd_workspace_bytes(sh), workspace, x.device)
+    with _on(x.device):
+        _lib.fs_gated_mlp_fwd(sh, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ptr(b_gate),
+                              _ptr(b_up), _ptr(b_down), y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device))
+    return y
+
+
+def gated_mlp_bwd(dy, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, act: str = "silu", workspace=None):
+    """Gradients of sum(y * dy) as GatedMlpGrads, None for absent biases."""
+    sh = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
+    _check_tensor("dy", dy, x.shape, torch.bfloat16)
+    _check_on(x.device, dy=dy)
+    out = [None if t is None else torch.empty_like(t) for t in (x, w_gate, w_up, w_down, b_gate, b_up, b_down)]
+    ws = _mlp_workspace(_lib.fs_gated_mlp_bwd_workspace_bytes(sh), workspace, x.device)
+    with _on(x.device):
+        _lib.fs_gated_mlp_bwd(sh, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                              _ptr(b_gate), _ptr(b_up), *(_ptr(t) for t in out), ws.data_ptr(), ws.numel(),
+                              _stream(x.device))
+    return GatedMlpGrads(*out)
+
+
+class GatedMlp(torch.autograd.Function):
+    """Autograd wrapper of the gated feed-forward block (forward and backward in libfswin.so)."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, b_gate, b_up, b_down, act):
+        params = (w_gate, w_up, w_down, b_gate, b_up, b_down)
+        ctx.present = [t is not None for t in params]
+        ctx.save_for_backward(x, *(t for t in params if t is not None))
+        ctx.act = act
+        return gated_mlp_fwd(x, *params, act=act)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, *rest = ctx.saved_tensors
+        params = [rest.pop(0) if there else None for there in ctx.present]
+        return (*gated_mlp_bwd(dy.contiguous(), x, *params, act=ctx.act), None)
+
+
+def gated_mlp(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, act: str = "silu"):
+    """Autograd gated feed-forward block; arguments as gated_mlp_fwd."""
+    return GatedMlp.apply(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
