@@ -49,6 +49,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libfswin.so (building it first when it is missing and nvcc exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

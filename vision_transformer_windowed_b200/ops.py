@@ -285,39 +285,61 @@ def log_distance_buckets(M: int, exact: int = 4, device="cuda"):
     return (one[:, None] * n + one[None, :]).contiguous().to(device), n * n
 
 
-def _check_on(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _need(name: str, t: torch.Tensor, dtype, shape, device: int) -> None:
+    """One argument's checks in one test; only a failing argument takes the slow road to its message."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
+    _check_tensor(name, t, shape, dtype)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 class _on:
-    """Makes the tensors' device current for the launches (a no-op when it is)."""
+    """Makes the tensors' device current for the launches (a no-op when it is); gives its current stream."""
 
-    def __init__(self, device):
-        self.index = device.index if device.index != torch.cuda.current_device() else -1
+    def __init__(self, device: int):
+        self.device = device
+        self.prev = torch._C._cuda_getDevice()
 
-    def __enter__(self):
-        if self.index >= 0:
-            self.prev = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
+    def __enter__(self) -> int:
+        if self.prev != self.device:
+            torch.cuda.set_device(self.device)
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
     def __exit__(self, *exc):
-        if self.index >= 0:
+        if self.prev != self.device:
             torch.cuda.set_device(self.prev)
 
 
-def _check_relbias(q, k, v, table, M: int, buckets) -> None:
+def _workspace(need: int, workspace, device: int) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 256), device=torch.device("cuda", device), dtype=torch.uint8)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{device}")
+    return workspace
+
+
+def _check_relbias(q, k, v, table, M: int, buckets) -> int:
+    device, shape = _device_of("q", q), q.shape
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_tensor(name, t, q.shape, torch.bfloat16)
+        _need(name, t, torch.bfloat16, shape, device)
     if table.dim() != 2:
         raise ValueError("table must be [heads, buckets]")
-    _check_tensor("table", table, (q.shape[3], table.shape[1]), torch.bfloat16)
+    _need("table", table, torch.bfloat16, (shape[3], table.shape[1]), device)
     if buckets is not None:
-        _check_tensor("buckets", buckets, (2 * M - 1, 2 * M - 1), torch.int32)
+        _need("buckets", buckets, torch.int32, (2 * M - 1, 2 * M - 1), device)
     elif table.shape[1] != (2 * M - 1) ** 2:
         raise ValueError(f"without a bucket map the table has {(2 * M - 1) ** 2} entries a head, got {table.shape[1]}")
-    _check_on(q.device, k=k, v=v, table=table, buckets=buckets)
+    return device
 
 
 def winattn_relbias_fwd(q, k, v, table, M: int, s: int, buckets=None, o=None, lse=None, need_lse: bool = True):
@@ -326,20 +348,18 @@ def winattn_relbias_fwd(q, k, v, table, M: int, s: int, buckets=None, o=None, ls
     table: bf16 [heads, n]; buckets: int32 [2M-1, 2M-1] (query minus key, row then column, each plus M-1), or None:
     n = (2M-1)^2.  A bucket outside [0, n) adds no bias.  need_lse=False: inference, LSE is returned as None."""
     sh = _shape(q, M, s)
-    B, H, W, heads, d = q.shape
-    _check_relbias(q, k, v, table, M, buckets)
+    device = _check_relbias(q, k, v, table, M, buckets)
     if o is None:
         o = torch.empty_like(q)
-    if lse is None and need_lse:
-        lse = torch.empty((B, H, W, heads), device=q.device, dtype=torch.float32)
-    _check_tensor("o", o, q.shape, torch.bfloat16)
+    else:
+        _need("o", o, torch.bfloat16, q.shape, device)
     if lse is not None:
-        _check_tensor("lse", lse, (B, H, W, heads), torch.float32)
-    _check_on(q.device, o=o, lse=lse)
-    with _on(q.device):
-        _lib.fs_winattn_relbias_fwd(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
-                                    buckets.data_ptr() if buckets is not None else 0, table.shape[1], o.data_ptr(),
-                                    lse.data_ptr() if lse is not None else 0, _stream(q.device))
+        _need("lse", lse, torch.float32, q.shape[:4], device)
+    elif need_lse:
+        lse = torch.empty(q.shape[:4], device=q.device, dtype=torch.float32)
+    with _on(device) as stream:
+        _lib.fs_winattn_relbias_fwd(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(), _ptr(buckets),
+                                    table.shape[1], o.data_ptr(), _ptr(lse), stream)
     return o, lse
 
 
@@ -352,28 +372,23 @@ def winattn_relbias_bwd(q, k, v, o, dout, lse, table, M: int, s: int, buckets=No
                         dv=None, dtable=None):
     """dQ, dK, dV, dtable (bf16, like the table) of sum(O * dout)."""
     sh = _shape(q, M, s)
-    B, H, W, heads, d = q.shape
-    _check_relbias(q, k, v, table, M, buckets)
-    for name, t in (("o", o), ("dout", dout)):
-        _check_tensor(name, t, q.shape, torch.bfloat16)
-    _check_tensor("lse", lse, (B, H, W, heads), torch.float32)
+    device, shape = _check_relbias(q, k, v, table, M, buckets), q.shape
+    for name, t in (("o", o), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
+        if t is not None:
+            _need(name, t, torch.bfloat16, shape, device)
+    _need("lse", lse, torch.float32, shape[:4], device)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(q) if dk is None else dk
     dv = torch.empty_like(q) if dv is None else dv
-    dtable = torch.empty_like(table) if dtable is None else dtable
-    for name, t, ref in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("dtable", dtable, table)):
-        _check_tensor(name, t, ref.shape, torch.bfloat16)
-    if workspace is None:
-        workspace = alloc_relbias_workspace(q, M, s)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check_on(q.device, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, dtable=dtable, workspace=workspace)
-    with _on(q.device):
+    if dtable is None:
+        dtable = torch.empty_like(table)
+    else:
+        _need("dtable", dtable, torch.bfloat16, table.shape, device)
+    ws = _workspace(_lib.fs_winattn_relbias_bwd_workspace_bytes(sh) if workspace is None else 0, workspace, device)
+    with _on(device) as stream:
         _lib.fs_winattn_relbias_bwd(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
-                                    lse.data_ptr(), table.data_ptr(),
-                                    buckets.data_ptr() if buckets is not None else 0, table.shape[1], dq.data_ptr(),
-                                    dk.data_ptr(), dv.data_ptr(), dtable.data_ptr(), workspace.data_ptr(),
-                                    workspace.numel(), _stream(q.device))
+                                    lse.data_ptr(), table.data_ptr(), _ptr(buckets), table.shape[1], dq.data_ptr(),
+                                    dk.data_ptr(), dv.data_ptr(), dtable.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     return dq, dk, dv, dtable
 
 
@@ -409,36 +424,34 @@ _STEP_PARAMS = ("gate", "scale", "post_weight", "post_bias", "pre_weight", "pre_
 ResidualNormGrads = namedtuple("ResidualNormGrads", ("dx", "df") + tuple("d" + n for n in _STEP_PARAMS))
 
 
-def _ptr(t) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
 def _resnorm_shape(stream, f, params, pre, post, eps: float, p: float, rng):
-    """Checks a residual step's arguments; `stream`: x, or r in the backward."""
+    """(shape, device) of a residual step whose arguments pass the checks; `stream`: x, or r in the backward; params in
+    the order of _STEP_PARAMS."""
     if pre not in _NORMS or post not in _NORMS:
         raise ValueError("pre and post must be None, 'layer' or 'rms'")
-    if stream.dim() < 2:
+    shape, dtype = stream.shape, stream.dtype
+    if len(shape) < 2:
         raise ValueError("expected a [samples, ..., channels] tensor")
-    if stream.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"the residual stream must be bfloat16 or float32, got {stream.dtype}")
-    B, C = stream.shape[0], stream.shape[-1]
-    _check_tensor("x", stream, stream.shape, stream.dtype)
-    _check_tensor("f", f, stream.shape, torch.bfloat16)
-    for name, t in params.items():
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"the residual stream must be bfloat16 or float32, got {dtype}")
+    B, C = shape[0], shape[-1]
+    device = _device_of("x", stream)
+    _need("x", stream, dtype, shape, device)
+    _need("f", f, torch.bfloat16, shape, device)
+    for name, t in zip(_STEP_PARAMS, params):
         if t is not None:
-            _check_tensor(name, t, (B,) if name == "gate" else (C,), stream.dtype)
-    for kind, which in ((pre, "pre"), (post, "post")):
-        if kind is None and (params[which + "_weight"] is not None or params[which + "_bias"] is not None):
+            _need(name, t, dtype, (B,) if name == "gate" else (C,), device)
+    for kind, which, w, b in ((post, "post", params[2], params[3]), (pre, "pre", params[4], params[5])):
+        if kind is None and (w is not None or b is not None):
             raise ValueError(f"{which}_weight and {which}_bias need {which}='layer' or 'rms'")
     if not 0.0 <= p < 1.0:
         raise ValueError("p must lie in [0, 1)")
     if p > 0.0:
         if rng is None:
             raise ValueError("dropout needs rng, an int64 tensor (seed, offset)")
-        _check_tensor("rng", rng, (2,), torch.int64)
-    _check_on(stream.device, f=f, rng=rng, **params)
+        _need("rng", rng, torch.int64, (2,), device)
     tokens = stream.numel() // (B * C) if B and C else 0
-    return _lib.ResnormShape(B, tokens, C, int(stream.dtype == torch.float32), _NORMS[pre], _NORMS[post], eps, p)
+    return _lib.ResnormShape(B, tokens, C, dtype is torch.float32, _NORMS[pre], _NORMS[post], eps, p), device
 
 
 def residual_norm_fwd(x, f, gate=None, scale=None, post=None, post_weight=None, post_bias=None, pre="layer",
@@ -450,20 +463,22 @@ def residual_norm_fwd(x, f, gate=None, scale=None, post=None, post_weight=None, 
     or "rms", with weight and bias or without.  Parameters are of x's type, n is bf16.  p: dropout probability, drawn
     from rng, an int64 CUDA tensor (seed, offset) that the kernel reads when it runs; advance the offset between
     steps.  r may be x and n may be f, to work in place."""
-    params = dict(gate=gate, scale=scale, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
-                  pre_bias=pre_bias)
-    sh = _resnorm_shape(x, f, params, pre, post, eps, p, rng)
-    r = torch.empty_like(x) if r is None else r
-    n = torch.empty_like(f) if n is None and pre is not None else n
-    _check_tensor("r", r, x.shape, x.dtype)
-    if pre is not None:
-        _check_tensor("n", n, x.shape, torch.bfloat16)
-    _check_on(x.device, r=r, n=n)
-    with _on(x.device):
-        _lib.fs_resnorm_fwd(sh, x.data_ptr(), f.data_ptr(), _ptr(gate), _ptr(scale), _ptr(post_weight), _ptr(post_bias),
-                            _ptr(pre_weight), _ptr(pre_bias), _ptr(rng) if p > 0.0 else 0, r.data_ptr(), _ptr(n),
-                            _stream(x.device))
-    return r, n if pre is not None else None
+    params = (gate, scale, post_weight, post_bias, pre_weight, pre_bias)
+    sh, device = _resnorm_shape(x, f, params, pre, post, eps, p, rng)
+    if r is None:
+        r = torch.empty_like(x)
+    else:
+        _need("r", r, x.dtype, x.shape, device)
+    if pre is None:
+        n = None
+    elif n is None:
+        n = torch.empty_like(f)
+    else:
+        _need("n", n, torch.bfloat16, x.shape, device)
+    with _on(device) as stream:
+        _lib.fs_resnorm_fwd(sh, x.data_ptr(), f.data_ptr(), *map(_ptr, params), _ptr(rng) if p > 0.0 else 0,
+                            r.data_ptr(), _ptr(n), stream)
+    return r, n
 
 
 def residual_norm_bwd(dr, dn, r, f, gate=None, scale=None, post=None, post_weight=None, post_bias=None, pre="layer",
@@ -471,30 +486,22 @@ def residual_norm_bwd(dr, dn, r, f, gate=None, scale=None, post=None, post_weigh
                       skip=()):
     """Gradients of sum(r * dr) + sum(n * dn) as ResidualNormGrads; None for an absent parameter and for the names in
     `skip` ("gate", "scale", ...).  dr or dn may be None (zero); r is the forward's, rng as the forward read it."""
-    params = dict(gate=gate, scale=scale, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
-                  pre_bias=pre_bias)
-    sh = _resnorm_shape(r, f, params, pre, post, eps, p, rng)
+    params = (gate, scale, post_weight, post_bias, pre_weight, pre_bias)
+    sh, device = _resnorm_shape(r, f, params, pre, post, eps, p, rng)
     if dr is not None:
-        _check_tensor("dr", dr, r.shape, r.dtype)
+        _need("dr", dr, r.dtype, r.shape, device)
     if dn is not None:
         if pre is None:
             raise ValueError("dn without a pre norm")
-        _check_tensor("dn", dn, r.shape, torch.bfloat16)
-    need = _lib.fs_resnorm_bwd_workspace_bytes(sh)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), device=r.device, dtype=torch.uint8)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check_on(r.device, dr=dr, dn=dn, workspace=workspace)
-    out = {name: None if t is None or name in skip else torch.empty_like(t) for name, t in params.items()}
+        _need("dn", dn, torch.bfloat16, r.shape, device)
+    ws = _workspace(_lib.fs_resnorm_bwd_workspace_bytes(sh) if workspace is None else 0, workspace, device)
+    out = [None if t is None or name in skip else torch.empty_like(t) for name, t in zip(_STEP_PARAMS, params)]
     dx, df = torch.empty_like(r), torch.empty_like(f)
-    with _on(r.device):
-        _lib.fs_resnorm_bwd(sh, _ptr(dr), _ptr(dn), r.data_ptr(), f.data_ptr(), _ptr(gate), _ptr(scale),
-                            _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias),
-                            _ptr(rng) if p > 0.0 else 0, dx.data_ptr(), df.data_ptr(),
-                            *(_ptr(out[name]) for name in _STEP_PARAMS), workspace.data_ptr(), workspace.numel(),
-                            _stream(r.device))
-    return ResidualNormGrads(dx, df, *(out[name] for name in _STEP_PARAMS))
+    with _on(device) as stream:
+        _lib.fs_resnorm_bwd(sh, _ptr(dr), _ptr(dn), r.data_ptr(), f.data_ptr(), *map(_ptr, params),
+                            _ptr(rng) if p > 0.0 else 0, dx.data_ptr(), df.data_ptr(), *map(_ptr, out), ws.data_ptr(),
+                            ws.numel(), stream)
+    return ResidualNormGrads(dx, df, *out)
 
 
 class ResidualNorm(torch.autograd.Function):
@@ -540,27 +547,19 @@ GatedMlpGrads = namedtuple("GatedMlpGrads", ("dx",) + tuple("d" + n for n in _ML
 
 
 def _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act: str):
+    """(shape, device) of a gated feed-forward block whose arguments pass the checks."""
     if act not in _ACTS:
         raise ValueError("act must be 'silu' or 'gelu'")
     if x.dim() < 1 or w_gate.dim() != 2:
         raise ValueError("expected x [..., channels] and w_gate [hidden, channels]")
     C, F = x.shape[-1], w_gate.shape[0]
-    _check_tensor("x", x, x.shape, torch.bfloat16)
-    for name, t, shape in (("w_gate", w_gate, (F, C)), ("w_up", w_up, (F, C)), ("w_down", w_down, (C, F)),
-                           ("b_gate", b_gate, (F,)), ("b_up", b_up, (F,)), ("b_down", b_down, (C,))):
-        if t is not None or name[0] == "w":
-            _check_tensor(name, t, shape, torch.bfloat16)
-    _check_on(x.device, w_gate=w_gate, w_up=w_up, w_down=w_down, b_gate=b_gate, b_up=b_up, b_down=b_down)
-    return _lib.MlpShape(x.numel() // C if C else 0, C, F, _ACTS[act])
-
-
-def _mlp_workspace(need: int, workspace, device):
-    if workspace is None:
-        return torch.empty(max(need, 256), device=device, dtype=torch.uint8)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check_on(device, workspace=workspace)
-    return workspace
+    device = _device_of("x", x)
+    for name, t, shape in (("x", x, x.shape), ("w_gate", w_gate, (F, C)), ("w_up", w_up, (F, C)),
+                           ("w_down", w_down, (C, F)), ("b_gate", b_gate, (F,)), ("b_up", b_up, (F,)),
+                           ("b_down", b_down, (C,))):
+        if t is not None:
+            _need(name, t, torch.bfloat16, shape, device)
+    return _lib.MlpShape(x.numel() // C if C else 0, C, F, _ACTS[act]), device
 
 
 def gated_mlp_fwd(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, act: str = "silu", y=None,
@@ -568,28 +567,27 @@ def gated_mlp_fwd(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, 
     """y = (act(x w_gate^T + b_gate) * (x w_up^T + b_up)) w_down^T + b_down, all bf16.
 
     x [..., C]; w_gate, w_up [F, C]; w_down [C, F]; C and F multiples of 8; act "silu" or "gelu"."""
-    sh = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
-    y = torch.empty_like(x) if y is None else y
-    _check_tensor("y", y, x.shape, torch.bfloat16)
-    _check_on(x.device, y=y)
-    ws = _mlp_workspace(_lib.fs_gated_mlp_fwd_workspace_bytes(sh), workspace, x.device)
-    with _on(x.device):
+    sh, device = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need("y", y, torch.bfloat16, x.shape, device)
+    ws = _workspace(_lib.fs_gated_mlp_fwd_workspace_bytes(sh) if workspace is None else 0, workspace, device)
+    with _on(device) as stream:
         _lib.fs_gated_mlp_fwd(sh, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ptr(b_gate),
-                              _ptr(b_up), _ptr(b_down), y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device))
+                              _ptr(b_up), _ptr(b_down), y.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     return y
 
 
 def gated_mlp_bwd(dy, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, act: str = "silu", workspace=None):
     """Gradients of sum(y * dy) as GatedMlpGrads, None for absent biases."""
-    sh = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
-    _check_tensor("dy", dy, x.shape, torch.bfloat16)
-    _check_on(x.device, dy=dy)
+    sh, device = _mlp_shape(x, w_gate, w_up, w_down, b_gate, b_up, b_down, act)
+    _need("dy", dy, torch.bfloat16, x.shape, device)
     out = [None if t is None else torch.empty_like(t) for t in (x, w_gate, w_up, w_down, b_gate, b_up, b_down)]
-    ws = _mlp_workspace(_lib.fs_gated_mlp_bwd_workspace_bytes(sh), workspace, x.device)
-    with _on(x.device):
+    ws = _workspace(_lib.fs_gated_mlp_bwd_workspace_bytes(sh) if workspace is None else 0, workspace, device)
+    with _on(device) as stream:
         _lib.fs_gated_mlp_bwd(sh, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
-                              _ptr(b_gate), _ptr(b_up), *(_ptr(t) for t in out), ws.data_ptr(), ws.numel(),
-                              _stream(x.device))
+                              _ptr(b_gate), _ptr(b_up), *map(_ptr, out), ws.data_ptr(), ws.numel(), stream)
     return GatedMlpGrads(*out)
 
 
