@@ -31,43 +31,64 @@ constexpr float kScale = 0.17677669529663688f;  // 1 / sqrt(32)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kSmemLimit = 232448;  // shared memory a CTA can use
 
-// The 16 table words of a 16-slot group: rp[x] points at the word of the group's
-// first slot in its x-th box row (one row of 16, two of 8, four of 4).
+// A tile's 128 slots as four chunks of 32: the table offset of chunk c relative to
+// the tile's first slot is (c >> 1) x + (c & 1) y, and a chunk's second 16 slots lie
+// `half` further on.  kBW: the geometry's box width (boxes of a tile follow each
+// other along the columns; at kBW = 4 and M = 16 four of them fill a window row).
+template <int kBW>
+struct ChunkOffsets {
+    int x, y, half;
+    __device__ __forceinline__ ChunkOffsets(const Geo& g, int pitch) {
+        if (kBW == 64) { x = pitch; y = 32; half = 16; }
+        else if (kBW == 32) { x = 2 * pitch; y = pitch; half = 16; }
+        else if (kBW == 16) { x = 4 * pitch; y = 2 * pitch; half = pitch; }
+        else if (kBW == 8) { x = 8; y = 4 * pitch; half = 2 * pitch; }
+        else { x = g.M == 16 ? 4 * pitch : 16; y = 8; half = 4; }
+    }
+    __device__ __forceinline__ int at(int c) const { return ((c & 2) ? x : 0) + ((c & 1) ? y : 0); }
+};
+
+// The 16 table words of a 16-slot group from the word of its first slot: one box
+// row of 16, two of 8 or four of 4.  kSign: the direction in which they lie.
 template <int kBW, int kSign>
 struct BiasRows {
-    const float* rp[kBW >= 16 ? 1 : 16 / kBW];
+    static constexpr int kRows = kBW >= 16 ? 1 : 16 / kBW;
+    const float* rp[kRows];
     __device__ __forceinline__ BiasRows(const float* p, int pitch) {
 #pragma unroll
-        for (int x = 0; x < (kBW >= 16 ? 1 : 16 / kBW); ++x) rp[x] = p + kSign * x * pitch;
+        for (int x = 0; x < kRows; ++x) rp[x] = p + kSign * x * pitch;
     }
     __device__ __forceinline__ float operator[](int e) const {
-        return kBW >= 16 ? rp[0][kSign * e] : rp[e / kBW][kSign * (e % kBW)];
+        return kRows == 1 ? rp[0][kSign * e] : rp[e / kBW][kSign * (e % kBW)];
     }
 };
 
-// Table offset of the first slot of 16-slot group c of a window's tile.
-__device__ __forceinline__ int group_offset(const Geo& g, long long tile, int c, int pitch) {
+// Table offset of the first slot of a window's tile.
+__device__ __forceinline__ int tile_offset(const Geo& g, long long tile, int pitch) {
     int i, j;
-    tile_row_pos(g, tile, 16 * c, &i, &j);
+    tile_row_pos(g, tile, 0, &i, &j);
     return i * pitch + j;
 }
 
 // ------------------------------------------------------------------ forward
 namespace fwd {
 
-// Two workers a CTA, each with 256 TMEM columns: S [0, 128), P (bf16) [128, 192),
-// O [192, 224).  Warps 4 w .. 4 w + 3: worker w's softmax, thread = query row;
-// warp 8 + w issues its products, warp 10 + w its copies.  The next key tile's S
-// starts as soon as the four warps have read the present one into registers.
-constexpr int kThreads = 384;
-constexpr int kMaxStages = 4;
-constexpr uint32_t kColP = 128, kColO = 192;
+// Four workers a CTA, each with 128 TMEM columns and a key tile's chain of its own:
+// S = Q K^T, softmax, P V, O += P V.  A worker waits for itself at every link, so the
+// SM runs four such chains beside each other: with two (S and P V of neighbouring
+// tiles overlapped instead) the special function unit was a third busy.
+//   warps 4 w .. 4 w + 3: worker w's softmax, thread = query row, O in registers
+//   warp 16 + w:          its copies (TMA, two key/value tiles in flight) and products
+// TMEM: S [0, 128); P (bf16) over columns already read [0, 64), P V [64, 96).
+constexpr int kWorkers = 4;
+constexpr int kThreads = kWorkers * 128 + 128;
+constexpr uint32_t kColP = 0, kColO = 64;
 
 struct WorkerBars {
-    uint64_t q_full[2], q_free[2], kv_full[kMaxStages], kv_free[kMaxStages], s_full, s_free, p_ready, pv_done, done;
+    uint64_t q_full[2], q_free[2], kv_full[2], s_full, p_ready, pv_full, o_read, done;
 };
 struct Bars {
-    WorkerBars w[2];
+    WorkerBars w[kWorkers];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -83,7 +104,7 @@ struct Params {
     unsigned long long limit_ns;
     int streams;     // CTAs of a head
     int pitch;
-    int stages;      // key/value tiles in flight a worker
+    int q_tiles;     // query tiles a worker holds: the next item's comes in early where two fit
     int worker_bytes, tab_off, bar_off;
 };
 
@@ -98,34 +119,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Geo& g = prm.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % g.heads;
-    const int wk = warp < 8 ? warp >> 2 : warp & 1;
+    const int wk = warp < 4 * kWorkers ? warp >> 2 : warp - 4 * kWorkers;
     WorkerBars& wb = bars->w[wk];
-    const long long stride = 2ll * prm.streams;
-    const long long X0 = 2ll * (blockIdx.x / g.heads) + wk;
+    const long long stride = static_cast<long long>(kWorkers) * prm.streams;
+    const long long X0 = static_cast<long long>(kWorkers) * (blockIdx.x / g.heads) + wk;
     const long long item0 = static_cast<long long>(h) * g.tiles;
-    const int pitch = prm.pitch, stages = prm.stages;
+    const int pitch = prm.pitch, nq = prm.q_tiles;
 
     if (tid == 0) {
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < kWorkers; ++w) {
             WorkerBars& b = bars->w[w];
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&b.q_full[i], 1);
-                mbar_init(&b.q_free[i], 1);
-            }
-            for (int i = 0; i < kMaxStages; ++i) {
+                mbar_init(&b.q_free[i], 4);
                 mbar_init(&b.kv_full[i], 1);
-                mbar_init(&b.kv_free[i], 1);
             }
             mbar_init(&b.s_full, 1);
-            mbar_init(&b.s_free, 4);
             mbar_init(&b.p_ready, 4);
-            mbar_init(&b.pv_done, 1);
+            mbar_init(&b.pv_full, 1);
+            mbar_init(&b.o_read, 4);
             mbar_init(&b.done, 1);
         }
         bars->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 4 * kWorkers) {
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
     }
@@ -134,94 +152,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem_base + 256 * wk;
+    const uint32_t tmem = bars->tmem_base + 128 * wk;
     const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
-    // a worker's buffers: two Q tiles, the O staging tile, the K, V stages
+    // a worker's buffers: the Q tiles (an item's O rows are staged over its Q), two K, V stages
     uint8_t* wsm = smem + wk * prm.worker_bytes;
-    uint8_t* ost = wsm + 2 * kTileBytes;
-    uint8_t* kvs = wsm + 3 * kTileBytes;
+    uint8_t* kvs = wsm + nq * kTileBytes;
 
-    if (warp >= 10) {
-        if (lane == 0) {
-            uint32_t qi = 0, st = 0, sph = 0;
-            bool ok = true;
-            for (long long X = X0; X < g.tiles && ok; X += stride, ++qi) {
-                const FwdItem I = d_fwd_item(g, item0 + X);
-                const uint32_t b = qi & 1u;
-                if (!mbar_wait(&wb.q_free[b], ((qi >> 1) & 1u) ^ 1u, ctl, 0x7601)) break;
-                mbar_arrive_expect_tx(&wb.q_full[b], kTileBytes);
-                tile_tma(g, &mq, wsm + b * kTileBytes, &wb.q_full[b], X, h, false);
-                for (int u = 0; u < I.nkv; ++u) {
-                    if (!((I.act >> u) & 1u)) continue;
-                    if (!(ok = mbar_wait(&wb.kv_free[st], sph ^ 1u, ctl, 0x7602))) break;
-                    mbar_arrive_expect_tx(&wb.kv_full[st], 2 * kTileBytes);
-                    uint8_t* d = kvs + st * 2 * kTileBytes;
-                    tile_tma(g, &mk, d, &wb.kv_full[st], I.kv0 + u, h, false);
-                    tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[st], I.kv0 + u, h, false);
-                    if (++st == static_cast<uint32_t>(stages)) {
-                        st = 0;
-                        sph ^= 1u;
-                    }
-                }
-            }
-        }
-    } else if (warp >= 8) {
-        if (lane == 0) {
+    if (warp >= 4 * kWorkers) {
+        if (lane == 0 && X0 < g.tiles) {
             const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t id_pv = make_idesc_bf16(kTile, kHeadDim, false, true);
             const uint32_t wbase = smem_u32(wsm);
             const uint64_t dK0 = make_sdesc(wbase, 16, 512, kSw64);
             const uint64_t dMN0 = make_sdesc(wbase, 8192, 512, kSw64);
-            // the worker's key tiles of all its items in one sequence; S runs one tile
-            // ahead of P V, so at most one item ahead: their tile counts alternate
-            long long X = X0;                        // item of the next S
-            uint32_t qi = 0, left_s = 0, st_s = 0, ph_s = 0, n_s = 0;
-            uint32_t vi = 0, left_v = 0, st_v = 0, n_v = 0;
-            uint32_t count0 = 0, count1 = 0;         // key tiles of the even and of the odd items
-            auto do_s = [&]() -> bool {
-                if (left_s == 0) {
-                    left_s = __popc(d_fwd_item(g, item0 + X).act);
-                    if (qi & 1u) count1 = left_s;
-                    else count0 = left_s;
-                    if (!mbar_wait(&wb.q_full[qi & 1u], (qi >> 1) & 1u, ctl, 0x7603)) return false;
-                }
-                if (!mbar_wait(&wb.kv_full[st_s], ph_s, ctl, 0x7604)) return false;
-                if (n_s > 0 && !mbar_wait(&wb.s_free, (n_s - 1u) & 1u, ctl, 0x7605)) return false;
-                tc_fence_after();
-                const uint64_t qo = (qi & 1u) * (kTileBytes >> 4);
-                const uint64_t ko = (3 + 2 * st_s) * (kTileBytes >> 4);
-#pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) umma_ss(tmem, dK0 + qo + 2 * k, dK0 + ko + 2 * k, id_s, k > 0);
-                umma_commit(&wb.s_full);
-                if (++st_s == static_cast<uint32_t>(stages)) {
-                    st_s = 0;
-                    ph_s ^= 1u;
-                }
-                ++n_s;
-                if (--left_s == 0) {
-                    umma_commit(&wb.q_free[qi & 1u]);
-                    ++qi;
-                    X += stride;
-                }
-                return true;
+            auto load_q = [&](long long X, uint32_t b) {
+                mbar_arrive_expect_tx(&wb.q_full[b], kTileBytes);
+                tile_tma(g, &mq, wsm + b * kTileBytes, &wb.q_full[b], X, h, false);
             };
-            bool ok = X >= g.tiles || do_s();
-            while (ok && n_v < n_s) {
-                // the next S, behind the softmax of the present one
-                if ((left_s > 0 || X < g.tiles) && !do_s()) break;
-                if (!mbar_wait(&wb.p_ready, n_v & 1u, ctl, 0x7606)) break;
-                tc_fence_after();
-                const bool first = left_v == 0;
-                if (first) left_v = vi++ & 1u ? count1 : count0;
-                const uint64_t vo = (4 + 2 * st_v) * (kTileBytes >> 4);
+            long long LX = X0, Lkv0 = 0;  // the key/value tiles of all items in one sequence, two ahead
+            uint32_t Lact = 0, Lst = 0;
+            auto load_kv = [&]() {
+                if (Lact == 0) {
+                    if (LX >= g.tiles) return;
+                    const FwdItem I = d_fwd_item(g, item0 + LX);
+                    Lkv0 = I.kv0;
+                    Lact = I.act;
+                    LX += stride;
+                }
+                const int u = __ffs(Lact) - 1;
+                Lact &= Lact - 1u;
+                uint8_t* d = kvs + Lst * 2 * kTileBytes;
+                mbar_arrive_expect_tx(&wb.kv_full[Lst], 2 * kTileBytes);
+                tile_tma(g, &mk, d, &wb.kv_full[Lst], Lkv0 + u, h, false);
+                tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[Lst], Lkv0 + u, h, false);
+                Lst ^= 1u;
+            };
+            load_q(X0, 0);
+            load_kv();
+            if (nq == 2 && X0 + stride < g.tiles) load_q(X0 + stride, 1);
+            load_kv();
+            uint32_t j = 0, it = 0;
+            bool ok = true;
+            for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
+                const uint32_t qb = nq == 2 ? it & 1u : 0u;
+                const int count = __popc(d_fwd_item(g, item0 + X).act);
+                if (!mbar_wait(&wb.q_full[qb], nq == 2 ? (it >> 1) & 1u : it & 1u, ctl, 0x7601)) break;
+                const uint64_t qo = qb * (kTileBytes >> 4);
+                for (int c = 0; c < count; ++c, ++j) {
+                    const uint32_t st = j & 1u, ph = j & 1u;
+                    const uint64_t ko = (nq + 2 * st) * (kTileBytes >> 4), vo = ko + (kTileBytes >> 4);
+                    if (!(ok = mbar_wait(&wb.kv_full[st], (j >> 1) & 1u, ctl, 0x7602))) break;
+                    if (j > 0 && !(ok = mbar_wait(&wb.o_read, ph ^ 1u, ctl, 0x7603))) break;  // the last P V is read
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_ts(tmem + kColO, tmem + kColP + 8 * k, dMN0 + vo + 64 * k, id_pv, (k > 0 || !first) ? 1u : 0u);
-                umma_commit(&wb.kv_free[st_v]);
-                umma_commit(&wb.pv_done);
-                if (++st_v == static_cast<uint32_t>(stages)) st_v = 0;
-                ++n_v;
-                --left_v;
+                    for (int k = 0; k < kHeadDim / 16; ++k) umma_ss(tmem, dK0 + qo + 2 * k, dK0 + ko + 2 * k, id_s, k > 0);
+                    umma_commit(&wb.s_full);
+                    if (nq == 2 && c == 0 && it > 0 && X + stride < g.tiles) {
+                        // the item before has stored its O from there
+                        if (!(ok = mbar_wait(&wb.q_free[qb ^ 1u], ((it - 1u) >> 1) & 1u, ctl, 0x7604))) break;
+                        load_q(X + stride, qb ^ 1u);
+                    }
+                    if (!(ok = mbar_wait(&wb.p_ready, ph, ctl, 0x7605))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_ts(tmem + kColO, tmem + kColP + 8 * k, dMN0 + vo + 64 * k, id_pv, k > 0);
+                    umma_commit(&wb.pv_full);
+                    if (!(ok = mbar_wait(&wb.pv_full, ph, ctl, 0x7606))) break;  // the stage is free
+                    load_kv();
+                }
+                if (ok && nq == 1 && X + stride < g.tiles) {
+                    if (!mbar_wait(&wb.q_free[0], it & 1u, ctl, 0x7607)) break;
+                    load_q(X + stride, 0);
+                }
             }
             umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
             mbar_wait(&wb.done, 0, ctl, 0x76ff);
@@ -233,9 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
-        uint32_t n = 0;  // key tiles seen
+        const ChunkOffsets<kBW> co(g, pitch);
+        uint32_t n = 0, it = 0;  // key tiles and items seen
         bool ok = true;
-        for (long long X = X0; X < g.tiles && ok; X += stride) {
+        for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
             const FwdItem I = d_fwd_item(g, item0 + X);
             int pi, pj;
             long long tok;
@@ -243,122 +247,107 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* brow = tab + (pi + g.M - 1) * pitch + pj + g.M - 1;
             const uint32_t myseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
             float m = -INFINITY, l = 0.f;
-            bool first = true;
-            for (int u = 0; u < I.nkv && ok; ++u) {
-                if (!((I.act >> u) & 1u)) continue;
-                const long long kt = I.kv0 + u;
-                const uint32_t a16 = I.masked ? d_allow16(g, myseg, kt, I.win) : 0xFFu;
-                if (!wwait(&wb.s_full, n & 1u, 0x7607)) { ok = false; break; }
-                tc_fence_after();
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
-                bool waited = n == 0;
-                uint32_t v[2][32];
-                tmem_ld32(trow, v[0]);
+            float o[32];
 #pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++n) {
+                const long long kt = I.kv0 + __ffs(act) - 1;
+                const uint32_t a16 = I.masked ? d_allow16(g, myseg, kt, I.win) : 0xFFu;
+                if (!wwait(&wb.s_full, n & 1u, 0x7608)) { ok = false; break; }
+                tc_fence_after();
+                float l2[2] = {0.f, 0.f};
+                const float* btile = brow - tile_offset(g, kt, pitch);
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld();
-                    if (c < 3) {
-                        tmem_ld32(trow + 32 * (c + 1), v[(c + 1) & 1]);
-                    } else {  // S is in registers: the next one may start
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&wb.s_free);
-                    }
+                    uint32_t v[32];
+                    tmem_ld32(trow + 32 * c, v);
+                    const BiasRows<kBW, -1> b0(btile - co.at(c), pitch), b1(btile - co.at(c) - co.half, pitch);
                     float t[32];
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const BiasRows<kBW, -1> b(brow - group_offset(g, kt, 2 * c + hh, pitch), pitch);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const int a = 16 * hh + e;
-                            ffma2(t[a], t[a + 1], __uint_as_float(v[c & 1][a]), __uint_as_float(v[c & 1][a + 1]), sl2, sl2,
-                                  b[e], b[e + 1]);
-                        }
+                    for (int e = 0; e < 16; ++e) {
+                        t[e] = b0[e];
+                        t[16 + e] = b1[e];
                     }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        ffma2(t[e], t[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2, t[e], t[e + 1]);
                     if (I.masked) {
+                        const bool on0 = (a16 >> (2 * c)) & 1u, on1 = (a16 >> (2 * c + 1)) & 1u;
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh)
-                            if (!((a16 >> (2 * c + hh)) & 1u)) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) t[16 * hh + e] = -INFINITY;
-                            }
+                        for (int e = 0; e < 16; ++e) {
+                            t[e] = on0 ? t[e] : -INFINITY;
+                            t[16 + e] = on1 ? t[16 + e] : -INFINITY;
+                        }
                     }
                     // The running maximum only moves when a chunk exceeds it by more than
                     // 2^64: probabilities up to 2^64 stay far inside bf16's and fp32's range,
                     // and the final division uses the same maximum as the sum.
-                    float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float c2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) c4[(e >> 1) & 3] = fmax3(c4[(e >> 1) & 3], t[e], t[e + 1]);
-                    const float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+                    for (int e = 0; e < 32; e += 2) c2[(e >> 1) & 1] = fmax3(c2[(e >> 1) & 1], t[e], t[e + 1]);
+                    const float cm = fmaxf(c2[0], c2[1]);
                     const bool grow = cm > m + 64.f;
-                    if (!waited) {  // P and O: the previous tile's product is done with them
-                        if (!wwait(&wb.pv_done, (n - 1u) & 1u, 0x7608)) { ok = false; break; }
-                        tc_fence_after();
-                        waited = true;
-                    }
                     if (__any_sync(0xFFFFFFFFu, grow)) {
                         const float alpha = grow ? ex2_approx(m - cm) : 1.f;
                         if (grow) m = cm;
                         l *= alpha;
+                        l2[0] *= alpha;
+                        l2[1] *= alpha;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) l4[e] *= alpha;
-                        if (!first) {
-#pragma unroll 1
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t ov[16];
-                                tmem_ld16(trow + kColO + 16 * k, ov);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                tmem_st16(trow + kColO + 16 * k, ov);
-                            }
-                        }
+                        for (int e = 0; e < 32; e += 2) fmul2(o[e], o[e + 1], o[e], o[e + 1], alpha, alpha);
                         tmem_wait_st();
 #pragma unroll 1
-                        for (int k = 0; k < c; ++k) {  // this tile's chunks already written
-                            uint32_t pw[16];
-                            tmem_ld16(trow + kColP + 16 * k, pw);
+                        for (int k = 0; k < 2 * c; ++k) {  // this tile's chunks already written
+                            uint32_t pw[8];
+                            tmem_ld8(trow + kColP + 8 * k, pw);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
+                            for (int e = 0; e < 8; ++e)
                                 pw[e] = pack_bf16x2(bf16lo_to_f32(pw[e]) * alpha, bf16hi_to_f32(pw[e]) * alpha);
-                            tmem_st16(trow + kColP + 16 * k, pw);
+                            tmem_st8(trow + kColP + 8 * k, pw);
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : m;  // no key so far: P = 0
-                    uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float t0, t1;
-                        fadd2(t0, t1, t[2 * e], t[2 * e + 1], -mu, -mu);
-                        const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                        const int a = (e & 1) * 2;
-                        fadd2(l4[a], l4[a + 1], l4[a], l4[a + 1], p0, p1);
-                        w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int a = 16 * hh + 2 * e;
+                            float t0, t1;
+                            fadd2(t0, t1, t[a], t[a + 1], -mu, -mu);
+                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                            fadd2(l2[0], l2[1], l2[0], l2[1], p0, p1);
+                            w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
+                        }
+                        tmem_st8(trow + kColP + 16 * c + 8 * hh, w);  // over columns of S already read
                     }
-                    tmem_st16(trow + kColP + 16 * c, w);
                 }
-                if (!ok) break;
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l += l2[0] + l2[1];
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&wb.p_ready);
-                first = false;
-                ++n;
-            }
-            if (!ok || first) break;
-            if (!wwait(&wb.pv_done, (n - 1u) & 1u, 0x7609)) break;
-            tc_fence_after();
-            uint32_t ov[32];
-            tmem_ld32(trow + kColO, ov);
-            tmem_wait_ld();
-            tc_fence_before();  // ordered before the next item's product by its p_ready
-            const float inv = 1.f / l;
-            float x[32];
+                if (!wwait(&wb.pv_full, n & 1u, 0x7609)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t v[32];
+                tmem_ld32(trow + kColO, v);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wb.o_read);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(ov[e]) * inv;  // no key: O = 0
-            store_row_swz(ost, r, x);
+                for (int e = 0; e < 32; e += 2)
+                    fadd2(o[e], o[e + 1], o[e], o[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            }
+            if (!ok) break;
+            const float inv = 1.f / l;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;  // no key: O = 0
+            const uint32_t qb = nq == 2 ? it & 1u : 0u;
+            uint8_t* ost = wsm + qb * kTileBytes;
+            store_row_swz(ost, r, o);
             if (valid && prm.lse != nullptr) prm.lse[tok] = (m + lg2_approx(l)) * kLn2;
             __syncwarp();
 #pragma unroll
@@ -371,13 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4*>(prm.o + tk * kRowBytes + 16 * c) =
                         *reinterpret_cast<const uint4*>(ost + row * kRowBytes + ((c ^ ((row >> 1) & 3)) << 4));
             }
+            fence_proxy_async_smem();  // the rows are read before TMA writes the next Q over them
             __syncwarp();
+            if (lane == 0) mbar_arrive(&wb.q_free[qb]);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(bars->tmem_base, 512);
+    if (warp == 4 * kWorkers) tmem_dealloc(bars->tmem_base, 512);
 }
 
 }  // namespace fwd
@@ -464,20 +455,27 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Param
     p.rowv[ht * kTile + r] = make_float2(lse2, D);
 }
 
-// Main kernel: a worker is four warps (thread = key row, and query row of dQ)
-// with 256 TMEM columns, its own buffers and barriers.  Item = (key tile, head):
-// the query tiles of its window in turn.  Per step
+// Main kernel: a worker is eight warps with 256 TMEM columns, its own buffers and
+// barriers; two warpgroups split a step's query columns, thread = key row (and query
+// row of dQ).  Item = (key tile, head): the query tiles of its window in turn.  A step
 //   S^T = K Q^T, dP^T = V dO^T; P^T and dS^T (bf16, the products' operand type) over
-//   consumed columns, dS also to shared memory; dV = P^T dO, dK = dS^T Q, dQ = dS K;
-// dV and dK add up in registers, dQ is staged over the step's Q and dO tiles and
-// added into the fp32 accumulator tile with one bulk reduction.  While those three
-// products run, the warps sum dS over equal displacements (add_diagonals).  Two
-// workers a CTA fill each other's waits.  TMEM columns:
-constexpr uint32_t kColS = 0, kColDP = 128, kColP = 0, kColDS = 128, kColDV = 64, kColDQ = 96, kColDK = 192;
+//   columns that the warpgroup has read, dS also to shared memory; dV = P^T dO,
+//   dK = dS^T Q, dQ = dS K
+// adds dV (first warpgroup) and dK (second) up in registers; dQ is staged over the
+// step's Q and dO tiles and added into the fp32 accumulator tile with one bulk
+// reduction.  While the three products run, one warpgroup (they take turns) sums dS
+// over equal displacements.  Two workers a CTA fill each other's waits; a warpgroup of
+// its own copies (warps 2, 3) and issues the products (warps 0, 1): issued by a
+// computing thread, the copies cost its warp 2.7 thousand cycles a step and the
+// products 1.7, for which the other warps then waited.
+// TMEM columns: S^T [0,128), dP^T [128,256).  P^T of the first warpgroup [0,32), of the
+// second [64,96); dS^T [128,160) and [192,224); dV [32,64), dQ [96,128), dK [160,192).
+constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 32, kColDQ = 96, kColDK = 160;
 constexpr int kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, and the rows' (lse2, D)
 
 struct WorkerBars {
-    uint64_t kv_full[2], st_full[2], s_full, mma_done, grp, done;
+    // dq_ready per stage: the copies may lag a step behind the next one's dQ
+    uint64_t kv_full[2], st_full[2], s_full, p_ready, mma_done, dq_ready[2], done;
 };
 struct Bars {
     WorkerBars w[2];
@@ -498,88 +496,124 @@ __host__ __device__ constexpr int sums_off(int kv_stages) { return stage_off(kv_
 // touch one sum and every sum has a fixed order.  Lane (g, kp, m) walks block g's
 // keys 4 kk + kp and query quads kk + m (mod w / 4): eight bytes a load, and its
 // four columns e belong to displacement 4 m + e - kp, or w less once the quads wrap.
+// Blocks of equal displacement follow each other and add up in registers first.
 template <int kBW>  // 4, 8, 16, 32, 64: the geometry's box width
 struct Diag {
     static constexpr int w = kBW < 32 ? kBW : 32;
     static constexpr int quads = w / 4;
     static constexpr int conc = 32 / w;         // blocks a warp walks at once
     static constexpr int nseg = kTile / w;
+    float A[4], B[4];  // before and after the quads wrap
 
-    // key and query tile of the step, by their window positions of segment 0's row
-    static __device__ __forceinline__ void block(const Geo& g, uint32_t ds, float* sums, long long ku, long long qt,
-                                                 int a, int b, int kp, int m, int side) {
-        float A[4] = {0.f, 0.f, 0.f, 0.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-        const int q0 = b * w;
-        const uint32_t qbase = ds + ((q0 >> 6) << 14);
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[e] = B[e] = 0.f;
+    }
+    // Shared address of the lane's first load of a key segment's rows: key kp, query
+    // column 0; and the lane's offsets from there for every kk (the swizzle of key row
+    // r: 16-byte chunk index xor r & 7).
+    __device__ __forceinline__ void walk(uint32_t rows, const uint32_t (&off)[quads], uint32_t flip, int m) {
 #pragma unroll
         for (int kk = 0; kk < quads; ++kk) {
-            const int r = a * w + 4 * kk + kp;
-            const int p = kk + m;
-            const int col = (q0 & 63) + 4 * (p & (quads - 1));  // first of four query columns inside the 64-column half
-            const uint32_t addr = qbase + ((r >> 3) << 10) + ((r & 7) << 7) + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 4) << 1));
             uint32_t x, y;
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(addr));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(rows + (off[kk] ^ flip)));
             const float v[4] = {bf16lo_to_f32(x), bf16hi_to_f32(x), bf16lo_to_f32(y), bf16hi_to_f32(y)};
-            const bool wrap = p >= quads;
-            const float fa = wrap ? 0.f : 1.f, fb = wrap ? 1.f : 0.f;
+            const float fb = kk + m >= quads ? 1.f : 0.f, fa = 1.f - fb;
             ffma2(A[0], A[1], v[0], v[1], fa, fa, A[0], A[1]);
             ffma2(A[2], A[3], v[2], v[3], fa, fa, A[2], A[3]);
-            ffma2(B[0], B[1], v[0], v[1], fb, fb, B[0], B[1]);
-            ffma2(B[2], B[3], v[2], v[3], fb, fb, B[2], B[3]);
+            if (quads > 1) {
+                ffma2(B[0], B[1], v[0], v[1], fb, fb, B[0], B[1]);
+                ffma2(B[2], B[3], v[2], v[3], fb, fb, B[2], B[3]);
+            }
         }
-        int ia, ja, ib, jb;
-        tile_row_pos(g, ku, a * w, &ia, &ja);
-        tile_row_pos(g, qt, q0, &ib, &jb);
-        float* dst = sums + (ib - ia + g.M - 1) * side + (jb - ja + g.M - 1) + 4 * m - kp;
-        // lanes of one block hold distinct displacements for one e, and so do the
-        // blocks walked at once; the wrapped ones of a neighbour may coincide, so
-        // they follow in a step of their own
+    }
+    // dst: the sum of displacement 4 m - kp of this lane's block.  Lanes of one block
+    // hold distinct displacements for one e, and so do the blocks walked at once; the
+    // wrapped ones of a neighbouring block may coincide with those, so they follow in
+    // a step of their own.
+    __device__ __forceinline__ void flush(float* dst, int m) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             dst[e] += A[e];
-            __syncwarp();
-            if (m > 0) dst[e - w] += B[e];
+            if (conc > 1) __syncwarp();
+            if (quads > 1 && m > 0) dst[e - w] += B[e];
             __syncwarp();
         }
+        clear();
     }
 
     static __device__ __forceinline__ void step(const Geo& g, uint32_t ds, float* sums, long long ku, long long qt,
                                                 int quad, int lane, int side) {
         const int kp = lane & 3, m = (lane >> 2) & (quads - 1), gi = lane / (4 * quads);
+        uint32_t off[quads];
+#pragma unroll
+        for (int kk = 0; kk < quads; ++kk) {
+            const uint32_t r = 4 * kk + kp, p = (kk + m) & (quads - 1);
+            off[kk] = ((r >> 3) << 10) + ((r & 7) << 7) + ((((p >> 1) ^ (r & 7)) << 4) | ((p & 1) << 3));
+        }
+        // window positions of the tiles' first slots; a segment's from there
+        int ki0, kj0, qi0, qj0;
+        tile_row_pos(g, ku, 0, &ki0, &kj0);
+        tile_row_pos(g, qt, 0, &qi0, &qj0);
+        float* origin = sums + (qi0 - ki0 + g.M - 1) * side + (qj0 - kj0 + g.M - 1) + 4 * m - kp;
+        Diag d;
+        d.clear();
+        int last = 0;
+        bool some = false;
+        auto block = [&](int a, int b, int di, int dj) {  // di, dj: of the segments, relative to the tiles
+            const int at = di * side + dj;
+            // the blocks walked at once move on together
+            if (some && __any_sync(0xFFFFFFFFu, at != last)) d.flush(origin + last, m);
+            last = at;
+            some = true;
+            const int q0 = b * w;
+            // key rows a w ..: whole eight-row groups, or (w = 4) half of one, whose rows
+            // 4 .. 7 have the swizzle's bit 2 set
+            const uint32_t rows = ds + ((q0 >> 6) << 14) + (((a * w) >> 3) << 10) + (w == 4 ? ((a & 1) << 9) : 0);
+            const uint32_t flip = (((q0 & 63) >> 3) ^ (w == 4 ? ((a & 1) << 2) : 0)) << 4 | (w == 4 ? ((q0 & 4) << 1) : 0);
+            d.walk(rows, off, flip, m);
+        };
         if (kBW == 64) {  // two rows of two 32-column segments
-            const int ra0 = static_cast<int>(ku & (g.tpw - 1)) * 2, rb0 = static_cast<int>(qt & (g.tpw - 1)) * 2;
 #pragma unroll 1
-            for (int ab = 0; ab < 16; ++ab) {
-                const int a = ab >> 2, b = ab & 3;
-                if (((rb0 + (b >> 1) - ra0 - (a >> 1)) & 3) != quad) continue;
-                block(g, ds, sums, ku, qt, a, b, kp, m, side);
+            for (int ab = 0; ab < 16; ++ab) {  // key row, query row, halves: equal displacements in a row
+                const int ra = ab >> 3, rb = (ab >> 2) & 1, ha = (ab >> 1) & 1, hb = ab & 1;
+                if (((qi0 - ki0 + rb - ra) & 3) != quad) continue;
+                block(2 * ra + ha, 2 * rb + hb, rb - ra, 32 * (hb - ha));
             }
-            return;
-        }
-        // Boxes of bh rows (a multiple of 4, at multiples of 4): segment = box * bh + row
-        constexpr int bh = kBW == 32 ? 4 : (kBW == 16 ? 8 : kBW);
-        constexpr int per = bh / 4;  // matching rows a box
+        } else {
+            // boxes of bh rows (a multiple of 4, at multiples of 4): segment = box bh + row;
+            // boxes of a tile along the columns, but at kBW = 4, M = 16 two rows of four
+            constexpr int bh = kBW == 32 ? 4 : (kBW == 16 ? 8 : kBW);
+            constexpr int per = bh / 4;  // matching rows a box
+            const int wrapped = kBW == 4 && g.M == 16;
+            const int xb = gi / per;
+            const int bi = wrapped ? (xb >> 2) * 4 : 0, bj = (wrapped ? xb & 3 : xb) * kBW;
 #pragma unroll 1
-        for (int a = 0; a < nseg; ++a) {
-            const int row = ((a & (bh - 1)) + quad) & 3;
-            const int b = (gi / per) * bh + row + 4 * (gi % per);
-            block(g, ds, sums, ku, qt, a, b, kp, m, side);
+            for (int a = 0; a < nseg; ++a) {
+                const int xa = a / bh, ra = a & (bh - 1);
+                const int rb = ((ra + quad) & 3) + 4 * (gi % per);
+                const int ai = wrapped ? (xa >> 2) * 4 : 0, aj = (wrapped ? xa & 3 : xa) * kBW;
+                block(a, xb * bh + rb, bi + rb - ai - ra, bj - aj);
+            }
         }
+        if (some) d.flush(origin + last, m);
     }
 };
 
 template <int kBW, int kWorkers>
-__global__ void __launch_bounds__(128 * kWorkers, 1)
+__global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     main_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                 const __grid_constant__ Params prm) {
+    constexpr int kThreads = 256 * kWorkers + 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars* bars = reinterpret_cast<Bars*>(smem + prm.bar_off);
     float* tab = reinterpret_cast<float*>(smem + prm.tab_off);
     const Geo& g = prm.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wk = warp >> 2, quad = warp & 3, r = tid & (kTile - 1);
+    const bool computes = warp < 8 * kWorkers;
+    const int wk = computes ? warp >> 3 : warp & 1;  // (one worker: its second helpers have no item)
     const int h = blockIdx.x % g.heads;
     WorkerBars& wb = bars->w[wk];
     const int pitch = prm.pitch, side = 2 * g.M - 1, kvs = prm.kv_stages;
@@ -595,242 +629,250 @@ __global__ void __launch_bounds__(128 * kWorkers, 1)
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&b.kv_full[i], 1);
                 mbar_init(&b.st_full[i], 1);
+                mbar_init(&b.dq_ready[i], 8);
             }
             mbar_init(&b.s_full, 1);
+            mbar_init(&b.p_ready, 8);
             mbar_init(&b.mma_done, 1);
-            mbar_init(&b.grp, 4);
             mbar_init(&b.done, 1);
         }
         bars->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0) {
+    if (warp == 8 * kWorkers) {
         tmem_alloc(&bars->tmem_base, 256 * kWorkers);
         tmem_relinquish();
     }
     build_bias(tab, pitch, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, g.M, tid,
-               128 * kWorkers);
-    for (int e = r; e < side * side; e += kTile) sums[e] = 0.f;
+               kThreads);
+    if (computes)
+        for (int e = tid & 255; e < side * side; e += 256) sums[e] = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base + 256 * wk;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
-    const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
-    const uint32_t id_dv = make_idesc_bf16(kTile, kHeadDim, false, true);
-    const uint32_t id_dq = make_idesc_bf16(kTile, kHeadDim, true, true);
-    const uint32_t wbase = smem_u32(wsm);
-    const uint64_t dK0 = make_sdesc(wbase, 16, 512, kSw64);
-    const uint64_t dMN0 = make_sdesc(wbase, 8192, 512, kSw64);
-    const uint64_t dDS = make_sdesc(wbase, 16384, 1024, kSw128);
-    const float sl2 = g.scale_log2;
     const int st0 = stage_off(kvs);
-    uint32_t gph = 0;
-    auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
-        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
-    };
-    auto group_sync = [&](unsigned int where) -> bool {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wb.grp);
-        const bool passed = wwait(&wb.grp, gph, where);
-        gph ^= 1u;
-        return passed;
-    };
 
-    // The copying thread (lane 0 of the worker's second warp) runs one step ahead.
-    const bool loader = quad == 1 && lane == 0;
-    long long LX = X0;      // item of the next step to load
-    long long Lq0 = 0;
-    uint32_t Lact = 0, Lst = 0;
-    auto load_kv = [&](long long X, int b) {
-        uint8_t* d = wsm + kKVOff + b * 2 * kTileBytes;
-        mbar_arrive_expect_tx(&wb.kv_full[b], 2 * kTileBytes);
-        tile_tma(g, &mk, d, &wb.kv_full[b], X, h, false);
-        tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[b], X, h, false);
-    };
-    auto load_step = [&]() {
-        if (Lact == 0) {
-            if (LX >= g.tiles) return;
-            const BwdItem I = d_bwd_item(g, item0 + LX);
-            Lq0 = I.q0;
-            Lact = I.act;
-            LX += stride;
-            if (Lact == 0) return;
-        }
-        const int n = __ffs(Lact) - 1;
-        Lact &= Lact - 1u;
-        const long long T = Lq0 + n;
-        uint8_t* d = wsm + st0 + Lst * kStageBytes;
-        uint64_t* bar = &wb.st_full[Lst];
-        mbar_arrive_expect_tx(bar, kStageBytes);
-        tile_tma(g, &mq, d, bar, T, h, false);
-        tile_tma(g, &mdo, d + kTileBytes, bar, T, h, false);
-        bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * kTile, 1024, bar);
-        Lst ^= 1u;
-    };
-    if (loader && X0 < g.tiles) {
-        load_kv(X0, 0);
-        load_step();
-        load_step();
-    }
-    __syncwarp();
-
-    uint32_t step = 0, item = 0;
-    bool ok = true;
-    for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
-        const BwdItem I = d_bwd_item(g, item0 + X);
-        const int kvb = kvs == 2 ? static_cast<int>(item & 1u) : 0;
-        const uint32_t kvph = kvs == 2 ? (item >> 1) & 1u : item & 1u;
-        // the other buffer's item is finished: the next item's keys and values
-        if (loader && kvs == 2 && X + stride < g.tiles) load_kv(X + stride, kvb ^ 1);
-        int ki, kj;
-        long long ktok;
-        const bool kvalid = slot_token(g, X, r, h, &ki, &kj, &ktok);
-        const float* brow = tab + (g.M - 1 - ki) * pitch + g.M - 1 - kj;
-        const uint32_t keyseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
-        float dv[32], dk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) dv[e] = dk[e] = 0.f;
-        const uint64_t ko = (kKVOff + kvb * 2 * kTileBytes) >> 4, vo = ko + (kTileBytes >> 4);
-        bool first = true;
-        for (int n = 0; n < I.nq && ok; ++n) {
-            if (!bwd_active(g, I, n)) continue;
-            const long long T = I.q0 + n;
-            const uint32_t b = step & 1u, ph = step & 1u;
-            uint8_t* stg = wsm + st0 + b * kStageBytes;
-            const uint64_t qo = static_cast<uint64_t>((st0 + b * kStageBytes) >> 4), dof = qo + (kTileBytes >> 4);
-            if (first && !wwait(&wb.kv_full[kvb], kvph, 0x7501)) { ok = false; break; }
-            first = false;
-            if (!wwait(&wb.st_full[b], (step >> 1) & 1u, 0x7502)) { ok = false; break; }
-            if (r == 0) {
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) {
-                    umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
-                    umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+    if (!computes) {
+        const int role = (warp - 8 * kWorkers) >> 1;  // 0: products, 1: copies
+        if (lane == 0 && wk < kWorkers && X0 < g.tiles && role == 1) {
+            // the query tiles of all items in one sequence, two steps ahead
+            long long LX = X0, Lq0 = 0, Tst0 = 0, Tst1 = 0;
+            uint32_t Lact = 0, Lst = 0;
+            auto load_kv = [&](long long X, uint32_t b) {
+                uint8_t* d = wsm + kKVOff + b * 2 * kTileBytes;
+                mbar_arrive_expect_tx(&wb.kv_full[b], 2 * kTileBytes);
+                tile_tma(g, &mk, d, &wb.kv_full[b], X, h, false);
+                tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[b], X, h, false);
+            };
+            auto load_step = [&]() {
+                if (Lact == 0) {
+                    if (LX >= g.tiles) return;
+                    const BwdItem I = d_bwd_item(g, item0 + LX);
+                    Lq0 = I.q0;
+                    Lact = I.act;
+                    LX += stride;
                 }
-                umma_commit(&wb.s_full);
+                const long long T = Lq0 + __ffs(Lact) - 1;
+                Lact &= Lact - 1u;
+                uint8_t* d = wsm + st0 + Lst * kStageBytes;
+                uint64_t* bar = &wb.st_full[Lst];
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                tile_tma(g, &mq, d, bar, T, h, false);
+                tile_tma(g, &mdo, d + kTileBytes, bar, T, h, false);
+                bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * kTile, 1024, bar);
+                if (Lst) Tst1 = T;
+                else Tst0 = T;
+                Lst ^= 1u;
+            };
+            load_kv(X0, 0);
+            load_step();
+            load_step();
+            if (kvs == 2 && X0 + stride < g.tiles) load_kv(X0 + stride, 1);
+            uint32_t step = 0, item = 0;
+            bool ok = true;
+            for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
+                const int count = __popc(d_bwd_item(g, item0 + X).act);
+                for (int c = 0; c < count; ++c, ++step) {
+                    if (!(ok = mbar_wait(&wb.dq_ready[step & 1u], (step >> 1) & 1u, ctl, 0x7501))) break;
+                    uint8_t* d = wsm + st0 + (step & 1u) * kStageBytes;
+                    bulk_reduce_add_f32(prm.acc + (item0 + ((step & 1u) ? Tst1 : Tst0)) * kTile * kHeadDim, d, 2 * kTileBytes);
+                    bulk_commit();
+                    // the item's products are done with its keys and values
+                    if (c == count - 1 && X + kvs * stride < g.tiles) load_kv(X + kvs * stride, kvs == 2 ? item & 1u : 0u);
+                    bulk_wait_read_all();
+                    load_step();
+                }
             }
-            if (loader && step > 0) {  // the other stage: its reduction has left it, the next step's rows come in
-                bulk_wait_read_all();
-                load_step();
-            }
-            const uint32_t a16 = I.masked ? d_allow16(g, keyseg, T, I.win) : 0xFFu;
-            const float4* vec = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // (lse2, D) of two queries
-            if (!wwait(&wb.s_full, ph, 0x7503)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint8_t* base = wsm + (c >> 1) * 16384 + (r >> 3) * 1024 + (r & 7) * 128;
-                uint32_t sv[32], pv[32];
-                tmem_ld32(trow + kColS + 32 * c, sv);
-                tmem_ld32(trow + kColDP + 32 * c, pv);
-                tmem_wait_ld();
-                uint32_t wp[16], wd[16];
+            bulk_wait_all();
+        } else if (lane == 0 && wk < kWorkers && X0 < g.tiles) {
+            const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+            const uint32_t id_dv = make_idesc_bf16(kTile, kHeadDim, false, true);
+            const uint32_t id_dq = make_idesc_bf16(kTile, kHeadDim, true, true);
+            const uint32_t wbase = smem_u32(wsm);
+            const uint64_t dK0 = make_sdesc(wbase, 16, 512, kSw64);
+            const uint64_t dMN0 = make_sdesc(wbase, 8192, 512, kSw64);
+            const uint64_t dDS = make_sdesc(wbase, 16384, 1024, kSw128);
+            uint32_t step = 0, item = 0;
+            bool ok = true;
+            for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
+                const int count = __popc(d_bwd_item(g, item0 + X).act);
+                const uint32_t kvb = kvs == 2 ? item & 1u : 0u;
+                const uint64_t ko = (kKVOff + kvb * 2 * kTileBytes) >> 4, vo = ko + (kTileBytes >> 4);
+                if (!mbar_wait(&wb.kv_full[kvb], kvs == 2 ? (item >> 1) & 1u : item & 1u, ctl, 0x7502)) break;
+                for (int c = 0; c < count; ++c, ++step) {
+                    const uint32_t b = step & 1u;
+                    const uint64_t qo = static_cast<uint64_t>((st0 + b * kStageBytes) >> 4), dof = qo + (kTileBytes >> 4);
+                    if (!(ok = mbar_wait(&wb.st_full[b], (step >> 1) & 1u, ctl, 0x7503))) break;
+                    if (step > 0 && !(ok = mbar_wait(&wb.dq_ready[b ^ 1u], ((step - 1u) >> 1) & 1u, ctl, 0x7504))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const BiasRows<(kBW > 16 ? 16 : kBW), 1> bias(brow + group_offset(g, T, 2 * c + hh, pitch), pitch);
-                    const bool on = (a16 >> (2 * c + hh)) & 1u;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int a = 16 * hh + e;
-                        const float4 LD = vec[16 * c + a / 2];
-                        float t0, t1, d0, d1;
-                        fadd2(t0, t1, bias[e], bias[e + 1], -LD.x, -LD.z);
-                        ffma2(t0, t1, __uint_as_float(sv[a]), __uint_as_float(sv[a + 1]), sl2, sl2, t0, t1);
-                        float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                        fadd2(d0, d1, __uint_as_float(pv[a]), __uint_as_float(pv[a + 1]), -LD.y, -LD.w);
-                        fmul2(d0, d1, d0, d1, p0, p1);
-                        if (!on) p0 = p1 = d0 = d1 = 0.f;
-                        wp[a / 2] = pack_bf16x2(p0, p1);
-                        wd[a / 2] = pack_bf16x2(d0, d1);
+                    for (int k = 0; k < kHeadDim / 16; ++k) {
+                        umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
+                        umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
                     }
-                }
-                tmem_st16(trow + kColP + 16 * c, wp);
-                tmem_st16(trow + kColDS + 16 * c, wd);
+                    umma_commit(&wb.s_full);
+                    if (!(ok = mbar_wait(&wb.p_ready, b, ctl, 0x7505))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const int cc = 4 * (c & 1) + q4;
-                    *reinterpret_cast<uint4*>(base + ((cc ^ (r & 7)) << 4)) =
-                        make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_ts(tmem + kColDV, tmem + kColS + 8 * k + (k < 4 ? 0 : 32), dMN0 + dof + 64 * k, id_dv, k > 0);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_ts(tmem + kColDK, tmem + kColDP + 8 * k + (k < 4 ? 0 : 32), dMN0 + qo + 64 * k, id_dv, k > 0);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_ss(tmem + kColDQ, dDS + 128 * k, dMN0 + ko + 64 * k, id_dq, k > 0);
+                    umma_commit(&wb.mma_done);
                 }
             }
-            tmem_wait_st();
-            fence_proxy_async_smem();
-            tc_fence_before();
-            if (!group_sync(0x7504)) { ok = false; break; }  // every row's P^T, dS^T and dS written
-            if (r == 0) {
+            umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
+            mbar_wait(&wb.done, 0, ctl, 0x75ff);
+        }
+    } else {
+        const int wg = (warp >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const float sl2 = g.scale_log2;
+        const ChunkOffsets<kBW> co(g, pitch);
+        auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
+            return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
+        };
+        uint8_t* dsrow = wsm + wg * 16384 + (r >> 3) * 1024 + (r & 7) * 128;
+        const uint32_t wbase = smem_u32(wsm);
+        uint32_t step = 0;
+        bool ok = true;
+        for (long long X = X0; X < g.tiles && ok; X += stride) {
+            const BwdItem I = d_bwd_item(g, item0 + X);
+            int ki, kj;
+            long long ktok;
+            const bool kvalid = slot_token(g, X, r, h, &ki, &kj, &ktok);
+            const float* brow = tab + (g.M - 1 - ki) * pitch + g.M - 1 - kj;
+            const uint32_t keyseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
+            float acc[32];  // dV (first warpgroup) or dK (second) of this key row
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+            for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++step) {
+                const long long T = I.q0 + __ffs(act) - 1;
+                const uint32_t ph = step & 1u;
+                uint8_t* stg = wsm + st0 + ph * kStageBytes;
+                const uint32_t a16 = I.masked ? d_allow16(g, keyseg, T, I.win) : 0xFFu;
+                const float* bt = brow + tile_offset(g, T, pitch);
+                const float4* vec = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // (lse2, D) of two queries
+                if (!wwait(&wb.st_full[ph], (step >> 1) & 1u, 0x7506) || !wwait(&wb.s_full, ph, 0x7507)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
+#pragma unroll 1
+                for (int hc = 0; hc < 4; ++hc) {  // 16 queries: one piece of box rows, one region
+                    const int c16 = 4 * wg + hc;
+                    uint32_t sv[16], pv[16];
+                    tmem_ld16(trow + kColS + 16 * c16, sv);
+                    tmem_ld16(trow + kColDP + 16 * c16, pv);
+                    const BiasRows<kBW, 1> bias(bt + co.at(c16 >> 1) + ((c16 & 1) ? co.half : 0), pitch);
+                    uint32_t wp[8], wd[8];
+                    float t[16];
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_ts(tmem + kColDV, tmem + kColP + 8 * k, dMN0 + dof + 64 * k, id_dv, k > 0);
+                    for (int e = 0; e < 16; ++e) t[e] = bias[e];
+                    tmem_wait_ld();
+                    if ((a16 >> c16) & 1u) {
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_ts(tmem + kColDK, tmem + kColDS + 8 * k, dMN0 + qo + 64 * k, id_dv, k > 0);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 LD = vec[8 * c16 + e / 2];
+                            float t0, t1, d0, d1;
+                            ffma2(t0, t1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, sl2, t[e], t[e + 1]);
+                            fadd2(t0, t1, t0, t1, -LD.x, -LD.z);
+                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                            fadd2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), -LD.y, -LD.w);
+                            fmul2(d0, d1, d0, d1, p0, p1);
+                            wp[e / 2] = pack_bf16x2(p0, p1);
+                            wd[e / 2] = pack_bf16x2(d0, d1);
+                        }
+                    } else {
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_ss(tmem + kColDQ, dDS + 128 * k, dMN0 + ko + 64 * k, id_dq, k > 0);
-                umma_commit(&wb.mma_done);
+                        for (int e = 0; e < 8; ++e) wp[e] = wd[e] = 0u;
+                    }
+                    __syncwarp();
+                    tmem_st8(trow + kColS + 64 * wg + 8 * hc, wp);
+                    tmem_st8(trow + kColDP + 64 * wg + 8 * hc, wd);
+#pragma unroll
+                    for (int q4 = 0; q4 < 2; ++q4)
+                        *reinterpret_cast<uint4*>(dsrow + (((2 * hc + q4) ^ (r & 7)) << 4)) =
+                            make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
+                }
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wb.p_ready);
+                if (static_cast<int>(ph) == wg) {
+                    if (!wwait(&wb.p_ready, ph, 0x7508)) { ok = false; break; }  // every row's dS is written
+                    Diag<kBW>::step(g, wbase, sums, X, T, quad, lane, side);
+                }
+                if (!wwait(&wb.mma_done, ph, 0x7509)) { ok = false; break; }
+                tc_fence_after();
+                {
+                    uint32_t v[32], q[16];
+                    tmem_ld32(trow + (wg == 0 ? kColDV : kColDK), v);
+                    tmem_ld16(trow + kColDQ + 16 * wg, q);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        fadd2(acc[e], acc[e + 1], acc[e], acc[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    // half of dQ's query row over the step's Q and dO tiles, 16-byte chunks
+                    // permuted by the row so that the warp's stores spread over the banks
+                    // (the accumulator tile keeps the permutation)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4*>(stg + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4)) =
+                            make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wb.dq_ready[ph]);
             }
-            Diag<kBW>::step(g, wbase, sums, X, T, quad, lane, side);
-            if (!wwait(&wb.mma_done, ph, 0x7505)) { ok = false; break; }
-            tc_fence_after();
-            {
-                uint32_t v[32];
-                tmem_ld32(trow + kColDV, v);
-                tmem_wait_ld();
+            if (!ok) break;
+            if (kvalid) {
+                if (wg == 1) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    fadd2(dv[e], dv[e + 1], dv[e], dv[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                tmem_ld32(trow + kColDK, v);
-                tmem_wait_ld();
+                    for (int e = 0; e < 32; ++e) acc[e] *= kScale;
+                }
+                uint4* dst = reinterpret_cast<uint4*>((wg == 0 ? prm.dv : prm.dk) + ktok * kRowBytes);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    fadd2(dk[e], dk[e + 1], dk[e], dk[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                tmem_ld32(trow + kColDQ, v);
-                tmem_wait_ld();
-                // dQ of this query row over the step's Q and dO tiles, 16-byte chunks
-                // permuted by the row so that the warp's stores spread over the banks
-                // (the accumulator tile keeps the permutation)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(stg + r * 128 + ((c ^ (r & 7)) << 4)) =
-                        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                for (int c = 0; c < 4; ++c) dst[c] = pack_chunk(acc, c);
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            if (!group_sync(0x7506)) { ok = false; break; }  // dQ staged; products, sums and K, V rows read
-            if (loader) {
-                bulk_reduce_add_f32(prm.acc + (item0 + T) * kTile * kHeadDim, stg, 2 * kTileBytes);
-                bulk_commit();
-            }
-            ++step;
         }
-        if (!ok) break;
-        if (loader && kvs == 1 && X + stride < g.tiles) load_kv(X + stride, 0);
-        if (kvalid) {
-            uint4* dst = reinterpret_cast<uint4*>(prm.dv + ktok * kRowBytes);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) dst[c] = pack_chunk(dv, c);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) dk[e] *= kScale;
-            dst = reinterpret_cast<uint4*>(prm.dk + ktok * kRowBytes);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) dst[c] = pack_chunk(dk, c);
-        }
-    }
-    if (loader) bulk_wait_all();
-    if (r == 0) {
-        umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
-        mbar_wait(&wb.done, 0, ctl, 0x75ff);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(bars->tmem_base, 256 * kWorkers);
-    float* dst = prm.part + (X0 * g.heads + h) * static_cast<long long>(side * side);
-    for (int e = r; e < side * side; e += kTile) dst[e] = sums[e];
+    if (warp == 8 * kWorkers) tmem_dealloc(bars->tmem_base, 256 * kWorkers);
+    if (computes) {
+        float* dst = prm.part + (X0 * g.heads + h) * static_cast<long long>(side * side);
+        for (int e = tid & 255; e < side * side; e += 256) dst[e] = sums[e];
+    }
 }
 
 // post: per (tile, head), thread = slot row: dq from the accumulator.
@@ -930,9 +972,12 @@ cudaError_t launch_relbias_fwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
     if (g.N < kTile) {
         e = launch_small_fwd(g, p, status, limit_ns, num_sms, stream);
     } else {
-        static SmemOptIn optin[3];
-        const int kind = g.bw >= 16 ? 2 : (g.bw == 8 ? 1 : 0);
-        auto* kern = kind == 2 ? fwd::fwd_kernel<16> : (kind == 1 ? fwd::fwd_kernel<8> : fwd::fwd_kernel<4>);
+        static SmemOptIn optin[5];
+        using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, fwd::Params);
+        static const Kernel kernels[5] = {fwd::fwd_kernel<4>, fwd::fwd_kernel<8>, fwd::fwd_kernel<16>,
+                                          fwd::fwd_kernel<32>, fwd::fwd_kernel<64>};
+        const int kind = ilog2_exact(g.bw) - 2;
+        const Kernel kern = kernels[kind];
         if ((e = optin[kind].ensure(reinterpret_cast<const void*>(kern), kSmemLimit)) != cudaSuccess) return e;
         fwd::Params prm{};
         prm.g = g;
@@ -944,12 +989,12 @@ cudaError_t launch_relbias_fwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
         prm.status = status;
         prm.limit_ns = limit_ns;
         prm.pitch = bias_pitch(g.M, g.bw);
-        prm.stages = g.M == 64 ? 3 : fwd::kMaxStages;  // the table of M = 64 takes the fourth stage's place
-        prm.worker_bytes = (3 + 2 * prm.stages) * kTileBytes;
-        prm.tab_off = 2 * prm.worker_bytes;
+        prm.q_tiles = g.M == 64 ? 1 : 2;  // the table of M = 64 takes the second tiles' place
+        prm.worker_bytes = (prm.q_tiles + 4) * kTileBytes;
+        prm.tab_off = fwd::kWorkers * prm.worker_bytes;
         prm.bar_off = (prm.tab_off + (2 * g.M - 1) * prm.pitch * 4 + 127) / 128 * 128;
         const int smem = prm.bar_off + static_cast<int>(sizeof(fwd::Bars)) + 1024;
-        prm.streams = streams_per_head((g.tiles + 1) / 2, g.heads, num_sms);
+        prm.streams = streams_per_head((g.tiles + fwd::kWorkers - 1) / fwd::kWorkers, g.heads, num_sms);
         kern<<<static_cast<unsigned>(prm.streams) * g.heads, fwd::kThreads, smem, stream>>>(maps.q, maps.k, maps.v, prm);
         e = cudaGetLastError();
     }
@@ -1020,7 +1065,7 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
             const Kernel kern = kernels[W - 1][kind];
             e = optin[W - 1][kind].ensure(reinterpret_cast<const void*>(kern), kSmemLimit);
             if (e == cudaSuccess) {
-                kern<<<static_cast<unsigned>(prm.streams) * g.heads, 128 * W, smem, stream>>>(maps.q, maps.k, maps.v,
+                kern<<<static_cast<unsigned>(prm.streams) * g.heads, 256 * W + 128, smem, stream>>>(maps.q, maps.k, maps.v,
                                                                                              maps.dout, prm);
                 e = cudaGetLastError();
             }

@@ -24,10 +24,11 @@ constexpr int kSms = 148;  // SMs of a B200: bounds the CTAs, and with them the 
 // warp hold 32 consecutive slots, boxes of bw tokens a row, and read table words
 // of their own (row, column) shifted by a common amount: bw consecutive words per
 // box row.  A pitch of 16 (bw = 16) or 8 or 24 (bw <= 8) modulo 32 puts the box
-// rows of a warp into different banks, so a warp's 32 reads take one pass.
+// rows of a warp into different banks, so a warp's 32 reads take one pass.  At M =
+// 64 the padded table would not fit beside the tiles.
 __host__ __device__ constexpr int bias_pitch(int M, int bw) {
     int p = 2 * M - 1;
-    if (bw >= 32) return p;
+    if (bw >= 32 || M == 64) return p;
     if (bw == 16) {
         while (p % 32 != 16) ++p;
     } else {
