@@ -156,7 +156,7 @@ template <int OP>
 __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
     constexpr int stages = stages_of(OP), kStageBytes = stage_bytes(OP);
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* ones = smem + kOnesOff;  // kDw only

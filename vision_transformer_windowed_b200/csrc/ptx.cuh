@@ -13,6 +13,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// The first 1024-byte boundary of dynamic shared memory, by pointer arithmetic: a
+// pointer made from an integer would lose its address space.
+__device__ __forceinline__ uint8_t* align_smem(uint8_t* raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -78,7 +82,11 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
                                             volatile int* abort_flag, uint64_t limit_ns, unsigned int where) {
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
+        // the clock and the flag only every few tries: a waiting warp's polls take issue
+        // slots from the working ones
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > limit_ns) {
             atomicCAS(status, 0u, (kErrTimeout << 24) | (where & 0xFFFFFFu));
@@ -326,6 +334,44 @@ __device__ __forceinline__ void fmul2(float& dx, float& dy, float ax, float ay, 
         "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "=f"(dx), "=f"(dy)
         : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+
+// The same on values that stay packed: a pair held as one 64-bit value keeps its two
+// registers together from one instruction to the next.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long pair(uint32_t a, uint32_t b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add_pair(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul_pair(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// a += v or b += v, by the condition.
+__device__ __forceinline__ void add_pair_either(bool to_b, unsigned long long& a, unsigned long long& b,
+                                                unsigned long long v) {
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@!p add.rn.f32x2 %0, %0, %3;\n\t@p add.rn.f32x2 %1, %1, %3;\n\t}"
+        : "+l"(a), "+l"(b)
+        : "r"(static_cast<int>(to_b)), "l"(v));
 }
 
 // Packs two floats into f16x2 with `lo` in the low half (round to nearest even).

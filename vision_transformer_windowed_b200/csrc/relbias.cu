@@ -14,6 +14,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "dgeo.cuh"
 #include "geometry.cuh"
 #include "kernels.cuh"
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ Params prm) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + prm.bar_off);
     float* tab = reinterpret_cast<float*>(smem + prm.tab_off);
     const Geo& g = prm.g;
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
         const ChunkOffsets<kBW> co(g, pitch);
+        const unsigned long long sl2_2 = pair(sl2, sl2);
         uint32_t n = 0, it = 0;  // key tiles and items seen
         bool ok = true;
         for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
@@ -246,85 +249,93 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = slot_token(g, X, r, h, &pi, &pj, &tok);
             const float* brow = tab + (pi + g.M - 1) * pitch + pj + g.M - 1;
             const uint32_t myseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
-            float m = -INFINITY, l = 0.f;
-            float o[32];
+            float m = -INFINITY;
+            unsigned long long l = 0, o[16];  // pairs: the row sum in two parts, O
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 16; ++e) o[e] = 0;
             for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++n) {
                 const long long kt = I.kv0 + __ffs(act) - 1;
                 const uint32_t a16 = I.masked ? d_allow16(g, myseg, kt, I.win) : 0xFFu;
                 if (!wwait(&wb.s_full, n & 1u, 0x7608)) { ok = false; break; }
                 tc_fence_after();
-                float l2[2] = {0.f, 0.f};
                 const float* btile = brow - tile_offset(g, kt, pitch);
+                // one key tile's probabilities; kMasked: some of its groups are not attended
+                auto softmax_tile = [&](auto masked) {
+                    constexpr bool kMasked = decltype(masked)::value;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(trow + 32 * c, v);
-                    const BiasRows<kBW, -1> b0(btile - co.at(c), pitch), b1(btile - co.at(c) - co.half, pitch);
-                    float t[32];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        t[e] = b0[e];
-                        t[16 + e] = b1[e];
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        ffma2(t[e], t[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2, t[e], t[e + 1]);
-                    if (I.masked) {
-                        const bool on0 = (a16 >> (2 * c)) & 1u, on1 = (a16 >> (2 * c + 1)) & 1u;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            t[e] = on0 ? t[e] : -INFINITY;
-                            t[16 + e] = on1 ? t[16 + e] : -INFINITY;
-                        }
-                    }
-                    // The running maximum only moves when a chunk exceeds it by more than
-                    // 2^64: probabilities up to 2^64 stay far inside bf16's and fp32's range,
-                    // and the final division uses the same maximum as the sum.
-                    float c2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) c2[(e >> 1) & 1] = fmax3(c2[(e >> 1) & 1], t[e], t[e + 1]);
-                    const float cm = fmaxf(c2[0], c2[1]);
-                    const bool grow = cm > m + 64.f;
-                    if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float alpha = grow ? ex2_approx(m - cm) : 1.f;
-                        if (grow) m = cm;
-                        l *= alpha;
-                        l2[0] *= alpha;
-                        l2[1] *= alpha;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) fmul2(o[e], o[e + 1], o[e], o[e + 1], alpha, alpha);
-                        tmem_wait_st();
-#pragma unroll 1
-                        for (int k = 0; k < 2 * c; ++k) {  // this tile's chunks already written
-                            uint32_t pw[8];
-                            tmem_ld8(trow + kColP + 8 * k, pw);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                pw[e] = pack_bf16x2(bf16lo_to_f32(pw[e]) * alpha, bf16hi_to_f32(pw[e]) * alpha);
-                            tmem_st8(trow + kColP + 8 * k, pw);
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;  // no key so far: P = 0
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t w[8];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(trow + 32 * c, v);
+                        const BiasRows<kBW, -1> b0(btile - co.at(c), pitch), b1(btile - co.at(c) - co.half, pitch);
+                        unsigned long long t[16];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int a = 16 * hh + 2 * e;
-                            float t0, t1;
-                            fadd2(t0, t1, t[a], t[a + 1], -mu, -mu);
-                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                            fadd2(l2[0], l2[1], l2[0], l2[1], p0, p1);
-                            w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
+                            t[e] = pair(b0[2 * e], b0[2 * e + 1]);
+                            t[8 + e] = pair(b1[2 * e], b1[2 * e + 1]);
                         }
-                        tmem_st8(trow + kColP + 16 * c + 8 * hh, w);  // over columns of S already read
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) t[e] = fma_pair(pair(v[2 * e], v[2 * e + 1]), sl2_2, t[e]);
+                        if (kMasked) {
+                            const bool on0 = (a16 >> (2 * c)) & 1u, on1 = (a16 >> (2 * c + 1)) & 1u;
+                            const unsigned long long none = pair(-INFINITY, -INFINITY);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                t[e] = on0 ? t[e] : none;
+                                t[8 + e] = on1 ? t[8 + e] : none;
+                            }
+                        }
+                        // The running maximum only moves when a chunk exceeds it by more than
+                        // 2^64: probabilities up to 2^64 stay far inside bf16's and fp32's range,
+                        // and the final division uses the same maximum as the sum.
+                        float c2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x, y;
+                            unpair(t[e], x, y);
+                            c2[e & 1] = fmax3(c2[e & 1], x, y);
+                        }
+                        const float cm = fmaxf(c2[0], c2[1]);
+                        const bool grow = cm > m + 64.f;
+                        if (__any_sync(0xFFFFFFFFu, grow)) {
+                            const float alpha = grow ? ex2_approx(m - cm) : 1.f;
+                            const unsigned long long alpha2 = pair(alpha, alpha);
+                            if (grow) m = cm;
+                            l = mul_pair(l, alpha2);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = mul_pair(o[e], alpha2);
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int k = 0; k < 2 * c; ++k) {  // this tile's chunks already written
+                                uint32_t pw[8];
+                                tmem_ld8(trow + kColP + 8 * k, pw);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    pw[e] = pack_bf16x2(bf16lo_to_f32(pw[e]) * alpha, bf16hi_to_f32(pw[e]) * alpha);
+                                tmem_st8(trow + kColP + 8 * k, pw);
+                            }
+                        }
+                        const float mu = m == -INFINITY ? 0.f : -m;  // no key so far: P = 0
+                        const unsigned long long mu2 = pair(mu, mu);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float p0, p1;
+                                unpair(add_pair(t[8 * hh + e], mu2), p0, p1);
+                                p0 = ex2_approx(p0);
+                                p1 = ex2_approx(p1);
+                                l = add_pair(l, pair(p0, p1));
+                                w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
+                            }
+                            tmem_st8(trow + kColP + 16 * c + 8 * hh, w);  // over columns of S already read
+                        }
                     }
-                }
-                l += l2[0] + l2[1];
+                };
+                if (I.masked) softmax_tile(std::true_type{});
+                else softmax_tile(std::false_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -338,17 +349,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&wb.o_read);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    fadd2(o[e], o[e + 1], o[e], o[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                for (int e = 0; e < 16; ++e) o[e] = add_pair(o[e], pair(v[2 * e], v[2 * e + 1]));
             }
             if (!ok) break;
-            const float inv = 1.f / l;
+            float la, lb, x[32];
+            unpair(l, la, lb);
+            la += lb;
+            const float inv = 1.f / la;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;  // no key: O = 0
+            for (int e = 0; e < 16; ++e) {
+                unpair(o[e], x[2 * e], x[2 * e + 1]);
+                x[2 * e] = la == 0.f ? 0.f : x[2 * e] * inv;  // no key: O = 0
+                x[2 * e + 1] = la == 0.f ? 0.f : x[2 * e + 1] * inv;
+            }
             const uint32_t qb = nq == 2 ? it & 1u : 0u;
             uint8_t* ost = wsm + qb * kTileBytes;
-            store_row_swz(ost, r, o);
-            if (valid && prm.lse != nullptr) prm.lse[tok] = (m + lg2_approx(l)) * kLn2;
+            store_row_swz(ost, r, x);
+            if (valid && prm.lse != nullptr) prm.lse[tok] = (m + lg2_approx(la)) * kLn2;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // eight whole 64-byte rows a store
@@ -392,7 +409,7 @@ __host__ inline WsLayout ws_layout(const Geo& g) {
     size_t o = 0;
     if (g.N >= kTile) {
         L.acc = o;  o += round256(ht * kTile * kHeadDim * 4);  // fp32 dQ [heads][tiles][128][32], 16-byte chunks permuted
-        L.rowv = o; o += round256(ht * kTile * 8);             // per slot row: lse log2(e), D
+        L.rowv = o; o += round256(ht * kTile * 8);             // per (head, tile): -lse log2(e) [128], -D [128]
         const int W = workers(g);
         L.streams = W * streams_per_head((g.tiles + W - 1) / W, g.heads, kSms);
     } else {
@@ -413,7 +430,7 @@ struct Params {
     const int* buckets;
     int n_buckets;
     float* acc;
-    float2* rowv;
+    float* rowv;
     float* part;
     unsigned int* status;
     unsigned long long limit_ns;
@@ -452,7 +469,8 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Param
         D = (d[0] + d[1]) + (d[2] + d[3]);
         lse2 = grad_lse2(__ldg(p.lse + tok));
     }
-    p.rowv[ht * kTile + r] = make_float2(lse2, D);
+    p.rowv[ht * 2 * kTile + r] = -lse2;  // negated: the main kernel adds them, packed
+    p.rowv[ht * 2 * kTile + kTile + r] = -D;
 }
 
 // Main kernel: a worker is eight warps with 256 TMEM columns, its own buffers and
@@ -471,7 +489,7 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Param
 // TMEM columns: S^T [0,128), dP^T [128,256).  P^T of the first warpgroup [0,32), of the
 // second [64,96); dS^T [128,160) and [192,224); dV [32,64), dQ [96,128), dK [160,192).
 constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 32, kColDQ = 96, kColDK = 160;
-constexpr int kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, and the rows' (lse2, D)
+constexpr int kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, and the rows' -lse2 and -D
 
 struct WorkerBars {
     // dq_ready per stage: the copies may lag a step behind the next one's dQ
@@ -503,12 +521,9 @@ struct Diag {
     static constexpr int quads = w / 4;
     static constexpr int conc = 32 / w;         // blocks a warp walks at once
     static constexpr int nseg = kTile / w;
-    float A[4], B[4];  // before and after the quads wrap
+    unsigned long long A[2], B[2];  // columns (0, 1), (2, 3) before and after the quads wrap
 
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) A[e] = B[e] = 0.f;
-    }
+    __device__ __forceinline__ void clear() { A[0] = A[1] = B[0] = B[1] = 0; }
     // Shared address of the lane's first load of a key segment's rows: key kp, query
     // column 0; and the lane's offsets from there for every kk (the swizzle of key row
     // r: 16-byte chunk index xor r & 7).
@@ -517,13 +532,13 @@ struct Diag {
         for (int kk = 0; kk < quads; ++kk) {
             uint32_t x, y;
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(rows + (off[kk] ^ flip)));
-            const float v[4] = {bf16lo_to_f32(x), bf16hi_to_f32(x), bf16lo_to_f32(y), bf16hi_to_f32(y)};
-            const float fb = kk + m >= quads ? 1.f : 0.f, fa = 1.f - fb;
-            ffma2(A[0], A[1], v[0], v[1], fa, fa, A[0], A[1]);
-            ffma2(A[2], A[3], v[2], v[3], fa, fa, A[2], A[3]);
+            const unsigned long long v0 = pair(x << 16, x & 0xFFFF0000u), v1 = pair(y << 16, y & 0xFFFF0000u);
             if (quads > 1) {
-                ffma2(B[0], B[1], v[0], v[1], fb, fb, B[0], B[1]);
-                ffma2(B[2], B[3], v[2], v[3], fb, fb, B[2], B[3]);
+                add_pair_either(kk + m >= quads, A[0], B[0], v0);
+                add_pair_either(kk + m >= quads, A[1], B[1], v1);
+            } else {
+                A[0] = add_pair(A[0], v0);
+                A[1] = add_pair(A[1], v1);
             }
         }
     }
@@ -532,11 +547,16 @@ struct Diag {
     // wrapped ones of a neighbouring block may coincide with those, so they follow in
     // a step of their own.
     __device__ __forceinline__ void flush(float* dst, int m) {
+        float a[4], b[4];
+        unpair(A[0], a[0], a[1]);
+        unpair(A[1], a[2], a[3]);
+        unpair(B[0], b[0], b[1]);
+        unpair(B[1], b[2], b[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            dst[e] += A[e];
+            dst[e] += a[e];
             if (conc > 1) __syncwarp();
-            if (quads > 1 && m > 0) dst[e - w] += B[e];
+            if (quads > 1 && m > 0) dst[e - w] += b[e];
             __syncwarp();
         }
         clear();
@@ -607,7 +627,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 const __grid_constant__ Params prm) {
     constexpr int kThreads = 256 * kWorkers + 128;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + prm.bar_off);
     float* tab = reinterpret_cast<float*>(smem + prm.tab_off);
     const Geo& g = prm.g;
@@ -681,7 +701,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 mbar_arrive_expect_tx(bar, kStageBytes);
                 tile_tma(g, &mq, d, bar, T, h, false);
                 tile_tma(g, &mdo, d + kTileBytes, bar, T, h, false);
-                bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * kTile, 1024, bar);
+                bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * 2 * kTile, 1024, bar);
                 if (Lst) Tst1 = T;
                 else Tst0 = T;
                 Lst ^= 1u;
@@ -755,6 +775,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float sl2 = g.scale_log2;
         const ChunkOffsets<kBW> co(g, pitch);
+        const unsigned long long sl2_2 = pair(sl2, sl2);
         auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
@@ -769,58 +790,71 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
             const bool kvalid = slot_token(g, X, r, h, &ki, &kj, &ktok);
             const float* brow = tab + (g.M - 1 - ki) * pitch + g.M - 1 - kj;
             const uint32_t keyseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
-            float acc[32];  // dV (first warpgroup) or dK (second) of this key row
+            unsigned long long acc[16];  // dV (first warpgroup) or dK (second) of this key row, in pairs
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+            for (int e = 0; e < 16; ++e) acc[e] = 0;
             for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++step) {
                 const long long T = I.q0 + __ffs(act) - 1;
                 const uint32_t ph = step & 1u;
                 uint8_t* stg = wsm + st0 + ph * kStageBytes;
                 const uint32_t a16 = I.masked ? d_allow16(g, keyseg, T, I.win) : 0xFFu;
                 const float* bt = brow + tile_offset(g, T, pitch);
-                const float4* vec = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // (lse2, D) of two queries
+                const float4* neg_l = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // of four queries each
+                const float4* neg_d = neg_l + kTile / 4;
                 if (!wwait(&wb.st_full[ph], (step >> 1) & 1u, 0x7506) || !wwait(&wb.s_full, ph, 0x7507)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                auto gradient_half = [&](auto masked) {
+                    constexpr bool kMasked = decltype(masked)::value;
 #pragma unroll 1
-                for (int hc = 0; hc < 4; ++hc) {  // 16 queries: one piece of box rows, one region
-                    const int c16 = 4 * wg + hc;
-                    uint32_t sv[16], pv[16];
-                    tmem_ld16(trow + kColS + 16 * c16, sv);
-                    tmem_ld16(trow + kColDP + 16 * c16, pv);
-                    const BiasRows<kBW, 1> bias(bt + co.at(c16 >> 1) + ((c16 & 1) ? co.half : 0), pitch);
-                    uint32_t wp[8], wd[8];
-                    float t[16];
+                    for (int hc = 0; hc < 4; ++hc) {  // 16 queries: one piece of box rows, one region
+                        const int c16 = 4 * wg + hc;
+                        uint32_t sv[16], pv[16];
+                        tmem_ld16(trow + kColS + 16 * c16, sv);
+                        tmem_ld16(trow + kColDP + 16 * c16, pv);
+                        const BiasRows<kBW, 1> bias(bt + co.at(c16 >> 1) + ((c16 & 1) ? co.half : 0), pitch);
+                        unsigned long long t[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) t[e] = bias[e];
-                    tmem_wait_ld();
-                    if ((a16 >> c16) & 1u) {
+                        for (int e = 0; e < 8; ++e) t[e] = pair(bias[2 * e], bias[2 * e + 1]);
+                        uint32_t wp[8], wd[8];
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float4 LD = vec[8 * c16 + e / 2];
-                            float t0, t1, d0, d1;
-                            ffma2(t0, t1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, sl2, t[e], t[e + 1]);
-                            fadd2(t0, t1, t0, t1, -LD.x, -LD.z);
-                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                            fadd2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), -LD.y, -LD.w);
-                            fmul2(d0, d1, d0, d1, p0, p1);
-                            wp[e / 2] = pack_bf16x2(p0, p1);
-                            wd[e / 2] = pack_bf16x2(d0, d1);
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 L = neg_l[4 * c16 + e / 2], D = neg_d[4 * c16 + e / 2];
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                const int i = e + f;
+                                float p0, p1, d0, d1;
+                                unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
+                                                f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                                p0 = ex2_approx(p0);
+                                p1 = ex2_approx(p1);
+                                unpair(mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]),
+                                                         f ? pair(D.z, D.w) : pair(D.x, D.y)), pair(p0, p1)), d0, d1);
+                                wp[i] = pack_bf16x2(p0, p1);
+                                wd[i] = pack_bf16x2(d0, d1);
+                            }
                         }
-                    } else {
+                        if (kMasked) {
+                            const bool on = (a16 >> c16) & 1u;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) wp[e] = wd[e] = 0u;
+                            for (int e = 0; e < 8; ++e) {
+                                wp[e] = on ? wp[e] : 0u;
+                                wd[e] = on ? wd[e] : 0u;
+                            }
+                        }
+                        tmem_st8(trow + kColS + 64 * wg + 8 * hc, wp);
+                        tmem_st8(trow + kColDP + 64 * wg + 8 * hc, wd);
+#pragma unroll
+                        for (int q4 = 0; q4 < 2; ++q4)
+                            *reinterpret_cast<uint4*>(dsrow + (((2 * hc + q4) ^ (r & 7)) << 4)) =
+                                make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
                     }
-                    __syncwarp();
-                    tmem_st8(trow + kColS + 64 * wg + 8 * hc, wp);
-                    tmem_st8(trow + kColDP + 64 * wg + 8 * hc, wd);
-#pragma unroll
-                    for (int q4 = 0; q4 < 2; ++q4)
-                        *reinterpret_cast<uint4*>(dsrow + (((2 * hc + q4) ^ (r & 7)) << 4)) =
-                            make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
-                }
+                };
+                if (I.masked) gradient_half(std::true_type{});
+                else gradient_half(std::false_type{});
                 tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -838,8 +872,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                     tmem_ld16(trow + kColDQ + 16 * wg, q);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        fadd2(acc[e], acc[e + 1], acc[e], acc[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    for (int e = 0; e < 16; ++e) acc[e] = add_pair(acc[e], pair(v[2 * e], v[2 * e + 1]));
                     // half of dQ's query row over the step's Q and dO tiles, 16-byte chunks
                     // permuted by the row so that the warp's stores spread over the banks
                     // (the accumulator tile keeps the permutation)
@@ -855,13 +888,17 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
             }
             if (!ok) break;
             if (kvalid) {
-                if (wg == 1) {
+                float x[32];
+                const float f = wg == 0 ? 1.f : kScale;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) acc[e] *= kScale;
+                for (int e = 0; e < 16; ++e) {
+                    unpair(acc[e], x[2 * e], x[2 * e + 1]);
+                    x[2 * e] *= f;
+                    x[2 * e + 1] *= f;
                 }
                 uint4* dst = reinterpret_cast<uint4*>((wg == 0 ? prm.dv : prm.dk) + ktok * kRowBytes);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dst[c] = pack_chunk(acc, c);
+                for (int c = 0; c < 4; ++c) dst[c] = pack_chunk(x, c);
             }
         }
     }
@@ -1031,7 +1068,7 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
         prm.buckets = p.buckets;
         prm.n_buckets = p.n_buckets;
         prm.acc = reinterpret_cast<float*>(p.ws + L.acc);
-        prm.rowv = reinterpret_cast<float2*>(p.ws + L.rowv);
+        prm.rowv = reinterpret_cast<float*>(p.ws + L.rowv);
         prm.part = part;
         prm.status = status;
         prm.limit_ns = limit_ns;

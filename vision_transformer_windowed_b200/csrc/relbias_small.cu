@@ -119,7 +119,7 @@ struct Params {
 template <int kBW>
 __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant__ Params prm) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
     float* tab = reinterpret_cast<float*>(smem + kTabOff);
     const Geo& g = prm.g;
@@ -346,7 +346,7 @@ struct Params {
 template <int kBW>
 __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant__ Params prm) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
     float* tab = reinterpret_cast<float*>(smem + kTabOff);
     const Geo& g = prm.g;
