@@ -23,7 +23,6 @@
 #include "relbias.cuh"
 #include "rows.cuh"
 #include "schedule.cuh"
-#include "tile_io.cuh"
 
 namespace fswin {
 
@@ -65,11 +64,96 @@ struct BiasRows {
     }
 };
 
-// Table offset of the first slot of a window's tile.
-__device__ __forceinline__ int tile_offset(const Geo& g, long long tile, int pitch) {
+// Table offset of the first slot of tile u of a window.
+__device__ __forceinline__ int tile_offset(const Geo& g, int u, int pitch) {
     int i, j;
-    tile_row_pos(g, tile, 0, &i, &j);
+    tile_row_pos(g, u, 0, &i, &j);
     return i * pitch + j;
+}
+
+// The shift-region mask of a window depends on its kind alone (bit 1: in the last row
+// of windows, bit 0: in the last column): its tokens from row or column M - s on form
+// regions of their own.  One table a CTA: per kind and region class the 16-slot groups
+// of each tile that lie in the class, and per kind and tile the tiles it attends.
+struct Masks {
+    uint8_t groups[4][4][32];
+    uint32_t act[4][32];
+};
+
+__device__ __forceinline__ uint32_t region_class(const Geo& g, int kind, int i, int j) {
+    const uint32_t e = g.M - g.s;
+    return ((kind & 2) && static_cast<uint32_t>(i) >= e ? 2u : 0u) | ((kind & 1) && static_cast<uint32_t>(j) >= e ? 1u : 0u);
+}
+
+// Ends with a __syncthreads of its own after the first half; the caller's follows.
+__device__ __forceinline__ void build_masks(const Geo& g, Masks* m, int tid, int nt) {
+    if (!g.s) return;
+    for (int x = tid; x < 4 * g.tpw; x += nt) {
+        const int kind = x / g.tpw, u = x - kind * g.tpw;
+        uint32_t by_class[4] = {0u, 0u, 0u, 0u};
+        for (int c = 0; c < 8; ++c) {
+            int i, j;
+            tile_row_pos(g, u, 16 * c, &i, &j);
+            const uint32_t cls = region_class(g, kind, i, j);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) by_class[k] |= (cls == k ? 1u : 0u) << c;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m->groups[kind][k][u] = static_cast<uint8_t>(by_class[k]);
+    }
+    __syncthreads();
+    for (int x = tid; x < 4 * g.tpw; x += nt) {
+        const int kind = x / g.tpw, u = x - kind * g.tpw;
+        uint32_t act = 0;
+        for (int v = 0; v < g.tpw; ++v)
+            for (int k = 0; k < 4; ++k)
+                if (m->groups[kind][k][u] && m->groups[kind][k][v]) act |= 1u << v;
+        m->act[kind][u] = act;
+    }
+}
+
+// A work item: tile u (0 .. tpw - 1) of a window.
+struct Item {
+    int b, wr, wc, kind, u;
+    uint32_t act;   // tiles of the window that share a pair with it
+    long long w0;   // the window's first tile
+};
+
+__device__ __forceinline__ Item item_of(const Geo& g, const Masks* m, long long X) {
+    Item I;
+    const uint32_t gw = static_cast<uint32_t>(X >> g.ltpw);
+    I.u = static_cast<int>(X) & (g.tpw - 1);
+    I.w0 = X - I.u;
+    I.b = static_cast<int>(fdiv(g.fd_nW, gw));
+    const uint32_t rem = gw - static_cast<uint32_t>(I.b) * g.nW;
+    I.wr = static_cast<int>(fdiv(g.fd_nWw, rem));
+    I.wc = static_cast<int>(rem) - I.wr * g.nWw;
+    I.kind = g.s ? ((I.wr + 1) * g.M == g.Hp ? 2 : 0) | (I.wc + 1 == g.nWw ? 1 : 0) : 0;
+    I.act = I.kind ? m->act[I.kind][I.u] : low_bits(g.tpw);
+    return I;
+}
+
+// Token of slot r of the item's tile (window position i, j); false outside the grid.
+__device__ __forceinline__ bool item_token(const Geo& g, const Item& I, int i, int j, int h, long long* tok) {
+    int row = I.wr * g.M + i + g.s, col = I.wc * g.M + j + g.s;
+    if (row >= g.Hp) row -= g.Hp;
+    if (col >= g.Wp) col -= g.Wp;
+    *tok = ((static_cast<long long>(I.b) * g.H + row) * g.W + col) * g.heads + h;
+    return row < g.H && col < g.W;
+}
+
+// TMA loads of tile u of the item's window from two tensors into consecutive tiles.
+__device__ __forceinline__ void load_tiles(const Geo& g, const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst,
+                                           uint64_t* bar, const Item& I, int u, int h) {
+    for (int x = 0; x < g.bpt; ++x) {
+        const int k = (u << g.lbpt) + x;
+        int row = I.wr * g.M + ((k >> g.lnbc) << g.lbh) + g.s, col = I.wc * g.M + ((k & (g.nbc - 1)) << g.lbw) + g.s;
+        if (row >= g.Hp) row -= g.Hp;
+        if (col >= g.Wp) col -= g.Wp;
+        uint8_t* p = dst + x * g.BT * kRowBytes;
+        tma_load_5d(p, m0, bar, 0, h, col, row, I.b);
+        if (m1) tma_load_5d(p + kTileBytes, m1, bar, 0, h, col, row, I.b);
+    }
 }
 
 // ------------------------------------------------------------------ forward
@@ -93,6 +177,7 @@ struct Bars {
     WorkerBars w[kWorkers];
     uint32_t tmem_base;
     int abort_flag;
+    Masks masks;
 };
 
 struct Params {
@@ -125,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     WorkerBars& wb = bars->w[wk];
     const long long stride = static_cast<long long>(kWorkers) * prm.streams;
     const long long X0 = static_cast<long long>(kWorkers) * (blockIdx.x / g.heads) + wk;
-    const long long item0 = static_cast<long long>(h) * g.tiles;
     const int pitch = prm.pitch, nq = prm.q_tiles;
 
     if (tid == 0) {
@@ -149,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
     }
+    build_masks(g, &bars->masks, tid, kThreads);
     build_bias(tab, pitch, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, g.M, tid,
                kThreads);
     tc_fence_before();
@@ -167,26 +252,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t wbase = smem_u32(wsm);
             const uint64_t dK0 = make_sdesc(wbase, 16, 512, kSw64);
             const uint64_t dMN0 = make_sdesc(wbase, 8192, 512, kSw64);
+            const Masks* masks = &bars->masks;
             auto load_q = [&](long long X, uint32_t b) {
+                const Item I = item_of(g, masks, X);
                 mbar_arrive_expect_tx(&wb.q_full[b], kTileBytes);
-                tile_tma(g, &mq, wsm + b * kTileBytes, &wb.q_full[b], X, h, false);
+                load_tiles(g, &mq, nullptr, wsm + b * kTileBytes, &wb.q_full[b], I, I.u, h);
             };
-            long long LX = X0, Lkv0 = 0;  // the key/value tiles of all items in one sequence, two ahead
-            uint32_t Lact = 0, Lst = 0;
+            long long LX = X0;  // the key/value tiles of all items in one sequence, two ahead
+            Item L{};
+            uint32_t Lst = 0;
             auto load_kv = [&]() {
-                if (Lact == 0) {
+                if (L.act == 0) {
                     if (LX >= g.tiles) return;
-                    const FwdItem I = d_fwd_item(g, item0 + LX);
-                    Lkv0 = I.kv0;
-                    Lact = I.act;
+                    L = item_of(g, masks, LX);
                     LX += stride;
                 }
-                const int u = __ffs(Lact) - 1;
-                Lact &= Lact - 1u;
-                uint8_t* d = kvs + Lst * 2 * kTileBytes;
+                const int u = __ffs(L.act) - 1;
+                L.act &= L.act - 1u;
                 mbar_arrive_expect_tx(&wb.kv_full[Lst], 2 * kTileBytes);
-                tile_tma(g, &mk, d, &wb.kv_full[Lst], Lkv0 + u, h, false);
-                tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[Lst], Lkv0 + u, h, false);
+                load_tiles(g, &mk, &mv, kvs + Lst * 2 * kTileBytes, &wb.kv_full[Lst], L, u, h);
                 Lst ^= 1u;
             };
             load_q(X0, 0);
@@ -197,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
                 const uint32_t qb = nq == 2 ? it & 1u : 0u;
-                const int count = __popc(d_fwd_item(g, item0 + X).act);
+                const int count = __popc(item_of(g, masks, X).act);
                 if (!mbar_wait(&wb.q_full[qb], nq == 2 ? (it >> 1) & 1u : it & 1u, ctl, 0x7601)) break;
                 const uint64_t qo = qb * (kTileBytes >> 4);
                 for (int c = 0; c < count; ++c, ++j) {
@@ -209,6 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kHeadDim / 16; ++k) umma_ss(tmem, dK0 + qo + 2 * k, dK0 + ko + 2 * k, id_s, k > 0);
                     umma_commit(&wb.s_full);
+                    // the next tile's copies, into the stage whose product was waited for, while
+                    // this tile's softmax runs: the copying thread's address arithmetic (thousands
+                    // of cycles among sixteen busy warps) stays off the chain
+                    if (j > 0) load_kv();
                     if (nq == 2 && c == 0 && it > 0 && X + stride < g.tiles) {
                         // the item before has stored its O from there
                         if (!(ok = mbar_wait(&wb.q_free[qb ^ 1u], ((it - 1u) >> 1) & 1u, ctl, 0x7604))) break;
@@ -221,7 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_ts(tmem + kColO, tmem + kColP + 8 * k, dMN0 + vo + 64 * k, id_pv, k > 0);
                     umma_commit(&wb.pv_full);
                     if (!(ok = mbar_wait(&wb.pv_full, ph, ctl, 0x7606))) break;  // the stage is free
-                    load_kv();
                 }
                 if (ok && nq == 1 && X + stride < g.tiles) {
                     if (!mbar_wait(&wb.q_free[0], it & 1u, ctl, 0x7607)) break;
@@ -239,23 +326,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
         const ChunkOffsets<kBW> co(g, pitch);
-        const unsigned long long sl2_2 = pair(sl2, sl2);
         uint32_t n = 0, it = 0;  // key tiles and items seen
         bool ok = true;
         for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
-            const FwdItem I = d_fwd_item(g, item0 + X);
+            const Item I = item_of(g, &bars->masks, X);
             int pi, pj;
             long long tok;
-            const bool valid = slot_token(g, X, r, h, &pi, &pj, &tok);
+            tile_row_pos(g, I.u, r, &pi, &pj);
+            const bool valid = item_token(g, I, pi, pj, h, &tok);
             const float* brow = tab + (pi + g.M - 1) * pitch + pj + g.M - 1;
-            const uint32_t myseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
+            const uint8_t* groups = bars->masks.groups[I.kind][region_class(g, I.kind, pi, pj)];
             float m = -INFINITY;
-            unsigned long long l = 0, o[16];  // pairs: the row sum in two parts, O
+            float l[2] = {0.f, 0.f};
+            unsigned long long o[16];  // in pairs
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0;
             for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++n) {
-                const long long kt = I.kv0 + __ffs(act) - 1;
-                const uint32_t a16 = I.masked ? d_allow16(g, myseg, kt, I.win) : 0xFFu;
+                const int kt = __ffs(act) - 1;
+                const uint32_t a16 = I.kind ? groups[kt] : 0xFFu;
                 if (!wwait(&wb.s_full, n & 1u, 0x7608)) { ok = false; break; }
                 tc_fence_after();
                 const float* btile = brow - tile_offset(g, kt, pitch);
@@ -267,22 +355,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t v[32];
                         tmem_ld32(trow + 32 * c, v);
                         const BiasRows<kBW, -1> b0(btile - co.at(c), pitch), b1(btile - co.at(c) - co.half, pitch);
-                        unsigned long long t[16];
+                        float t[32];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            t[e] = pair(b0[2 * e], b0[2 * e + 1]);
-                            t[8 + e] = pair(b1[2 * e], b1[2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) {
+                            t[e] = b0[e];
+                            t[16 + e] = b1[e];
                         }
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) t[e] = fma_pair(pair(v[2 * e], v[2 * e + 1]), sl2_2, t[e]);
+                        for (int e = 0; e < 32; ++e) t[e] = fmaf(__uint_as_float(v[e]), sl2, t[e]);
                         if (kMasked) {
                             const bool on0 = (a16 >> (2 * c)) & 1u, on1 = (a16 >> (2 * c + 1)) & 1u;
-                            const unsigned long long none = pair(-INFINITY, -INFINITY);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                t[e] = on0 ? t[e] : none;
-                                t[8 + e] = on1 ? t[8 + e] : none;
+                            for (int e = 0; e < 16; ++e) {
+                                t[e] = on0 ? t[e] : -INFINITY;
+                                t[16 + e] = on1 ? t[16 + e] : -INFINITY;
                             }
                         }
                         // The running maximum only moves when a chunk exceeds it by more than
@@ -290,18 +377,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // and the final division uses the same maximum as the sum.
                         float c2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float x, y;
-                            unpair(t[e], x, y);
-                            c2[e & 1] = fmax3(c2[e & 1], x, y);
-                        }
+                        for (int e = 0; e < 16; ++e) c2[e & 1] = fmax3(c2[e & 1], t[2 * e], t[2 * e + 1]);
                         const float cm = fmaxf(c2[0], c2[1]);
                         const bool grow = cm > m + 64.f;
                         if (__any_sync(0xFFFFFFFFu, grow)) {
                             const float alpha = grow ? ex2_approx(m - cm) : 1.f;
                             const unsigned long long alpha2 = pair(alpha, alpha);
                             if (grow) m = cm;
-                            l = mul_pair(l, alpha2);
+                            l[0] *= alpha;
+                            l[1] *= alpha;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = mul_pair(o[e], alpha2);
                             tmem_wait_st();
@@ -316,25 +400,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st8(trow + kColP + 8 * k, pw);
                             }
                         }
-                        const float mu = m == -INFINITY ? 0.f : -m;  // no key so far: P = 0
-                        const unsigned long long mu2 = pair(mu, mu);
+                        const float mu = m == -INFINITY ? 0.f : m;  // no key so far: P = 0
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             uint32_t w[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                float p0, p1;
-                                unpair(add_pair(t[8 * hh + e], mu2), p0, p1);
-                                p0 = ex2_approx(p0);
-                                p1 = ex2_approx(p1);
-                                l = add_pair(l, pair(p0, p1));
+                                const float p0 = ex2_approx(t[16 * hh + 2 * e] - mu);
+                                const float p1 = ex2_approx(t[16 * hh + 2 * e + 1] - mu);
+                                l[0] += p0;
+                                l[1] += p1;
                                 w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
                             }
                             tmem_st8(trow + kColP + 16 * c + 8 * hh, w);  // over columns of S already read
                         }
                     }
                 };
-                if (I.masked) softmax_tile(std::true_type{});
+                if (I.kind) softmax_tile(std::true_type{});
                 else softmax_tile(std::false_type{});
                 tmem_wait_st();
                 tc_fence_before();
@@ -352,9 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 16; ++e) o[e] = add_pair(o[e], pair(v[2 * e], v[2 * e + 1]));
             }
             if (!ok) break;
-            float la, lb, x[32];
-            unpair(l, la, lb);
-            la += lb;
+            float x[32];
+            const float la = l[0] + l[1];
             const float inv = 1.f / la;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -499,6 +580,7 @@ struct Bars {
     WorkerBars w[2];
     uint32_t tmem_base;
     int abort_flag;
+    Masks masks;
 };
 
 // A worker's shared memory: dS, K and V (kv_stages), two query stages, the table sums.
@@ -534,8 +616,8 @@ struct Diag {
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(rows + (off[kk] ^ flip)));
             const unsigned long long v0 = pair(x << 16, x & 0xFFFF0000u), v1 = pair(y << 16, y & 0xFFFF0000u);
             if (quads > 1) {
-                add_pair_either(kk + m >= quads, A[0], B[0], v0);
-                add_pair_either(kk + m >= quads, A[1], B[1], v1);
+                add_pair_either(m, quads - kk, A[0], B[0], v0);
+                add_pair_either(m, quads - kk, A[1], B[1], v1);
             } else {
                 A[0] = add_pair(A[0], v0);
                 A[1] = add_pair(A[1], v1);
@@ -562,7 +644,7 @@ struct Diag {
         clear();
     }
 
-    static __device__ __forceinline__ void step(const Geo& g, uint32_t ds, float* sums, long long ku, long long qt,
+    static __device__ __forceinline__ void step(const Geo& g, uint32_t ds, float* sums, int ku, int qt,
                                                 int quad, int lane, int side) {
         const int kp = lane & 3, m = (lane >> 2) & (quads - 1), gi = lane / (4 * quads);
         uint32_t off[quads];
@@ -663,6 +745,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         tmem_alloc(&bars->tmem_base, 256 * kWorkers);
         tmem_relinquish();
     }
+    build_masks(g, &bars->masks, tid, kThreads);
     build_bias(tab, pitch, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, g.M, tid,
                kThreads);
     if (computes)
@@ -678,29 +761,27 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         const int role = (warp - 8 * kWorkers) >> 1;  // 0: products, 1: copies
         if (lane == 0 && wk < kWorkers && X0 < g.tiles && role == 1) {
             // the query tiles of all items in one sequence, two steps ahead
-            long long LX = X0, Lq0 = 0, Tst0 = 0, Tst1 = 0;
-            uint32_t Lact = 0, Lst = 0;
+            long long LX = X0, Tst0 = 0, Tst1 = 0;
+            Item L{};
+            uint32_t Lst = 0;
             auto load_kv = [&](long long X, uint32_t b) {
-                uint8_t* d = wsm + kKVOff + b * 2 * kTileBytes;
+                const Item I = item_of(g, &bars->masks, X);
                 mbar_arrive_expect_tx(&wb.kv_full[b], 2 * kTileBytes);
-                tile_tma(g, &mk, d, &wb.kv_full[b], X, h, false);
-                tile_tma(g, &mv, d + kTileBytes, &wb.kv_full[b], X, h, false);
+                load_tiles(g, &mk, &mv, wsm + kKVOff + b * 2 * kTileBytes, &wb.kv_full[b], I, I.u, h);
             };
             auto load_step = [&]() {
-                if (Lact == 0) {
+                if (L.act == 0) {
                     if (LX >= g.tiles) return;
-                    const BwdItem I = d_bwd_item(g, item0 + LX);
-                    Lq0 = I.q0;
-                    Lact = I.act;
+                    L = item_of(g, &bars->masks, LX);
                     LX += stride;
                 }
-                const long long T = Lq0 + __ffs(Lact) - 1;
-                Lact &= Lact - 1u;
+                const int u = __ffs(L.act) - 1;
+                const long long T = L.w0 + u;
+                L.act &= L.act - 1u;
                 uint8_t* d = wsm + st0 + Lst * kStageBytes;
                 uint64_t* bar = &wb.st_full[Lst];
                 mbar_arrive_expect_tx(bar, kStageBytes);
-                tile_tma(g, &mq, d, bar, T, h, false);
-                tile_tma(g, &mdo, d + kTileBytes, bar, T, h, false);
+                load_tiles(g, &mq, &mdo, d, bar, L, u, h);
                 bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * 2 * kTile, 1024, bar);
                 if (Lst) Tst1 = T;
                 else Tst0 = T;
@@ -713,7 +794,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
             uint32_t step = 0, item = 0;
             bool ok = true;
             for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
-                const int count = __popc(d_bwd_item(g, item0 + X).act);
+                const int count = __popc(item_of(g, &bars->masks, X).act);
                 for (int c = 0; c < count; ++c, ++step) {
                     if (!(ok = mbar_wait(&wb.dq_ready[step & 1u], (step >> 1) & 1u, ctl, 0x7501))) break;
                     uint8_t* d = wsm + st0 + (step & 1u) * kStageBytes;
@@ -737,7 +818,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
             uint32_t step = 0, item = 0;
             bool ok = true;
             for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
-                const int count = __popc(d_bwd_item(g, item0 + X).act);
+                const int count = __popc(item_of(g, &bars->masks, X).act);
                 const uint32_t kvb = kvs == 2 ? item & 1u : 0u;
                 const uint64_t ko = (kKVOff + kvb * 2 * kTileBytes) >> 4, vo = ko + (kTileBytes >> 4);
                 if (!mbar_wait(&wb.kv_full[kvb], kvs == 2 ? (item >> 1) & 1u : item & 1u, ctl, 0x7502)) break;
@@ -775,7 +856,6 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float sl2 = g.scale_log2;
         const ChunkOffsets<kBW> co(g, pitch);
-        const unsigned long long sl2_2 = pair(sl2, sl2);
         auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
@@ -784,20 +864,21 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         uint32_t step = 0;
         bool ok = true;
         for (long long X = X0; X < g.tiles && ok; X += stride) {
-            const BwdItem I = d_bwd_item(g, item0 + X);
+            const Item I = item_of(g, &bars->masks, X);
             int ki, kj;
             long long ktok;
-            const bool kvalid = slot_token(g, X, r, h, &ki, &kj, &ktok);
+            tile_row_pos(g, I.u, r, &ki, &kj);
+            const bool kvalid = item_token(g, I, ki, kj, h, &ktok);
             const float* brow = tab + (g.M - 1 - ki) * pitch + g.M - 1 - kj;
-            const uint32_t keyseg = I.masked ? seg_at(d_tile_segs(g, X, I.win), r >> g.lBT) : 0u;
+            const uint8_t* groups = bars->masks.groups[I.kind][region_class(g, I.kind, ki, kj)];
             unsigned long long acc[16];  // dV (first warpgroup) or dK (second) of this key row, in pairs
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e] = 0;
             for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++step) {
-                const long long T = I.q0 + __ffs(act) - 1;
+                const int T = __ffs(act) - 1;  // query tile of the window
                 const uint32_t ph = step & 1u;
                 uint8_t* stg = wsm + st0 + ph * kStageBytes;
-                const uint32_t a16 = I.masked ? d_allow16(g, keyseg, T, I.win) : 0xFFu;
+                const uint32_t a16 = I.kind ? groups[T] : 0xFFu;
                 const float* bt = brow + tile_offset(g, T, pitch);
                 const float4* neg_l = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // of four queries each
                 const float4* neg_d = neg_l + kTile / 4;
@@ -815,27 +896,25 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                         tmem_ld16(trow + kColS + 16 * c16, sv);
                         tmem_ld16(trow + kColDP + 16 * c16, pv);
                         const BiasRows<kBW, 1> bias(bt + co.at(c16 >> 1) + ((c16 & 1) ? co.half : 0), pitch);
-                        unsigned long long t[8];
+                        float t[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) t[e] = pair(bias[2 * e], bias[2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) t[e] = bias[e];
                         uint32_t wp[8], wd[8];
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const float4 L = neg_l[4 * c16 + e / 2], D = neg_d[4 * c16 + e / 2];
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 L4 = neg_l[4 * c16 + e / 4], D4 = neg_d[4 * c16 + e / 4];
+                            const float L[4] = {L4.x, L4.y, L4.z, L4.w}, D[4] = {D4.x, D4.y, D4.z, D4.w};
+                            float p[4], d[4];
 #pragma unroll
-                            for (int f = 0; f < 2; ++f) {
-                                const int i = e + f;
-                                float p0, p1, d0, d1;
-                                unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
-                                                f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
-                                p0 = ex2_approx(p0);
-                                p1 = ex2_approx(p1);
-                                unpair(mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]),
-                                                         f ? pair(D.z, D.w) : pair(D.x, D.y)), pair(p0, p1)), d0, d1);
-                                wp[i] = pack_bf16x2(p0, p1);
-                                wd[i] = pack_bf16x2(d0, d1);
+                            for (int f = 0; f < 4; ++f) {
+                                p[f] = ex2_approx(fmaf(__uint_as_float(sv[e + f]), sl2, t[e + f]) + L[f]);
+                                d[f] = (__uint_as_float(pv[e + f]) + D[f]) * p[f];
                             }
+                            wp[e / 2] = pack_bf16x2(p[0], p[1]);
+                            wp[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                            wd[e / 2] = pack_bf16x2(d[0], d[1]);
+                            wd[e / 2 + 1] = pack_bf16x2(d[2], d[3]);
                         }
                         if (kMasked) {
                             const bool on = (a16 >> c16) & 1u;
@@ -853,7 +932,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                                 make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
                     }
                 };
-                if (I.masked) gradient_half(std::true_type{});
+                if (I.kind) gradient_half(std::true_type{});
                 else gradient_half(std::false_type{});
                 tmem_wait_st();
                 fence_proxy_async_smem();
@@ -862,7 +941,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 if (lane == 0) mbar_arrive(&wb.p_ready);
                 if (static_cast<int>(ph) == wg) {
                     if (!wwait(&wb.p_ready, ph, 0x7508)) { ok = false; break; }  // every row's dS is written
-                    Diag<kBW>::step(g, wbase, sums, X, T, quad, lane, side);
+                    Diag<kBW>::step(g, wbase, sums, I.u, T, quad, lane, side);
                 }
                 if (!wwait(&wb.mma_done, ph, 0x7509)) { ok = false; break; }
                 tc_fence_after();
