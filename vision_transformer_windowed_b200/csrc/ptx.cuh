@@ -366,14 +366,6 @@ __device__ __forceinline__ unsigned long long mul_pair(unsigned long long a, uns
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// a += v where x < y, else b += v.
-__device__ __forceinline__ void add_pair_either(int x, int y, unsigned long long& a, unsigned long long& b,
-                                                unsigned long long v) {
-    asm("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %2, %3;\n\t@p add.rn.f32x2 %0, %0, %4;\n\t@!p add.rn.f32x2 %1, %1, %4;\n\t}"
-        : "+l"(a), "+l"(b)
-        : "r"(x), "r"(y), "l"(v));
-}
-
 // Packs two floats into f16x2 with `lo` in the low half (round to nearest even).
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;

@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
         const ChunkOffsets<kBW> co(g, pitch);
+        const unsigned long long sl2_2 = pair(sl2, sl2);
         uint32_t n = 0, it = 0;  // key tiles and items seen
         bool ok = true;
         for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
@@ -337,8 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* brow = tab + (pi + g.M - 1) * pitch + pj + g.M - 1;
             const uint8_t* groups = bars->masks.groups[I.kind][region_class(g, I.kind, pi, pj)];
             float m = -INFINITY;
-            float l[2] = {0.f, 0.f};
-            unsigned long long o[16];  // in pairs
+            unsigned long long l = 0, o[16];  // pairs: the row sum in two parts, O
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0;
             for (uint32_t act = I.act; act != 0u; act &= act - 1u, ++n) {
@@ -355,21 +355,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t v[32];
                         tmem_ld32(trow + 32 * c, v);
                         const BiasRows<kBW, -1> b0(btile - co.at(c), pitch), b1(btile - co.at(c) - co.half, pitch);
-                        float t[32];
+                        unsigned long long t[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            t[e] = b0[e];
-                            t[16 + e] = b1[e];
+                        for (int e = 0; e < 8; ++e) {
+                            t[e] = pair(b0[2 * e], b0[2 * e + 1]);
+                            t[8 + e] = pair(b1[2 * e], b1[2 * e + 1]);
                         }
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) t[e] = fmaf(__uint_as_float(v[e]), sl2, t[e]);
+                        for (int e = 0; e < 16; ++e) t[e] = fma_pair(pair(v[2 * e], v[2 * e + 1]), sl2_2, t[e]);
                         if (kMasked) {
                             const bool on0 = (a16 >> (2 * c)) & 1u, on1 = (a16 >> (2 * c + 1)) & 1u;
+                            const unsigned long long none = pair(-INFINITY, -INFINITY);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                t[e] = on0 ? t[e] : -INFINITY;
-                                t[16 + e] = on1 ? t[16 + e] : -INFINITY;
+                            for (int e = 0; e < 8; ++e) {
+                                t[e] = on0 ? t[e] : none;
+                                t[8 + e] = on1 ? t[8 + e] : none;
                             }
                         }
                         // The running maximum only moves when a chunk exceeds it by more than
@@ -377,15 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // and the final division uses the same maximum as the sum.
                         float c2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) c2[e & 1] = fmax3(c2[e & 1], t[2 * e], t[2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) {
+                            float x, y;
+                            unpair(t[e], x, y);
+                            c2[e & 1] = fmax3(c2[e & 1], x, y);
+                        }
                         const float cm = fmaxf(c2[0], c2[1]);
                         const bool grow = cm > m + 64.f;
                         if (__any_sync(0xFFFFFFFFu, grow)) {
                             const float alpha = grow ? ex2_approx(m - cm) : 1.f;
                             const unsigned long long alpha2 = pair(alpha, alpha);
                             if (grow) m = cm;
-                            l[0] *= alpha;
-                            l[1] *= alpha;
+                            l = mul_pair(l, alpha2);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = mul_pair(o[e], alpha2);
                             tmem_wait_st();
@@ -400,16 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st8(trow + kColP + 8 * k, pw);
                             }
                         }
-                        const float mu = m == -INFINITY ? 0.f : m;  // no key so far: P = 0
+                        const float mu = m == -INFINITY ? 0.f : -m;  // no key so far: P = 0
+                        const unsigned long long mu2 = pair(mu, mu);
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             uint32_t w[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const float p0 = ex2_approx(t[16 * hh + 2 * e] - mu);
-                                const float p1 = ex2_approx(t[16 * hh + 2 * e + 1] - mu);
-                                l[0] += p0;
-                                l[1] += p1;
+                                float p0, p1;
+                                unpair(add_pair(t[8 * hh + e], mu2), p0, p1);
+                                p0 = ex2_approx(p0);
+                                p1 = ex2_approx(p1);
+                                l = add_pair(l, pair(p0, p1));
                                 w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
                             }
                             tmem_st8(trow + kColP + 16 * c + 8 * hh, w);  // over columns of S already read
@@ -434,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 16; ++e) o[e] = add_pair(o[e], pair(v[2 * e], v[2 * e + 1]));
             }
             if (!ok) break;
-            float x[32];
-            const float la = l[0] + l[1];
+            float la, lb, x[32];
+            unpair(l, la, lb);
+            la += lb;
             const float inv = 1.f / la;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -603,24 +610,24 @@ struct Diag {
     static constexpr int quads = w / 4;
     static constexpr int conc = 32 / w;         // blocks a warp walks at once
     static constexpr int nseg = kTile / w;
-    unsigned long long A[2], B[2];  // columns (0, 1), (2, 3) before and after the quads wrap
+    unsigned long long A[2], all[2];  // columns (0, 1), (2, 3): before the quads wrap, and all of them
 
-    __device__ __forceinline__ void clear() { A[0] = A[1] = B[0] = B[1] = 0; }
+    __device__ __forceinline__ void clear() { A[0] = A[1] = all[0] = all[1] = 0; }
     // Shared address of the lane's first load of a key segment's rows: key kp, query
     // column 0; and the lane's offsets from there for every kk (the swizzle of key row
     // r: 16-byte chunk index xor r & 7).
-    __device__ __forceinline__ void walk(uint32_t rows, const uint32_t (&off)[quads], uint32_t flip, int m) {
+    __device__ __forceinline__ void walk(uint32_t rows, const uint32_t (&off)[quads], uint32_t flip,
+                                         const unsigned long long (&before)[quads]) {
 #pragma unroll
         for (int kk = 0; kk < quads; ++kk) {
             uint32_t x, y;
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(rows + (off[kk] ^ flip)));
             const unsigned long long v0 = pair(x << 16, x & 0xFFFF0000u), v1 = pair(y << 16, y & 0xFFFF0000u);
+            all[0] = add_pair(all[0], v0);
+            all[1] = add_pair(all[1], v1);
             if (quads > 1) {
-                add_pair_either(m, quads - kk, A[0], B[0], v0);
-                add_pair_either(m, quads - kk, A[1], B[1], v1);
-            } else {
-                A[0] = add_pair(A[0], v0);
-                A[1] = add_pair(A[1], v1);
+                A[0] = fma_pair(v0, before[kk], A[0]);
+                A[1] = fma_pair(v1, before[kk], A[1]);
             }
         }
     }
@@ -630,10 +637,12 @@ struct Diag {
     // a step of their own.
     __device__ __forceinline__ void flush(float* dst, int m) {
         float a[4], b[4];
-        unpair(A[0], a[0], a[1]);
-        unpair(A[1], a[2], a[3]);
-        unpair(B[0], b[0], b[1]);
-        unpair(B[1], b[2], b[3]);
+        unpair(quads > 1 ? A[0] : all[0], a[0], a[1]);
+        unpair(quads > 1 ? A[1] : all[1], a[2], a[3]);
+        unpair(all[0], b[0], b[1]);
+        unpair(all[1], b[2], b[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] -= a[e];  // the wrapped ones
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             dst[e] += a[e];
@@ -648,8 +657,11 @@ struct Diag {
                                                 int quad, int lane, int side) {
         const int kp = lane & 3, m = (lane >> 2) & (quads - 1), gi = lane / (4 * quads);
         uint32_t off[quads];
+        unsigned long long before[quads];  // (1, 1) until the quads wrap, then (0, 0)
 #pragma unroll
         for (int kk = 0; kk < quads; ++kk) {
+            const float f = kk + m < quads ? 1.f : 0.f;
+            before[kk] = pair(f, f);
             const uint32_t r = 4 * kk + kp, p = (kk + m) & (quads - 1);
             off[kk] = ((r >> 3) << 10) + ((r & 7) << 7) + ((((p >> 1) ^ (r & 7)) << 4) | ((p & 1) << 3));
         }
@@ -673,7 +685,7 @@ struct Diag {
             // 4 .. 7 have the swizzle's bit 2 set
             const uint32_t rows = ds + ((q0 >> 6) << 14) + (((a * w) >> 3) << 10) + (w == 4 ? ((a & 1) << 9) : 0);
             const uint32_t flip = (((q0 & 63) >> 3) ^ (w == 4 ? ((a & 1) << 2) : 0)) << 4 | (w == 4 ? ((q0 & 4) << 1) : 0);
-            d.walk(rows, off, flip, m);
+            d.walk(rows, off, flip, before);
         };
         if (kBW == 64) {  // two rows of two 32-column segments
 #pragma unroll 1
@@ -856,6 +868,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float sl2 = g.scale_log2;
         const ChunkOffsets<kBW> co(g, pitch);
+        const unsigned long long sl2_2 = pair(sl2, sl2);
         auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
         };
@@ -896,25 +909,27 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                         tmem_ld16(trow + kColS + 16 * c16, sv);
                         tmem_ld16(trow + kColDP + 16 * c16, pv);
                         const BiasRows<kBW, 1> bias(bt + co.at(c16 >> 1) + ((c16 & 1) ? co.half : 0), pitch);
-                        float t[16];
+                        unsigned long long t[8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) t[e] = bias[e];
+                        for (int e = 0; e < 8; ++e) t[e] = pair(bias[2 * e], bias[2 * e + 1]);
                         uint32_t wp[8], wd[8];
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 L4 = neg_l[4 * c16 + e / 4], D4 = neg_d[4 * c16 + e / 4];
-                            const float L[4] = {L4.x, L4.y, L4.z, L4.w}, D[4] = {D4.x, D4.y, D4.z, D4.w};
-                            float p[4], d[4];
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 L = neg_l[4 * c16 + e / 2], D = neg_d[4 * c16 + e / 2];
 #pragma unroll
-                            for (int f = 0; f < 4; ++f) {
-                                p[f] = ex2_approx(fmaf(__uint_as_float(sv[e + f]), sl2, t[e + f]) + L[f]);
-                                d[f] = (__uint_as_float(pv[e + f]) + D[f]) * p[f];
+                            for (int f = 0; f < 2; ++f) {
+                                const int i = e + f;
+                                float p0, p1, d0, d1;
+                                unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
+                                                f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                                p0 = ex2_approx(p0);
+                                p1 = ex2_approx(p1);
+                                unpair(mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]),
+                                                         f ? pair(D.z, D.w) : pair(D.x, D.y)), pair(p0, p1)), d0, d1);
+                                wp[i] = pack_bf16x2(p0, p1);
+                                wd[i] = pack_bf16x2(d0, d1);
                             }
-                            wp[e / 2] = pack_bf16x2(p[0], p[1]);
-                            wp[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
-                            wd[e / 2] = pack_bf16x2(d[0], d[1]);
-                            wd[e / 2 + 1] = pack_bf16x2(d[2], d[3]);
                         }
                         if (kMasked) {
                             const bool on = (a16 >> c16) & 1u;
