@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     uint8_t* ones = smem + kOnesOff;  // kDw only
 
     if (tid == 0) {
@@ -223,17 +223,19 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             uint32_t st = 0, ph = 0;
             bool ok = true;
             for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x) {
                 const Tile x = tile_of(t);
                 for (int i = 0; i < x.nkb; ++i) {
-                    if (!(ok = mbar_wait(&bars->free_[st], ph ^ 1u, ctl, 0x8101))) break;
+                    if (!(ok = mbar_wait_warp(&bars->free_[st], ph ^ 1u, ctl, 0x8101))) break;
                     uint64_t* bar = &bars->full[st];
                     const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
                     const int k0 = (x.kb0 + i) * kBlockK;
-                    if (OP == kGate) {
+                    if (!elect_one()) {
+                        // the elected lane copies
+                    } else if (OP == kGate) {
                         mbar_arrive_expect_tx(bar, kABytes + 2 * prm.bn * 128);
                         tma_load_2d(s, &maps.a[0], bar, k0, x.m0);
                         tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                         for (int b = 0; b < 2; ++b) tma_load_2d(s + b * 8192, &maps.a[x.pr], bar, x.m0 + 64 * b, k0);
                         for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
                     }
+                    __syncwarp();
                     if (++st == stages) {
                         st = 0;
                         ph ^= 1u;
@@ -267,13 +270,13 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             uint32_t st = 0, ph = 0, n = 0;
             bool ok = true;
             for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
                 const Tile x = tile_of(t);
                 const uint32_t acc = tmem + 256 * (n & 1u);
-                if (!mbar_wait(&bars->acc_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8102)) break;
+                if (!mbar_wait_warp(&bars->acc_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8102)) break;
                 tc_fence_after();
                 const int width = width_of(x);
                 const uint32_t id = OP == kGate   ? make_idesc_bf16(kBlockM, 2 * prm.bn, false, false)
@@ -284,13 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                 const uint32_t id_ones = make_idesc_bf16(kBlockM, 16, true, false);
                 const bool bias = OP == kDw && x.n0 == 0 && prm.pr[x.pr].bias_part != nullptr;
                 for (int i = 0; i < x.nkb; ++i) {
-                    if (!(ok = mbar_wait(&bars->full[st], ph, ctl, 0x8103))) break;
+                    if (!(ok = mbar_wait_warp(&bars->full[st], ph, ctl, 0x8103))) break;
                     tc_fence_after();
                     const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
                     const int kb = OP == kDx && i >= kblocks ? i - kblocks : x.kb0 + i;
                     const int left = prm.k - kb * kBlockK;
                     const int steps = left >= kBlockK ? kBlockK / 16 : (left + 15) / 16;
-                    for (int k = 0; k < steps; ++k) {
+                    const bool issue = elect_one();
+                    for (int k = 0; issue && k < steps; ++k) {
                         const uint32_t more = i > 0 || k > 0;
                         if (OP == kDw) {
                             const uint64_t da = make_sdesc(s, 8192, 1024, kSw128) + 128 * k;
@@ -306,16 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                                         make_sdesc(sb + 2 * 64 * 128, 8192, 1024, kSw128) + 128 * k, id_dh, more);
                         }
                     }
-                    umma_commit(&bars->free_[st]);
+                    if (issue) umma_commit(&bars->free_[st]);
+                    __syncwarp();
                     if (++st == stages) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
-                if (ok) umma_commit(&bars->acc_full[n & 1u]);
+                if (ok && elect_one()) umma_commit(&bars->acc_full[n & 1u]);
+                __syncwarp();
             }
-            umma_commit(&bars->done);  // every product issued here has completed before the columns are freed
-            mbar_wait(&bars->done, 0, ctl, 0x81ff);
+            if (elect_one()) umma_commit(&bars->done);  // every product issued here has completed before the columns are freed
+            mbar_wait_warp(&bars->done, 0, ctl, 0x81ff);
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quad = ew & 3, half = ew >> 2;

@@ -104,6 +104,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     return mbar_wait_slow(bar, parity, ctl.status, ctl.abort_flag, ctl.limit_ns, where);
 }
 
+// The wait of a whole warp, the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const Ctl& ctl, unsigned int where) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctl, where));
+}
+
+// One lane of a converged warp.  A warp that issues tensor products or copies runs its
+// loop whole and elects a lane for the instructions themselves: descriptors and
+// coordinates then are the same in every lane and stay in uniform registers, which
+// these instructions read.  From a loop of one lane each operand is moved there first
+// (80 cycles a product in place of 40).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars* bars = reinterpret_cast<Bars*>(smem + prm.bar_off);
     float* tab = reinterpret_cast<float*>(smem + prm.tab_off);
     const Geo& g = prm.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int h = blockIdx.x % g.heads;
     const int wk = warp < 4 * kWorkers ? warp >> 2 : warp - 4 * kWorkers;
     WorkerBars& wb = bars->w[wk];
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* kvs = wsm + nq * kTileBytes;
 
     if (warp >= 4 * kWorkers) {
-        if (lane == 0 && X0 < g.tiles) {
+        if (X0 < g.tiles) {
             const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t id_pv = make_idesc_bf16(kTile, kHeadDim, false, true);
             const uint32_t wbase = smem_u32(wsm);
@@ -255,8 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Masks* masks = &bars->masks;
             auto load_q = [&](long long X, uint32_t b) {
                 const Item I = item_of(g, masks, X);
-                mbar_arrive_expect_tx(&wb.q_full[b], kTileBytes);
-                load_tiles(g, &mq, nullptr, wsm + b * kTileBytes, &wb.q_full[b], I, I.u, h);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&wb.q_full[b], kTileBytes);
+                    load_tiles(g, &mq, nullptr, wsm + b * kTileBytes, &wb.q_full[b], I, I.u, h);
+                }
+                __syncwarp();
             };
             long long LX = X0;  // the key/value tiles of all items in one sequence, two ahead
             Item L{};
@@ -269,8 +272,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int u = __ffs(L.act) - 1;
                 L.act &= L.act - 1u;
-                mbar_arrive_expect_tx(&wb.kv_full[Lst], 2 * kTileBytes);
-                load_tiles(g, &mk, &mv, kvs + Lst * 2 * kTileBytes, &wb.kv_full[Lst], L, u, h);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&wb.kv_full[Lst], 2 * kTileBytes);
+                    load_tiles(g, &mk, &mv, kvs + Lst * 2 * kTileBytes, &wb.kv_full[Lst], L, u, h);
+                }
+                __syncwarp();
                 Lst ^= 1u;
             };
             load_q(X0, 0);
@@ -282,41 +288,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (long long X = X0; X < g.tiles && ok; X += stride, ++it) {
                 const uint32_t qb = nq == 2 ? it & 1u : 0u;
                 const int count = __popc(item_of(g, masks, X).act);
-                if (!mbar_wait(&wb.q_full[qb], nq == 2 ? (it >> 1) & 1u : it & 1u, ctl, 0x7601)) break;
+                if (!mbar_wait_warp(&wb.q_full[qb], nq == 2 ? (it >> 1) & 1u : it & 1u, ctl, 0x7601)) break;
                 const uint64_t qo = qb * (kTileBytes >> 4);
                 for (int c = 0; c < count; ++c, ++j) {
                     const uint32_t st = j & 1u, ph = j & 1u;
                     const uint64_t ko = (nq + 2 * st) * (kTileBytes >> 4), vo = ko + (kTileBytes >> 4);
-                    if (!(ok = mbar_wait(&wb.kv_full[st], (j >> 1) & 1u, ctl, 0x7602))) break;
-                    if (j > 0 && !(ok = mbar_wait(&wb.o_read, ph ^ 1u, ctl, 0x7603))) break;  // the last P V is read
+                    if (!(ok = mbar_wait_warp(&wb.kv_full[st], (j >> 1) & 1u, ctl, 0x7602))) break;
+                    if (j > 0 && !(ok = mbar_wait_warp(&wb.o_read, ph ^ 1u, ctl, 0x7603))) break;  // the last P V is read
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kHeadDim / 16; ++k) umma_ss(tmem, dK0 + qo + 2 * k, dK0 + ko + 2 * k, id_s, k > 0);
-                    umma_commit(&wb.s_full);
+                        for (int k = 0; k < kHeadDim / 16; ++k)
+                            umma_ss(tmem, dK0 + qo + 2 * k, dK0 + ko + 2 * k, id_s, k > 0);
+                        umma_commit(&wb.s_full);
+                    }
+                    __syncwarp();
                     // the next tile's copies, into the stage whose product was waited for, while
                     // this tile's softmax runs: the copying thread's address arithmetic (thousands
                     // of cycles among sixteen busy warps) stays off the chain
                     if (j > 0) load_kv();
                     if (nq == 2 && c == 0 && it > 0 && X + stride < g.tiles) {
                         // the item before has stored its O from there
-                        if (!(ok = mbar_wait(&wb.q_free[qb ^ 1u], ((it - 1u) >> 1) & 1u, ctl, 0x7604))) break;
+                        if (!(ok = mbar_wait_warp(&wb.q_free[qb ^ 1u], ((it - 1u) >> 1) & 1u, ctl, 0x7604))) break;
                         load_q(X + stride, qb ^ 1u);
                     }
-                    if (!(ok = mbar_wait(&wb.p_ready, ph, ctl, 0x7605))) break;
+                    if (!(ok = mbar_wait_warp(&wb.p_ready, ph, ctl, 0x7605))) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_ts(tmem + kColO, tmem + kColP + 8 * k, dMN0 + vo + 64 * k, id_pv, k > 0);
-                    umma_commit(&wb.pv_full);
-                    if (!(ok = mbar_wait(&wb.pv_full, ph, ctl, 0x7606))) break;  // the stage is free
+                        for (int k = 0; k < kTile / 16; ++k)
+                            umma_ts(tmem + kColO, tmem + kColP + 8 * k, dMN0 + vo + 64 * k, id_pv, k > 0);
+                        umma_commit(&wb.pv_full);
+                    }
+                    __syncwarp();
+                    if (!(ok = mbar_wait_warp(&wb.pv_full, ph, ctl, 0x7606))) break;  // the stage is free
                 }
                 if (ok && nq == 1 && X + stride < g.tiles) {
-                    if (!mbar_wait(&wb.q_free[0], it & 1u, ctl, 0x7607)) break;
+                    if (!mbar_wait_warp(&wb.q_free[0], it & 1u, ctl, 0x7607)) break;
                     load_q(X + stride, 0);
                 }
             }
-            umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
-            mbar_wait(&wb.done, 0, ctl, 0x76ff);
+            if (elect_one()) umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
+            mbar_wait_warp(&wb.done, 0, ctl, 0x76ff);
         }
     } else {
         const int r = tid & (kTile - 1), quad = warp & 3;
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     Bars* bars = reinterpret_cast<Bars*>(smem + prm.bar_off);
     float* tab = reinterpret_cast<float*>(smem + prm.tab_off);
     const Geo& g = prm.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const bool computes = warp < 8 * kWorkers;
     const int wk = computes ? warp >> 3 : warp & 1;  // (one worker: its second helpers have no item)
     const int h = blockIdx.x % g.heads;
@@ -771,15 +784,18 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
 
     if (!computes) {
         const int role = (warp - 8 * kWorkers) >> 1;  // 0: products, 1: copies
-        if (lane == 0 && wk < kWorkers && X0 < g.tiles && role == 1) {
+        if (wk < kWorkers && X0 < g.tiles && role == 1) {
             // the query tiles of all items in one sequence, two steps ahead
             long long LX = X0, Tst0 = 0, Tst1 = 0;
             Item L{};
             uint32_t Lst = 0;
             auto load_kv = [&](long long X, uint32_t b) {
                 const Item I = item_of(g, &bars->masks, X);
-                mbar_arrive_expect_tx(&wb.kv_full[b], 2 * kTileBytes);
-                load_tiles(g, &mk, &mv, wsm + kKVOff + b * 2 * kTileBytes, &wb.kv_full[b], I, I.u, h);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&wb.kv_full[b], 2 * kTileBytes);
+                    load_tiles(g, &mk, &mv, wsm + kKVOff + b * 2 * kTileBytes, &wb.kv_full[b], I, I.u, h);
+                }
+                __syncwarp();
             };
             auto load_step = [&]() {
                 if (L.act == 0) {
@@ -792,9 +808,12 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 L.act &= L.act - 1u;
                 uint8_t* d = wsm + st0 + Lst * kStageBytes;
                 uint64_t* bar = &wb.st_full[Lst];
-                mbar_arrive_expect_tx(bar, kStageBytes);
-                load_tiles(g, &mq, &mdo, d, bar, L, u, h);
-                bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * 2 * kTile, 1024, bar);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, kStageBytes);
+                    load_tiles(g, &mq, &mdo, d, bar, L, u, h);
+                    bulk_load(d + 2 * kTileBytes, prm.rowv + (item0 + T) * 2 * kTile, 1024, bar);
+                }
+                __syncwarp();
                 if (Lst) Tst1 = T;
                 else Tst0 = T;
                 Lst ^= 1u;
@@ -808,18 +827,23 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
             for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
                 const int count = __popc(item_of(g, &bars->masks, X).act);
                 for (int c = 0; c < count; ++c, ++step) {
-                    if (!(ok = mbar_wait(&wb.dq_ready[step & 1u], (step >> 1) & 1u, ctl, 0x7501))) break;
+                    if (!(ok = mbar_wait_warp(&wb.dq_ready[step & 1u], (step >> 1) & 1u, ctl, 0x7501))) break;
                     uint8_t* d = wsm + st0 + (step & 1u) * kStageBytes;
-                    bulk_reduce_add_f32(prm.acc + (item0 + ((step & 1u) ? Tst1 : Tst0)) * kTile * kHeadDim, d, 2 * kTileBytes);
-                    bulk_commit();
+                    if (lane == 0) {  // one lane throughout: the waits below are for its own groups
+                        bulk_reduce_add_f32(prm.acc + (item0 + ((step & 1u) ? Tst1 : Tst0)) * kTile * kHeadDim, d,
+                                            2 * kTileBytes);
+                        bulk_commit();
+                    }
+                    __syncwarp();
                     // the item's products are done with its keys and values
                     if (c == count - 1 && X + kvs * stride < g.tiles) load_kv(X + kvs * stride, kvs == 2 ? item & 1u : 0u);
                     bulk_wait_read_all();
+                    __syncwarp();
                     load_step();
                 }
             }
             bulk_wait_all();
-        } else if (lane == 0 && wk < kWorkers && X0 < g.tiles) {
+        } else if (wk < kWorkers && X0 < g.tiles) {
             const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t id_dv = make_idesc_bf16(kTile, kHeadDim, false, true);
             const uint32_t id_dq = make_idesc_bf16(kTile, kHeadDim, true, true);
@@ -833,35 +857,41 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 const int count = __popc(item_of(g, &bars->masks, X).act);
                 const uint32_t kvb = kvs == 2 ? item & 1u : 0u;
                 const uint64_t ko = (kKVOff + kvb * 2 * kTileBytes) >> 4, vo = ko + (kTileBytes >> 4);
-                if (!mbar_wait(&wb.kv_full[kvb], kvs == 2 ? (item >> 1) & 1u : item & 1u, ctl, 0x7502)) break;
+                if (!mbar_wait_warp(&wb.kv_full[kvb], kvs == 2 ? (item >> 1) & 1u : item & 1u, ctl, 0x7502)) break;
                 for (int c = 0; c < count; ++c, ++step) {
                     const uint32_t b = step & 1u;
                     const uint64_t qo = static_cast<uint64_t>((st0 + b * kStageBytes) >> 4), dof = qo + (kTileBytes >> 4);
-                    if (!(ok = mbar_wait(&wb.st_full[b], (step >> 1) & 1u, ctl, 0x7503))) break;
-                    if (step > 0 && !(ok = mbar_wait(&wb.dq_ready[b ^ 1u], ((step - 1u) >> 1) & 1u, ctl, 0x7504))) break;
+                    if (!(ok = mbar_wait_warp(&wb.st_full[b], (step >> 1) & 1u, ctl, 0x7503))) break;
+                    if (step > 0 && !(ok = mbar_wait_warp(&wb.dq_ready[b ^ 1u], ((step - 1u) >> 1) & 1u, ctl, 0x7504))) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kHeadDim / 16; ++k) {
-                        umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
-                        umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+                        for (int k = 0; k < kHeadDim / 16; ++k) {
+                            umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
+                            umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+                        }
+                        umma_commit(&wb.s_full);
                     }
-                    umma_commit(&wb.s_full);
-                    if (!(ok = mbar_wait(&wb.p_ready, b, ctl, 0x7505))) break;
+                    __syncwarp();
+                    if (!(ok = mbar_wait_warp(&wb.p_ready, b, ctl, 0x7505))) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_ts(tmem + kColDV, tmem + kColS + 8 * k + (k < 4 ? 0 : 32), dMN0 + dof + 64 * k, id_dv, k > 0);
+                        for (int k = 0; k < kTile / 16; ++k)
+                            umma_ts(tmem + kColDV, tmem + kColS + 8 * k + (k < 4 ? 0 : 32), dMN0 + dof + 64 * k, id_dv, k > 0);
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_ts(tmem + kColDK, tmem + kColDP + 8 * k + (k < 4 ? 0 : 32), dMN0 + qo + 64 * k, id_dv, k > 0);
+                        for (int k = 0; k < kTile / 16; ++k)
+                            umma_ts(tmem + kColDK, tmem + kColDP + 8 * k + (k < 4 ? 0 : 32), dMN0 + qo + 64 * k, id_dv, k > 0);
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_ss(tmem + kColDQ, dDS + 128 * k, dMN0 + ko + 64 * k, id_dq, k > 0);
-                    umma_commit(&wb.mma_done);
+                        for (int k = 0; k < kTile / 16; ++k)
+                            umma_ss(tmem + kColDQ, dDS + 128 * k, dMN0 + ko + 64 * k, id_dq, k > 0);
+                        umma_commit(&wb.mma_done);
+                    }
+                    __syncwarp();
                 }
             }
-            umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
-            mbar_wait(&wb.done, 0, ctl, 0x75ff);
+            if (elect_one()) umma_commit(&wb.done);  // every product issued here has completed before the columns are freed
+            mbar_wait_warp(&wb.done, 0, ctl, 0x75ff);
         }
     } else {
         const int wg = (warp >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
