@@ -1064,45 +1064,59 @@ __global__ void __launch_bounds__(128) post_kernel(const __grid_constant__ Param
 }  // namespace bwd
 
 // ------------------------------------------------------------------ table gradient
-// Sum of the partials of a (head, displacement) in stream order; without a bucket
-// map the displacement is the bucket and the result the gradient itself.
-__global__ void __launch_bounds__(256) table_sum_kernel(const float* part, int streams, int heads, int nd, int n_buckets,
-                                                        float* disp, __nv_bfloat16* dtable) {
-    const int e = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
-    if (e >= nd) return;
-    const float* src = part + static_cast<long long>(h) * nd + e;
-    const long long step = static_cast<long long>(heads) * nd;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    int k = 0;
-    for (; k + 4 <= streams; k += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += __ldg(src + (k + i) * step);
+// Sum of the partials of a (head, displacement): eight slices of the streams side by
+// side, each in order, then the slices in order.  Without a bucket map the displacement
+// is the bucket and the result the gradient itself.
+__global__ void __launch_bounds__(256) table_sum_kernel(const float* part, int streams, int heads, int nd, float* disp,
+                                                        __nv_bfloat16* dtable) {
+    __shared__ float slice[8][32];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane, h = blockIdx.y;
+    const int per = (streams + 7) / 8, k1 = min(streams, (q + 1) * per);
+    float s = 0.f;
+    if (e < nd) {
+        const float* src = part + static_cast<long long>(h) * nd + e;
+        const long long step = static_cast<long long>(heads) * nd;
+#pragma unroll 8
+        for (int k = q * per; k < k1; ++k) s += __ldg(src + k * step);
     }
-    for (; k < streams; ++k) s[0] += __ldg(src + k * step);
-    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-    if (disp)
-        disp[static_cast<long long>(h) * nd + e] = sum;
-    else  // n_buckets == nd
-        dtable[static_cast<long long>(h) * n_buckets + e] = __float2bfloat16(sum);
+    slice[q][lane] = s;
+    __syncthreads();
+    if (q == 0 && e < nd) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += slice[i][lane];
+        if (disp)
+            disp[static_cast<long long>(h) * nd + e] = s;
+        else
+            dtable[static_cast<long long>(h) * nd + e] = __float2bfloat16(s);
+    }
 }
 
-// Warp per bucket: finds the bucket's displacements in order, lanes take heads.
-__global__ void __launch_bounds__(256) table_bucket_kernel(const float* disp, const int* buckets, int heads, int nd,
+// Gradient of a bucket: block (bucket, eight heads); threads scan the map and add the
+// displacements that are theirs and the bucket's, the block adds the threads in a
+// fixed tree.
+__global__ void __launch_bounds__(128) table_bucket_kernel(const float* disp, const int* buckets, int heads, int nd,
                                                            int n_buckets, __nv_bfloat16* dtable) {
-    const int bucket = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (bucket >= n_buckets) return;
-    for (int h0 = 0; h0 < heads; h0 += 32) {
-        float s = 0.f;
-        for (int e0 = 0; e0 < nd; e0 += 32) {
-            const int e = e0 + lane;
-            uint32_t hit = __ballot_sync(0xFFFFFFFFu, e < nd && __ldg(buckets + e) == bucket);
-            while (hit) {
-                const int d = e0 + __ffs(hit) - 1;
-                hit &= hit - 1u;
-                if (h0 + lane < heads) s += disp[static_cast<long long>(h0 + lane) * nd + d];
-            }
-        }
-        if (h0 + lane < heads) dtable[static_cast<long long>(h0 + lane) * n_buckets + bucket] = __float2bfloat16(s);
+    __shared__ float part[4][8];
+    const int bucket = blockIdx.x, h0 = blockIdx.y * 8, hn = min(8, heads - h0);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int e = threadIdx.x; e < nd; e += 128) {
+        if (__ldg(buckets + e) != bucket) continue;
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+            if (h < hn) s[h] += disp[static_cast<long long>(h0 + h) * nd + e];
+    }
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], o);
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][h] = s[h];
+    }
+    __syncthreads();
+    if (threadIdx.x < static_cast<unsigned>(hn)) {
+        const int h = threadIdx.x;
+        dtable[static_cast<long long>(h0 + h) * n_buckets + bucket] =
+            __float2bfloat16((part[0][h] + part[1][h]) + (part[2][h] + part[3][h]));
     }
 }
 
@@ -1110,12 +1124,12 @@ cudaError_t launch_table_grad(const float* part, int streams, const Geo& g, cons
                               cudaStream_t stream) {
     const int nd = displacements(g.M);
     __nv_bfloat16* dt = static_cast<__nv_bfloat16*>(p.dtable);
-    table_sum_kernel<<<dim3((nd + 255) / 256, g.heads), 256, 0, stream>>>(part, streams, g.heads, nd, p.n_buckets,
-                                                                        p.buckets ? disp : nullptr, dt);
+    table_sum_kernel<<<dim3((nd + 31) / 32, g.heads), 256, 0, stream>>>(part, streams, g.heads, nd,
+                                                                      p.buckets ? disp : nullptr, dt);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (p.buckets)
-        table_bucket_kernel<<<(p.n_buckets + 7) / 8, 256, 0, stream>>>(disp, p.buckets, g.heads, nd, p.n_buckets, dt);
+    if (e != cudaSuccess || !p.buckets) return e;
+    table_bucket_kernel<<<dim3(p.n_buckets, (g.heads + 7) / 8), 128, 0, stream>>>(disp, p.buckets, g.heads, nd,
+                                                                               p.n_buckets, dt);
     return cudaGetLastError();
 }
 

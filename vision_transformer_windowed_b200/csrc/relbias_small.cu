@@ -72,12 +72,56 @@ __device__ __forceinline__ void save_rows(uint8_t* dst, const uint8_t* tile, lon
     }
 }
 
-// The 16-column groups of its own window that row r attends (bit b: local slots
-// [16 b, 16 b + 16)), from the tile's segment bytes.
-__device__ __forceinline__ uint32_t own_groups(const Geo& g, long long X, int r) {
-    if (!g.s) return 0xFu;
-    const uint64_t segs = d_tile_segs(g, X, d_tile_win(g, X));
-    return (allow16(g, seg_at(segs, r >> g.lBT), segs) >> (4 * (r >> 6))) & 0xFu;
+// Row r of tile X of 8 x 8 windows: its token of head h (in `tok`; false outside the
+// grid) and the 16-slot groups of its window that it attends (bit b: local slots
+// [16 b, 16 b + 16)).  A shift makes regions only in the last row and column of
+// windows, cut at 4, and its 4 x 4 boxes are the groups: box b lies in row b >> 1 and
+// column b & 1 of the window's boxes.
+template <int kBW>
+__device__ __forceinline__ bool row_of(const Geo& g, long long X, int r, int h, long long* tok, uint32_t* groups) {
+    const uint32_t gw = static_cast<uint32_t>(2 * X) + (r >> 6);
+    const int e = r & 63;
+    const int b = static_cast<int>(fdiv(g.fd_nW, gw));
+    const uint32_t rem = gw - static_cast<uint32_t>(b) * g.nW;
+    const int wr = static_cast<int>(fdiv(g.fd_nWw, rem)), wc = static_cast<int>(rem) - wr * g.nWw;
+    int row = wr * 8 + slot_i<kBW>(e) + g.s, col = wc * 8 + slot_j<kBW>(e) + g.s;
+    if (row >= g.Hp) row -= g.Hp;
+    if (col >= g.Wp) col -= g.Wp;
+    *tok = ((static_cast<long long>(b) * g.H + row) * g.W + col) * g.heads + h;
+    uint32_t m = 0xFu;
+    if (kBW == 4) {
+        if ((wr + 1) * 8 == g.Hp) m &= (e >> 5) & 1 ? 0xCu : 0x3u;
+        if (wc + 1 == g.nWw) m &= (e >> 4) & 1 ? 0xAu : 0x5u;
+    }
+    *groups = m;
+    return gw < g.wins && row < g.H && col < g.W;
+}
+
+// The four rows whose 16-byte chunk lane % 4 this lane moves for its warp (rows lane / 4
+// + 8 i of the warp's 32): their byte offsets in a token tensor, negative for rows
+// outside the grid.
+__device__ __forceinline__ void chunk_offsets(long long (&off)[4], long long tok, bool valid, int lane) {
+    const long long mine = valid ? tok * kRowBytes : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long o = __shfl_sync(0xFFFFFFFFu, mine, (lane >> 2) + 8 * i);
+        off[i] = o < 0 ? -1 : o + 16 * (lane & 3);
+    }
+}
+__device__ __forceinline__ uint32_t chunk_place(int warp, int lane, int i) {
+    const int row = warp * 32 + (lane >> 2) + 8 * i;
+    return row * kRowBytes + (((lane & 3) ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void load_chunks(uint32_t tile, const uint8_t* src, const long long (&off)[4], int warp, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        cp_async16(tile + chunk_place(warp, lane, i), off[i] < 0 ? src : src + off[i], off[i] < 0 ? 0u : 16u);
+}
+__device__ __forceinline__ void save_chunks(uint8_t* dst, const uint8_t* tile, const long long (&off)[4], int warp, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (off[i] >= 0)
+            *reinterpret_cast<uint4*>(dst + off[i]) = *reinterpret_cast<const uint4*>(tile + chunk_place(warp, lane, i));
 }
 
 // ------------------------------------------------------------------ M = 8 forward
@@ -123,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant_
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
     float* tab = reinterpret_cast<float*>(smem + kTabOff);
     const Geo& g = prm.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = tid, wi = warp >> 1;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, r = tid, wi = warp >> 1;
     const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
 
     if (tid == 0) {
@@ -139,24 +183,27 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant_
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    auto row_tok = [&](long long X, long long* tok) {
-        int pi, pj;
-        return slot_token(g, X, r, h, &pi, &pj, tok);
+    const uint32_t sbase = smem_u32(smem);
+    // an item's rows: this row's token and groups, and the warp's copies
+    auto copy_item = [&](int slot, const long long (&off)[4]) {
+        const uint32_t sl = sbase + slot * kSlotBytes;
+        load_chunks(sl, prm.q, off, warp, lane);
+        load_chunks(sl + kTileBytes, prm.k, off, warp, lane);
+        load_chunks(sl + 2 * kTileBytes, prm.v, off, warp, lane);
     };
-    auto copy_item = [&](int slot, long long tok, bool valid) {
-        uint8_t* sl = smem + slot * kSlotBytes;
-        load_rows(sl, prm.q, tok, valid, warp, lane);
-        load_rows(sl + kTileBytes, prm.k, tok, valid, warp, lane);
-        load_rows(sl + 2 * kTileBytes, prm.v, tok, valid, warp, lane);
-    };
-    long long X = stream, tok = 0, tok_n = 0;
-    bool valid = X < g.tiles && row_tok(X, &tok), valid_n = false;
-    if (X < g.tiles) copy_item(0, tok, valid);
+    long long X = stream, Xn = X + prm.streams, tok = 0, tok_n = 0, off[4], off_n[4];
+    uint32_t grp4 = 0, grp4_n = 0;
+    bool valid = false, valid_n = false;
+    if (X < g.tiles) {
+        valid = row_of<kBW>(g, X, r, h, &tok, &grp4);
+        chunk_offsets(off, tok, valid, lane);
+        copy_item(0, off);
+    }
     cp_async_commit();
-    long long Xn = X + prm.streams;
     if (Xn < g.tiles) {
-        valid_n = row_tok(Xn, &tok_n);
-        copy_item(1, tok_n, valid_n);
+        valid_n = row_of<kBW>(g, Xn, r, h, &tok_n, &grp4_n);
+        chunk_offsets(off_n, tok_n, valid_n, lane);
+        copy_item(1, off_n);
     }
     cp_async_commit();
     build_bias(tab, kP8, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, kM8, tid,
@@ -169,10 +216,9 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant_
     const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
     const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
     const uint32_t id_pv = make_idesc_bf16(kTile, kHeadDim, false, true);  // P (TMEM) x V
-    const uint32_t sbase = smem_u32(smem);
     const uint64_t dK0 = make_sdesc(sbase, 16, 512, kSw64);     // K-major, 64-byte rows
     const uint64_t dMN0 = make_sdesc(sbase, 8192, 512, kSw64);  // MN-major, 64-byte rows
-    const float sl2 = g.scale_log2;
+    const unsigned long long sl2_2 = pair(g.scale_log2, g.scale_log2);
     const int e_r = r & 63;  // local slot: its window position does not depend on the item
     const float* brow = tab + (slot_i<kBW>(e_r) + kM8 - 1) * kP8 + slot_j<kBW>(e_r) + kM8 - 1;
     uint32_t gph = 0, ph = 0;
@@ -188,71 +234,84 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant_
         if (!wwait(&bars->grp, gph, 0x7301)) break;  // every row's copies landed; the previous item's O was read
         gph ^= 1;
         const uint64_t qo = static_cast<uint64_t>(((j & 1) * kSlotBytes) >> 4);
-        if (r == 0) {
+        if (warp == 0) {
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kHeadDim / 16; ++k)
-                umma_ss(tmem, dK0 + qo + 2 * k, dK0 + qo + (kTileBytes >> 4) + 2 * k, id_s, k > 0);
-            umma_commit(&bars->s_full);
+                for (int k = 0; k < kHeadDim / 16; ++k)
+                    umma_ss(tmem, dK0 + qo + 2 * k, dK0 + qo + (kTileBytes >> 4) + 2 * k, id_s, k > 0);
+                umma_commit(&bars->s_full);
+            }
+            __syncwarp();
         }
-        const uint32_t grp4 = own_groups(g, X, r);
         if (!wwait(&bars->s_full, ph, 0x7302)) break;
         tc_fence_after();
-        float t[64];
+        unsigned long long t[32];
         {
             uint32_t v[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 tmem_ld32(trow + 64 * wi + 32 * c, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int a = 32 * c + 2 * e;
+                    t[16 * c + e] = pair(brow[-slot_off<kBW>(a)], brow[-slot_off<kBW>(a + 1)]);
+                }
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int a = 32 * c + e;
-                    ffma2(t[a], t[a + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2,
-                          brow[-slot_off<kBW>(a)], brow[-slot_off<kBW>(a + 1)]);
-                }
+                for (int e = 0; e < 16; ++e)
+                    t[16 * c + e] = fma_pair(pair(v[2 * e], v[2 * e + 1]), sl2_2, t[16 * c + e]);
             }
         }
-        if (grp4 != 0xFu) {
+        if (kBW == 4 && grp4 != 0xFu) {
+            const unsigned long long none = pair(-INFINITY, -INFINITY);
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-                if (!((grp4 >> (e >> 4)) & 1u)) t[e] = -INFINITY;
+            for (int e = 0; e < 32; ++e) t[e] = (grp4 >> (e >> 3)) & 1u ? t[e] : none;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], t[e], t[e + 1]);
+        for (int e = 0; e < 32; ++e) {
+            float x, y;
+            unpair(t[e], x, y);
+            mx[e & 3] = fmax3(mx[e & 3], x, y);
+        }
         const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-        const float mu = m == -INFINITY ? 0.f : m;  // a row whose every key is masked: P = 0
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float mu = m == -INFINITY ? 0.f : -m;  // a row whose every key is masked: P = 0
+        const unsigned long long mu2 = pair(mu, mu);
+        unsigned long long l2[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int a = 32 * c + 2 * e;
-                float t0, t1;
-                fadd2(t0, t1, t[a], t[a + 1], -mu, -mu);
-                const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                const int s = (e & 1) * 2;
-                fadd2(l4[s], l4[s + 1], l4[s], l4[s + 1], p0, p1);
+                float p0, p1;
+                unpair(add_pair(t[16 * c + e], mu2), p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                l2[e & 1] = add_pair(l2[e & 1], pair(p0, p1));
                 w[e] = pack_bf16x2(p0, p1);  // P joins the tensor product in V's type
             }
             tmem_st16(trow + kColP + 16 * c, w);
         }
-        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        float la, lb;
+        unpair(add_pair(l2[0], l2[1]), la, lb);
+        const float l = la + lb;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_ready);
-        if (r == 0 && mbar_wait(&bars->p_ready, ph, ctl, 0x7203)) {
+        if (warp == 0 && mbar_wait_warp(&bars->p_ready, ph, ctl, 0x7203)) {
             tc_fence_after();
             const uint64_t vo = qo + (2 * kTileBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+                for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_ts(tmem + kColO + 32 * w, tmem + kColP + 8 * k, dMN0 + vo + 256 * w + 64 * k, id_pv, k > 0);
-            umma_commit(&bars->o_full);
+                    for (int k = 0; k < 4; ++k)
+                        umma_ts(tmem + kColO + 32 * w, tmem + kColP + 8 * k, dMN0 + vo + 256 * w + 64 * k, id_pv, k > 0);
+                umma_commit(&bars->o_full);
+            }
+            __syncwarp();
         }
         if (!wwait(&bars->o_full, ph, 0x7304)) break;
         tc_fence_after();
@@ -269,23 +328,27 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const __grid_constant_
         }
         if (valid && prm.lse != nullptr) prm.lse[tok] = (m + lg2_approx(l)) * kLn2;
         __syncwarp();
-        save_rows(prm.o, sl, tok, valid, warp, lane);
+        save_chunks(prm.o, sl, off, warp, lane);
         __syncwarp();  // the staged rows are read: the slot takes the rows of the item after the next
         X = Xn;
         tok = tok_n;
         valid = valid_n;
+        grp4 = grp4_n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) off[i] = off_n[i];
         Xn += prm.streams;
         if (Xn < g.tiles) {
-            valid_n = row_tok(Xn, &tok_n);
-            copy_item(j & 1, tok_n, valid_n);
+            valid_n = row_of<kBW>(g, Xn, r, h, &tok_n, &grp4_n);
+            chunk_offsets(off_n, tok_n, valid_n, lane);
+            copy_item(j & 1, off_n);
         }
         cp_async_commit();
         ph ^= 1;
     }
     cp_async_wait<0>();
-    if (r == 0) {  // every product issued here has completed before the columns are freed
-        umma_commit(&bars->done);
-        mbar_wait(&bars->done, 0, ctl, 0x72ff);
+    if (warp == 0) {  // every product issued here has completed before the columns are freed
+        if (elect_one()) umma_commit(&bars->done);
+        mbar_wait_warp(&bars->done, 0, ctl, 0x72ff);
     }
     tc_fence_before();
     __syncthreads();
@@ -314,7 +377,7 @@ constexpr uint32_t kTmemCols = 256;
 // key's window) over columns already read, and per window dV, dK, dQ over the rest
 constexpr uint32_t kColS = 0, kColDP = 128, kColP = 0, kColDS = 128;
 constexpr uint32_t kColDV = 64, kColDK = 192;
-__device__ __forceinline__ uint32_t col_dq(int w) { return w ? 160u : 32u; }
+__host__ __device__ constexpr uint32_t col_dq(int w) { return w ? 160u : 32u; }
 
 struct Bars {
     uint64_t s_full, p_ready, mma2_done, grp, done;
@@ -350,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
     float* tab = reinterpret_cast<float*>(smem + kTabOff);
     const Geo& g = prm.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
     const long long n = g.tiles > stream ? (g.tiles - stream + prm.streams - 1) / prm.streams : 0;
     auto tile_at = [&](long long j) { return stream + j * prm.streams; };
@@ -383,27 +446,30 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
     auto wwait = [&](uint64_t* bar, uint32_t phase, unsigned int where) -> bool {
         return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, ctl, where));
     };
-    float dacc[64];  // row warps: sum over the items of dS of (this key slot, query slot e)
+    // row warps: sum over the items of dS of (this key slot, query slots 2 e, 2 e + 1)
+    unsigned long long dacc[32];
 #pragma unroll
-    for (int e = 0; e < 64; ++e) dacc[e] = 0.f;
+    for (int e = 0; e < 32; ++e) dacc[e] = 0;
 
     if (warp == kWarpMover) {
         // rows of each item one item ahead, and the stores of the staged gradients
-        long long tok[2][4];
-        bool valid[2][4];
+        long long off[2][4][4];  // per slot and warp of rows: this lane's four chunks
+        const uint32_t sbase = smem_u32(smem);
         auto geo = [&](long long j, int b) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                int pi, pj;
-                valid[b][q] = slot_token(g, tile_at(j), lane + 32 * q, h, &pi, &pj, &tok[b][q]);
+                long long tok;
+                uint32_t groups;
+                const bool valid = row_of<kBW>(g, tile_at(j), lane + 32 * q, h, &tok, &groups);
+                chunk_offsets(off[b][q], tok, valid, lane);
             }
         };
-        auto load = [&](uint8_t* tile, const uint8_t* src, int b) {
+        auto load = [&](uint32_t tile, const uint8_t* src, int b) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_rows(tile, src, tok[b][q], valid[b][q], q, lane);
+            for (int q = 0; q < 4; ++q) load_chunks(tile, src, off[b][q], q, lane);
         };
         auto load_slot = [&](int b) {
-            uint8_t* sl = smem + b * kSlotBytes;
+            const uint32_t sl = sbase + b * kSlotBytes;
             load(sl, prm.q, b);
             load(sl + kTileBytes, prm.k, b);
             load(sl + 2 * kTileBytes, prm.v, b);
@@ -411,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
             cp_async_mbar_arrive(&bars->slot_full[b]);
         };
         auto load_o = [&](int b) {
-            load(smem + kOOff, prm.o, b);
+            load(sbase + kOOff, prm.o, b);
             cp_async_mbar_arrive(&bars->o_full);
         };
         if (n > 0) {
@@ -438,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
                 uint8_t* sl = smem + b * kSlotBytes;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    save_rows(prm.dq, sl, tok[b][q], valid[b][q], q, lane);
-                    save_rows(prm.dk, sl + kTileBytes, tok[b][q], valid[b][q], q, lane);
-                    save_rows(prm.dv, sl + 2 * kTileBytes, tok[b][q], valid[b][q], q, lane);
+                    save_chunks(prm.dq, sl, off[b][q], q, lane);
+                    save_chunks(prm.dk, sl + kTileBytes, off[b][q], q, lane);
+                    save_chunks(prm.dv, sl + 2 * kTileBytes, off[b][q], q, lane);
                 }
                 __syncwarp();  // the staged rows are read: the slot takes item jj + 2's rows
                 if (jj + 2 < n) {
@@ -461,18 +527,17 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
         const uint64_t dDS = make_sdesc(sbase + kDSOff, 8192, 1024, kSw128);  // the windows' blocks are the two halves of M
         const int r = tid, wi = warp >> 1;
         const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const float sl2 = g.scale_log2;
-        float* lse2v = reinterpret_cast<float*>(smem + kVecOff);
-        float* dvec = lse2v + kTile;
+        const unsigned long long sl2_2 = pair(g.scale_log2, g.scale_log2);
+        float* neg_l = reinterpret_cast<float*>(smem + kVecOff);  // -lse2 and -D of the tile's queries
+        float* neg_d = neg_l + kTile;
         const int e_r = r & 63;
         const float* brow = tab + (kM8 - 1 - slot_i<kBW>(e_r)) * kP8 + kM8 - 1 - slot_j<kBW>(e_r);
         uint8_t* dsrow = smem + kDSOff + wi * 8192 + (e_r >> 3) * 1024 + (r & 7) * 128;
         uint32_t gph = 0;
-        long long tok = 0;
-        bool valid = false;
+        uint32_t groups = 0;
         auto lse2_of = [&](long long j) {
-            int pi, pj;
-            valid = slot_token(g, tile_at(j), r, h, &pi, &pj, &tok);
+            long long tok;
+            const bool valid = row_of<kBW>(g, tile_at(j), r, h, &tok, &groups);
             return valid ? grad_lse2(__ldg(prm.lse + tok)) : INFINITY;  // outside the grid: no probability
         };
         float lse2 = n > 0 ? lse2_of(0) : 0.f;
@@ -492,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
                     ffma2(d4[0], d4[1], a[e], a[e + 1], b[e], b[e + 1], d4[0], d4[1]);
                     ffma2(d4[2], d4[3], a[e + 2], a[e + 3], b[e + 2], b[e + 3], d4[2], d4[3]);
                 }
-                dvec[r] = (d4[0] + d4[1]) + (d4[2] + d4[3]);
+                neg_d[r] = -((d4[0] + d4[1]) + (d4[2] + d4[3]));
             }
-            lse2v[r] = lse2;
+            neg_l[r] = -lse2;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->o_free);
             fence_proxy_async_smem();
@@ -503,56 +568,65 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
             gph ^= 1;
             const uint64_t qo = static_cast<uint64_t>(((j & 1) * kSlotBytes) >> 4);
             const uint64_t ko = qo + (kTileBytes >> 4), vo = qo + (2 * kTileBytes >> 4), dof = qo + (3 * kTileBytes >> 4);
-            if (r == 0) {
+            if (warp == 0) {
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) {
-                    umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
-                    umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+                    for (int k = 0; k < kHeadDim / 16; ++k) {
+                        umma_ss(tmem + kColS, dK0 + ko + 2 * k, dK0 + qo + 2 * k, id_s, k > 0);
+                        umma_ss(tmem + kColDP, dK0 + vo + 2 * k, dK0 + dof + 2 * k, id_s, k > 0);
+                    }
+                    umma_commit(&bars->s_full);
                 }
-                umma_commit(&bars->s_full);
+                __syncwarp();
             }
-            const uint32_t grp4 = own_groups(g, tile_at(j), r);
+            const uint32_t grp4 = groups;
             if (j + 1 < n) lse2 = lse2_of(j + 1);
             if (!wwait(&bars->s_full, ph, 0x7307)) break;
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t sv[32], pv[32];
-                tmem_ld32(trow + kColS + 64 * wi + 32 * c, sv);
-                tmem_ld32(trow + kColDP + 64 * wi + 32 * c, pv);
+            for (int c = 0; c < 4; ++c) {  // 16 queries: one region
+                uint32_t sv[16], pv[16];
+                tmem_ld16(trow + kColS + 64 * wi + 16 * c, sv);
+                tmem_ld16(trow + kColDP + 64 * wi + 16 * c, pv);
+                unsigned long long t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t[e] = pair(brow[slot_off<kBW>(16 * c + 2 * e)], brow[slot_off<kBW>(16 * c + 2 * e + 1)]);
                 tmem_wait_ld();
-                uint32_t wp[16], wd[16];
+                const bool on = kBW == 8 || ((grp4 >> c) & 1u);
+                uint32_t wp[8], wd[8];
 #pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const int a = 32 * c + 4 * e4, e = 4 * e4;
-                    const bool on = (grp4 >> (a >> 4)) & 1u;
-                    const float4 L4 = *reinterpret_cast<const float4*>(lse2v + 64 * wi + a);
-                    const float4 D4 = *reinterpret_cast<const float4*>(dvec + 64 * wi + a);
-                    float t0, t1, t2, t3;
-                    fadd2(t0, t1, brow[slot_off<kBW>(a)], brow[slot_off<kBW>(a + 1)], -L4.x, -L4.y);
-                    fadd2(t2, t3, brow[slot_off<kBW>(a + 2)], brow[slot_off<kBW>(a + 3)], -L4.z, -L4.w);
-                    ffma2(t0, t1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, sl2, t0, t1);
-                    ffma2(t2, t3, __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), sl2, sl2, t2, t3);
-                    float p0 = ex2_approx(t0), p1 = ex2_approx(t1), p2 = ex2_approx(t2), p3 = ex2_approx(t3);
-                    float d0, d1, d2, d3;
-                    fadd2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), -D4.x, -D4.y);
-                    fadd2(d2, d3, __uint_as_float(pv[e + 2]), __uint_as_float(pv[e + 3]), -D4.z, -D4.w);
-                    fmul2(d0, d1, d0, d1, p0, p1);
-                    fmul2(d2, d3, d2, d3, p2, p3);
-                    if (!on) p0 = p1 = p2 = p3 = d0 = d1 = d2 = d3 = 0.f;
-                    fadd2(dacc[a], dacc[a + 1], dacc[a], dacc[a + 1], d0, d1);
-                    fadd2(dacc[a + 2], dacc[a + 3], dacc[a + 2], dacc[a + 3], d2, d3);
-                    wp[2 * e4] = pack_bf16x2(p0, p1);  // P and dS join their products in bf16, the operands' type
-                    wp[2 * e4 + 1] = pack_bf16x2(p2, p3);
-                    wd[2 * e4] = pack_bf16x2(d0, d1);
-                    wd[2 * e4 + 1] = pack_bf16x2(d2, d3);
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 L = *reinterpret_cast<const float4*>(neg_l + 64 * wi + 16 * c + 2 * e);
+                    const float4 D = *reinterpret_cast<const float4*>(neg_d + 64 * wi + 16 * c + 2 * e);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const int i = e + f;
+                        float p0, p1;
+                        unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
+                                        f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
+                        unsigned long long d =
+                            mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]), f ? pair(D.z, D.w) : pair(D.x, D.y)),
+                                     pair(p0, p1));
+                        wp[i] = pack_bf16x2(p0, p1);  // P and dS join their products in bf16, the operands' type
+                        if (kBW == 4) {
+                            wp[i] = on ? wp[i] : 0u;
+                            d = on ? d : 0ull;
+                        }
+                        dacc[8 * c + i] = add_pair(dacc[8 * c + i], d);
+                        float d0, d1;
+                        unpair(d, d0, d1);
+                        wd[i] = pack_bf16x2(d0, d1);
+                    }
                 }
-                tmem_st16(trow + kColP + 16 * c, wp);
-                tmem_st16(trow + kColDS + 16 * c, wd);
+                tmem_st8(trow + kColP + 8 * c, wp);
+                tmem_st8(trow + kColDS + 8 * c, wd);
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4)
-                    *reinterpret_cast<uint4*>(dsrow + (((4 * c + q4) ^ (r & 7)) << 4)) =
+                for (int q4 = 0; q4 < 2; ++q4)
+                    *reinterpret_cast<uint4*>(dsrow + (((2 * c + q4) ^ (r & 7)) << 4)) =
                         make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
             }
             tmem_wait_st();
@@ -560,21 +634,24 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->p_ready);
-            if (r == 0 && mbar_wait(&bars->p_ready, ph, ctl, 0x7203)) {
+            if (warp == 0 && mbar_wait_warp(&bars->p_ready, ph, ctl, 0x7203)) {
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
+                    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_ts(tmem + kColDV + 32 * w, tmem + kColP + 8 * k, dMN0 + dof + 256 * w + 64 * k, id_dv, k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            umma_ts(tmem + kColDV + 32 * w, tmem + kColP + 8 * k, dMN0 + dof + 256 * w + 64 * k, id_dv, k > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_ts(tmem + kColDK + 32 * w, tmem + kColDS + 8 * k, dMN0 + qo + 256 * w + 64 * k, id_dv, k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            umma_ts(tmem + kColDK + 32 * w, tmem + kColDS + 8 * k, dMN0 + qo + 256 * w + 64 * k, id_dv, k > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_ss(tmem + col_dq(w), dDS + 128 * k, dMN0 + ko + 256 * w + 64 * k, id_dq, k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            umma_ss(tmem + col_dq(w), dDS + 128 * k, dMN0 + ko + 256 * w + 64 * k, id_dq, k > 0);
+                    }
+                    umma_commit(&bars->mma2_done);
                 }
-                umma_commit(&bars->mma2_done);
+                __syncwarp();
             }
             if (!wwait(&bars->mma2_done, ph, 0x7308)) break;
             tc_fence_after();
@@ -594,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->staged);
         }
-        if (r == 0) {
-            umma_commit(&bars->done);
-            mbar_wait(&bars->done, 0, ctl, 0x72ff);
+        if (warp == 0) {
+            if (elect_one()) umma_commit(&bars->done);
+            mbar_wait_warp(&bars->done, 0, ctl, 0x72ff);
         }
     }
     tc_fence_before();
@@ -608,7 +685,12 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
     float* st = reinterpret_cast<float*>(smem);
     if (warp < 4) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) st[e * kTile + tid] = dacc[e];
+        for (int e = 0; e < 32; ++e) {
+            float a, b;
+            unpair(dacc[e], a, b);
+            st[2 * e * kTile + tid] = a;
+            st[(2 * e + 1) * kTile + tid] = b;
+        }
     }
     __syncthreads();
     for (int d = tid; d < 225; d += kThreads) {
