@@ -48,7 +48,8 @@ constexpr int kRingBytes = 12 * kABytes;
 constexpr int kOnesOff = kStages * (kABytes + kDwMaxN * 128);  // kDw: 16 rows x 64 of 1.0 behind its ring
 constexpr int kOnesBytes = 2048;
 constexpr int kStoreOff = kRingBytes;
-constexpr int kBarOff = kStoreOff + kEpiWarps * 2 * kStoreBytes;
+constexpr int kBiasOff = kStoreOff + kEpiWarps * 2 * kStoreBytes;  // a warp's 32 bias columns, fp32
+constexpr int kBarOff = kBiasOff + kEpiWarps * 128;
 constexpr uint32_t kColOnes = 240;                 // bias gradient columns of kDw
 
 struct Bars {
@@ -102,55 +103,78 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
                  : "memory");
 }
 
-// act(g) and act'(g).  silu: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).  gelu: g
-// Phi(g), Phi(g) + g phi(g), Phi from the error function's approximation 7.1.26 of
-// M. Abramowitz and I. A. Stegun, "Handbook of Mathematical Functions" (absolute
-// error 1.5e-7, far below the result's bf16 step; on the negative side the small tail
-// is the computed term itself, so nothing cancels).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ unsigned long long pair_of(float x) { return pair(x, x); }
+
+// act(g) and, for the gradient, act'(g) of two values.
+// silu: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).
+// gelu: g Phi(g), Phi(g) + g phi(g), Phi from the error function's approximation 7.1.28
+// of M. Abramowitz and I. A. Stegun, "Handbook of Mathematical Functions",
+//   erf(z) = 1 - (1 + a1 z + ... + a6 z^6)^-16, z >= 0 (absolute error 3e-7, far below
+// the result's bf16 step): one reciprocal and no exponential; large z overflow to a
+// reciprocal of zero, the limit.
 template <bool kSlope>
-__device__ __forceinline__ void activate(float g, int act, float& a, float& slope) {
+__device__ __forceinline__ void activate(unsigned long long g, int act, unsigned long long& a, unsigned long long& slope) {
+    float x, y;
     if (act == 0) {
-        const float s = __fdividef(1.f, 1.f + ex2_approx(-1.4426950408889634f * g));
-        a = g * s;
-        if (kSlope) slope = fmaf(a, 1.f - s, s);
+        unpair(mul_pair(g, pair_of(-1.4426950408889634f)), x, y);
+        unpair(add_pair(pair(ex2_approx(x), ex2_approx(y)), pair_of(1.f)), x, y);
+        const unsigned long long s = pair(rcp_approx(x), rcp_approx(y));
+        a = mul_pair(g, s);
+        if (kSlope) slope = fma_pair(a, fma_pair(s, pair_of(-1.f), pair_of(1.f)), s);
         return;
     }
-    const float z = fabsf(g) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
-    const float e = ex2_approx(-0.72134752044448170f * g * g);  // e^(-g^2 / 2)
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float tail = 0.5f * p * t * e;  // Phi(-|g|)
-    const float cdf = g < 0.f ? tail : 1.f - tail;
-    a = g * cdf;
-    if (kSlope) slope = fmaf(g * 0.39894228040143268f, e, cdf);
-}
-
-// 32 columns of a bias row from column c (a multiple of 8) on; zero beyond n.
-__device__ __forceinline__ void add_bias(float (&x)[32], const __nv_bfloat16* bias, int c, int n) {
-    if (!bias) return;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if (c + 8 * q >= n) break;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(bias + c + 8 * q));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[8 * q + 2 * e] += bf16lo_to_f32(w[e]);
-            x[8 * q + 2 * e + 1] += bf16hi_to_f32(w[e]);
-        }
+    const unsigned long long z = mul_pair(g & 0x7FFFFFFF7FFFFFFFull, pair_of(0.70710678118654752f));
+    unsigned long long p = fma_pair(z, pair_of(0.0000430638f), pair_of(0.0002765672f));
+    p = fma_pair(p, z, pair_of(0.0001520143f));
+    p = fma_pair(p, z, pair_of(0.0092705272f));
+    p = fma_pair(p, z, pair_of(0.0422820123f));
+    p = fma_pair(p, z, pair_of(0.0705230784f));
+    p = fma_pair(p, z, pair_of(1.f));
+    p = mul_pair(p, p);
+    p = mul_pair(p, p);
+    p = mul_pair(p, p);
+    p = mul_pair(p, p);
+    unpair(p, x, y);
+    const unsigned long long half = fma_pair(pair(rcp_approx(x), rcp_approx(y)), pair_of(-0.5f), pair_of(0.5f));
+    const unsigned long long cdf = add_pair(half | (g & 0x8000000080000000ull), pair_of(0.5f));  // half >= 0
+    a = mul_pair(g, cdf);
+    if (kSlope) {
+        unpair(mul_pair(mul_pair(g, g), pair_of(-0.72134752044448170f)), x, y);
+        slope = fma_pair(mul_pair(g, pair_of(0.39894228040143268f)), pair(ex2_approx(x), ex2_approx(y)), cdf);
     }
 }
 
-__device__ __forceinline__ void load_cols(uint32_t taddr, float (&x)[32]) {
-    uint32_t v[32];
-    tmem_ld32(taddr, v);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+// Adds 32 bias columns, one a lane, to every lane's row of 32: through the warp's
+// shared memory, from which each lane reads them all.
+__device__ __forceinline__ float bias_at(const __nv_bfloat16* bias, int c, int n) {
+    return bias && c < n ? __bfloat162float(bias[c]) : 0.f;
 }
+__device__ __forceinline__ void add_bias(unsigned long long (&x)[16], float* place, float mine, int lane) {
+    __syncwarp();
+    place[lane] = mine;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 b = *reinterpret_cast<const float4*>(place + 4 * q);
+        x[2 * q] = add_pair(x[2 * q], pair(b.x, b.y));
+        x[2 * q + 1] = add_pair(x[2 * q + 1], pair(b.z, b.w));
+    }
+}
+
+// 32 accumulator columns of this thread's row, in pairs; wait_cols before they are used.
+struct Cols {
+    uint32_t v[32];
+    __device__ __forceinline__ void load(uint32_t taddr) { tmem_ld32(taddr, v); }
+    __device__ __forceinline__ void get(unsigned long long (&x)[16]) const {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = pair(v[2 * e], v[2 * e + 1]);
+    }
+};
 
 template <int OP>
 __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
@@ -327,18 +351,26 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
         const int ew = warp - 4, quad = ew & 3, half = ew >> 2;
         const int row_in = quad * 32 + lane;
         const uint32_t store = sbase + kStoreOff + ew * 2 * kStoreBytes;
+        float* wbias = reinterpret_cast<float*>(smem + kBiasOff) + ew * 32;
         uint32_t n = 0, sbuf = 0;
         // A warp's 32 x 32 block of results: staged in bf16, stored by TMA (which leaves
         // out what lies outside the result).  Two buffers: the store before the last has
         // read its buffer.
-        auto put = [&](const CUtensorMap* m, const float (&x)[32], int col, int row0) {
+        auto put = [&](const CUtensorMap* m, const unsigned long long (&x)[16], int col, int row0) {
             bulk_wait_read_but1();
             __syncwarp();
             const uint32_t dst = store + (sbuf & 1u) * kStoreBytes + lane * 64;
             const int sw = (lane >> 1) & 3;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint4 v = pack_chunk(x, c);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    unpair(x[4 * c + e], lo, hi);
+                    w[e] = pack_bf16x2(lo, hi);
+                }
+                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ sw) << 4)), "r"(v.x), "r"(v.y),
                              "r"(v.z), "r"(v.w)
                              : "memory");
@@ -363,13 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                 const int row = x.m0 + row_in, width = width_of(x);
                 float* dst = p.part + (static_cast<long long>(x.split) * p.m + row) * p.n + x.n0;
                 for (int c = 32 * half; c < width; c += 64) {
-                    float v[32];
-                    load_cols(acc + c, v);
+                    uint32_t v[32];
+                    tmem_ld32(acc + c, v);
+                    tmem_wait_ld();
                     if (row < p.m) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             if (x.n0 + c + e < p.n)
-                                *reinterpret_cast<float4*>(dst + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                                *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
                 if (half == 0 && x.n0 == 0 && p.bias_part) {
@@ -382,35 +415,40 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                 const int left = prm.n - x.n0, width = left < prm.bn ? left : prm.bn;
                 for (int c = 32 * half; c < width; c += 64) {
                     const int col = x.n0 + c;
-                    float a[32];
-                    load_cols(acc + c, a);
-                    if (OP == kLinear || OP == kDx) {
-                        if (OP == kLinear) add_bias(a, prm.bias0, col, prm.n);
-                    } else {
-                        float u[32];
-                        load_cols(acc + prm.bn + c, u);
-                        add_bias(a, prm.bias0, col, prm.n);
-                        add_bias(u, prm.bias1, col, prm.n);
+                    Cols ca, cu, cd;
+                    ca.load(acc + c);
+                    if (OP == kGate || OP == kGrad) cu.load(acc + prm.bn + c);
+                    if (OP == kGrad) cd.load(acc + 128 + c);
+                    const float b0 = OP == kDx ? 0.f : bias_at(prm.bias0, col + lane, prm.n);
+                    const float b1 = OP == kGate || OP == kGrad ? bias_at(prm.bias1, col + lane, prm.n) : 0.f;
+                    tmem_wait_ld();
+                    unsigned long long a[16];
+                    ca.get(a);
+                    if (OP != kDx && prm.bias0) add_bias(a, wbias, b0, lane);
+                    if (OP == kGate || OP == kGrad) {
+                        unsigned long long u[16];
+                        cu.get(u);
+                        if (prm.bias1) add_bias(u, wbias, b1, lane);
                         if (OP == kGate) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float f, s;
+                            for (int e = 0; e < 16; ++e) {
+                                unsigned long long f, s;
                                 activate<false>(a[e], prm.act, f, s);
-                                a[e] = f * u[e];
+                                a[e] = mul_pair(f, u[e]);
                             }
                         } else {
-                            float dh[32], du[32];
-                            load_cols(acc + 128 + c, dh);
+                            unsigned long long dh[16];
+                            cd.get(dh);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float f, s;
+                            for (int e = 0; e < 16; ++e) {
+                                unsigned long long f, s;
                                 activate<true>(a[e], prm.act, f, s);
-                                du[e] = dh[e] * f;
-                                a[e] = f * u[e];
-                                dh[e] *= u[e] * s;
+                                a[e] = mul_pair(f, u[e]);
+                                u[e] = mul_pair(mul_pair(dh[e], u[e]), s);  // dg
+                                dh[e] = mul_pair(dh[e], f);                 // du
                             }
-                            put(&maps.out[1], dh, col, row0);
-                            put(&maps.out[2], du, col, row0);
+                            put(&maps.out[1], u, col, row0);
+                            put(&maps.out[2], dh, col, row0);
                         }
                     }
                     put(&maps.out[0], a, col, row0);
