@@ -278,7 +278,8 @@ FS_API fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, c
  * b_gate, b_up [hidden] and b_down [channels], each of which may be NULL.  Products and
  * the activation are fp32; h is rounded to bf16 between the two products.
  * Shapes: 0 <= tokens < 2^31 - 256, channels 8 .. 16384 and hidden 8 .. 65536, both
- * multiples of 8 (else FS_ERR_SHAPE); every pointer 16-byte aligned (FS_ERR_ALIGN).
+ * multiples of 8, and fewer than 2^31 tiles of 128 tokens by 64 channels of the wider
+ * of the two (else FS_ERR_SHAPE); every pointer 16-byte aligned (FS_ERR_ALIGN).
  *
  * Backward: gradients of sum(y * dy), from x and the weights (h is formed again).  dx and
  * the weight gradients are bf16 like what they belong to; a NULL bias gradient is not

@@ -136,6 +136,9 @@ fs_status mlp_shape(const fs_mlp_shape* sh, MlpShape* out) {
     if (sh->tokens < 0 || sh->tokens > 0x7FFFFF00ll || sh->channels < 8 || sh->channels > 16384 || sh->channels % 8 ||
         sh->hidden < 8 || sh->hidden > 65536 || sh->hidden % 8 || sh->act < 0 || sh->act > 1)
         return FS_ERR_SHAPE;
+    // tiles of 128 tokens and 64 columns are counted in 31 bits
+    if ((sh->tokens / 128 + 1) * ((sh->hidden > sh->channels ? sh->hidden : sh->channels) / 64 + 1) > 0x7FFFFFFFll)
+        return FS_ERR_SHAPE;
     *out = MlpShape{sh->tokens, sh->channels, sh->hidden, sh->act};
     return FS_OK;
 }

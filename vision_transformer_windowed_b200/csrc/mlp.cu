@@ -30,8 +30,10 @@ namespace fswin {
 namespace mlp {
 
 enum : int { kGate, kLinear, kGrad, kDx, kDw };
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+// Warps of the epilogue: sixteen where it computes the activation (kGate: four a
+// scheduler hide each other's latencies, 176 -> 110 us at 524288 x 96 x 256), else eight.
+__host__ __device__ constexpr int epi_warps(int op) { return op == kGate ? 16 : 8; }
+__host__ __device__ constexpr int threads_of(int op) { return 128 + 32 * epi_warps(op); }
 constexpr int kBlockK = 64;
 constexpr int kBlockM = 128;
 constexpr int kABytes = kBlockM * kBlockK * 2;
@@ -48,8 +50,7 @@ constexpr int kRingBytes = 12 * kABytes;
 constexpr int kOnesOff = kStages * (kABytes + kDwMaxN * 128);  // kDw: 16 rows x 64 of 1.0 behind its ring
 constexpr int kOnesBytes = 2048;
 constexpr int kStoreOff = kRingBytes;
-constexpr int kBiasOff = kStoreOff + kEpiWarps * 2 * kStoreBytes;  // a warp's 32 bias columns, fp32
-constexpr int kBarOff = kBiasOff + kEpiWarps * 128;
+constexpr int kBarOff = kStoreOff + 16 * kStoreBytes;
 constexpr uint32_t kColOnes = 240;                 // bias gradient columns of kDw
 
 struct Bars {
@@ -71,6 +72,7 @@ struct Maps {
 
 struct Problem {       // kDw: one of the three weight gradients
     int m, n, tiles_n, tiles, first;  // first: its first tile in the launch
+    FastDiv by_n;      // tiles_n
     float* part;       // [splits][m][n]
     float* bias_part;  // [splits][m], or null
 };
@@ -80,7 +82,8 @@ struct Params {
     int segments;      // kDx: 2
     int bn;            // columns of a tile
     int tiles_n;
-    long long tiles;
+    FastDiv by_n, by_splits;  // tiles_n, splits
+    unsigned int tiles;
     int act;           // 0 silu, 1 gelu
     const __nv_bfloat16 *bias0, *bias1;
     Problem pr[3];
@@ -177,7 +180,8 @@ struct Cols {
 };
 
 template <int OP>
-__global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
+    constexpr int kEpiWarps = epi_warps(OP), kThreads = threads_of(OP);
     constexpr int stages = stages_of(OP), kStageBytes = stage_bytes(OP);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem(smem_raw);
@@ -219,22 +223,22 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
         int pr, m0, n0, kb0, nkb, split;
     };
     const int kblocks = (prm.k + kBlockK - 1) / kBlockK;
-    auto tile_of = [&](long long t) {
+    auto tile_of = [&](unsigned int t) {
         Tile x{0, 0, 0, 0, kblocks * (OP == kDx ? prm.segments : 1), 0};
         if (OP == kDw) {
-            x.split = static_cast<int>(t % prm.splits);
-            const int q = static_cast<int>(t / prm.splits);
+            const int q = static_cast<int>(fdiv(prm.by_splits, t));
+            x.split = static_cast<int>(t) - q * prm.splits;
             x.pr = q >= prm.pr[2].first ? 2 : (q >= prm.pr[1].first ? 1 : 0);
             const Problem& p = prm.pr[x.pr];
-            const int i = q - p.first;
-            x.m0 = i / p.tiles_n * kBlockM;
-            x.n0 = i % p.tiles_n * prm.bn;
+            const int i = q - p.first, mt = static_cast<int>(fdiv(p.by_n, static_cast<uint32_t>(i)));
+            x.m0 = mt * kBlockM;
+            x.n0 = (i - mt * p.tiles_n) * prm.bn;
             x.kb0 = x.split * prm.blocks_per_split;
             x.nkb = min(prm.blocks_per_split, kblocks - x.kb0);
         } else {
-            const long long mt = t / prm.tiles_n;
-            x.m0 = static_cast<int>(mt) * kBlockM;
-            x.n0 = static_cast<int>(t - mt * prm.tiles_n) * prm.bn;
+            const int mt = static_cast<int>(fdiv(prm.by_n, t));
+            x.m0 = mt * kBlockM;
+            x.n0 = (static_cast<int>(t) - mt * prm.tiles_n) * prm.bn;
         }
         return x;
     };
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
         {
             uint32_t st = 0, ph = 0;
             bool ok = true;
-            for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x) {
+            for (unsigned int t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x) {
                 const Tile x = tile_of(t);
                 for (int i = 0; i < x.nkb; ++i) {
                     if (!(ok = mbar_wait_warp(&bars->free_[st], ph ^ 1u, ctl, 0x8101))) break;
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
         {
             uint32_t st = 0, ph = 0, n = 0;
             bool ok = true;
-            for (long long t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
+            for (unsigned int t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
                 const Tile x = tile_of(t);
                 const uint32_t acc = tmem + 256 * (n & 1u);
                 if (!mbar_wait_warp(&bars->acc_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8102)) break;
@@ -348,18 +352,22 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
             mbar_wait_warp(&bars->done, 0, ctl, 0x81ff);
         }
     } else if (warp >= 4) {
-        const int ew = warp - 4, quad = ew & 3, half = ew >> 2;
+        const int ew = warp - 4, quad = ew & 3, first = 32 * (ew >> 2);  // its first columns
+        constexpr int kStep = 8 * kEpiWarps, kBufs = 16 / kEpiWarps;     // columns of a round, store buffers a warp
         const int row_in = quad * 32 + lane;
-        const uint32_t store = sbase + kStoreOff + ew * 2 * kStoreBytes;
-        float* wbias = reinterpret_cast<float*>(smem + kBiasOff) + ew * 32;
         uint32_t n = 0, sbuf = 0;
-        // A warp's 32 x 32 block of results: staged in bf16, stored by TMA (which leaves
-        // out what lies outside the result).  Two buffers: the store before the last has
-        // read its buffer.
-        auto put = [&](const CUtensorMap* m, const unsigned long long (&x)[16], int col, int row0) {
-            bulk_wait_read_but1();
+        // A warp's store buffer, once its last store has read it: takes the bias columns,
+        // then a 32 x 32 block of results in bf16, stored by TMA (which leaves out what
+        // lies outside the result).
+        auto buffer = [&]() {
+            if (kBufs == 2) bulk_wait_read_but1();
+            else bulk_wait_read_all();
             __syncwarp();
-            const uint32_t dst = store + (sbuf & 1u) * kStoreBytes + lane * 64;
+            return kStoreOff + (ew * kBufs + (kBufs == 2 ? static_cast<int>(sbuf & 1u) : 0)) * kStoreBytes;
+        };
+        auto put = [&](const CUtensorMap* m, const unsigned long long (&x)[16], int col, int row0) {
+            const int buf = buffer();
+            uint8_t* dst = smem + buf + lane * 64;
             const int sw = (lane >> 1) & 3;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -370,20 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                     unpair(x[4 * c + e], lo, hi);
                     w[e] = pack_bf16x2(lo, hi);
                 }
-                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ sw) << 4)), "r"(v.x), "r"(v.y),
-                             "r"(v.z), "r"(v.w)
-                             : "memory");
+                *reinterpret_cast<uint4*>(dst + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(m, store + (sbuf & 1u) * kStoreBytes, col, row0);
+                tma_store_2d(m, sbase + buf, col, row0);
                 bulk_commit();
             }
             ++sbuf;
         };
-        for (long long t = blockIdx.x; t < prm.tiles; t += gridDim.x, ++n) {
+        for (unsigned int t = blockIdx.x; t < prm.tiles; t += gridDim.x, ++n) {
             const Tile x = tile_of(t);
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[n & 1u], (n >> 1) & 1u, ctl, 0x8104));
             if (!ok) break;
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                 const Problem& p = prm.pr[x.pr];
                 const int row = x.m0 + row_in, width = width_of(x);
                 float* dst = p.part + (static_cast<long long>(x.split) * p.m + row) * p.n + x.n0;
-                for (int c = 32 * half; c < width; c += 64) {
+                for (int c = first; c < width; c += kStep) {
                     uint32_t v[32];
                     tmem_ld32(acc + c, v);
                     tmem_wait_ld();
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                                 *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
-                if (half == 0 && x.n0 == 0 && p.bias_part) {
+                if (first == 0 && x.n0 == 0 && p.bias_part) {
                     uint32_t v[16];
                     tmem_ld16(acc + kColOnes, v);
                     tmem_wait_ld();
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                 }
             } else {
                 const int left = prm.n - x.n0, width = left < prm.bn ? left : prm.bn;
-                for (int c = 32 * half; c < width; c += 64) {
+                for (int c = first; c < width; c += kStep) {
                     const int col = x.n0 + c;
                     Cols ca, cu, cd;
                     ca.load(acc + c);
@@ -421,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_kernel(const __grid_constant_
                     if (OP == kGrad) cd.load(acc + 128 + c);
                     const float b0 = OP == kDx ? 0.f : bias_at(prm.bias0, col + lane, prm.n);
                     const float b1 = OP == kGate || OP == kGrad ? bias_at(prm.bias1, col + lane, prm.n) : 0.f;
+                    float* wbias = reinterpret_cast<float*>(smem + buffer());
                     tmem_wait_ld();
                     unsigned long long a[16];
                     ca.get(a);
@@ -494,8 +500,8 @@ template <int OP>
 cudaError_t launch(const Maps& maps, const Params& prm, int num_sms, cudaStream_t stream) {
     static SmemOptIn optin;
     if (cudaError_t e = optin.ensure(reinterpret_cast<const void*>(mlp_kernel<OP>), kSmemBytes)) return e;
-    const long long grid = prm.tiles < num_sms ? prm.tiles : num_sms;
-    mlp_kernel<OP><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(maps, prm);
+    const unsigned int grid = prm.tiles < static_cast<unsigned>(num_sms) ? prm.tiles : num_sms;
+    mlp_kernel<OP><<<grid, threads_of(OP), kSmemBytes, stream>>>(maps, prm);
     return cudaGetLastError();
 }
 
@@ -575,7 +581,8 @@ cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     prm.k = C;
     prm.bn = tile_width(F, 128, 32);
     prm.tiles_n = (F + prm.bn - 1) / prm.bn;
-    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
+    prm.by_n = make_fastdiv(prm.tiles_n);
     prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_gate);
     prm.bias1 = static_cast<const __nv_bfloat16*>(p.b_up);
     if (encode_matrix(&maps.a[0], p.x, T, C, kBlockM, kBlockK, true) ||
@@ -589,7 +596,8 @@ cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     prm.k = F;
     prm.bn = tile_width(C, 256, 32);
     prm.tiles_n = (C + prm.bn - 1) / prm.bn;
-    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
+    prm.by_n = make_fastdiv(prm.tiles_n);
     prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_down);
     if (encode_matrix(&maps.a[0], p.ws, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.b[0], p.w_down, C, F, prm.bn, kBlockK, true) ||
@@ -616,7 +624,8 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     prm.k = C;
     prm.bn = 64;
     prm.tiles_n = (F + 63) / 64;
-    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
+    prm.by_n = make_fastdiv(prm.tiles_n);
     prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_gate);
     prm.bias1 = static_cast<const __nv_bfloat16*>(p.b_up);
     if (encode_matrix(&maps.a[0], p.x, T, C, kBlockM, kBlockK, true) ||
@@ -635,7 +644,8 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     prm.segments = 2;
     prm.bn = tile_width(C, 256, 64);
     prm.tiles_n = (C + prm.bn - 1) / prm.bn;
-    prm.tiles = static_cast<long long>(rows_m) * prm.tiles_n;
+    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
+    prm.by_n = make_fastdiv(prm.tiles_n);
     if (encode_matrix(&maps.a[0], dg, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.a[1], du, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.b[0], p.w_gate, F, C, kBlockK, 64, true) ||
@@ -655,6 +665,7 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
         q.n = i == 2 ? F : C;
         q.tiles_n = (q.n + prm.bn - 1) / prm.bn;
         q.tiles = (q.m + kBlockM - 1) / kBlockM * q.tiles_n;
+        q.by_n = make_fastdiv(q.tiles_n);
         q.first = first;
         first += q.tiles;
         q.part = reinterpret_cast<float*>(p.ws + L.part[i]);
@@ -666,7 +677,8 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     const int kblocks = (T + kBlockK - 1) / kBlockK;
     prm.splits = pick_splits(first, kblocks, num_sms);
     prm.blocks_per_split = (kblocks + prm.splits - 1) / prm.splits;
-    prm.tiles = static_cast<long long>(first) * prm.splits;
+    prm.tiles = static_cast<unsigned>(first) * prm.splits;
+    prm.by_splits = make_fastdiv(prm.splits);
     if ((e = launch<kDw>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
     SumParams sum{};
     sum.splits = prm.splits;
