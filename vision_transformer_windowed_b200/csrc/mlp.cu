@@ -120,36 +120,43 @@ __device__ __forceinline__ unsigned long long pair_of(float x) { return pair(x, 
 //   erf(z) = 1 - (1 + a1 z + ... + a6 z^6)^-16, z >= 0 (absolute error 3e-7, far below
 // the result's bf16 step): one reciprocal and no exponential; large z overflow to a
 // reciprocal of zero, the limit.
+// Four pairs at a time, step by step beside each other: one pair's steps depend on each
+// other.
 template <bool kSlope>
-__device__ __forceinline__ void activate(unsigned long long g, int act, unsigned long long& a, unsigned long long& slope) {
-    float x, y;
+__device__ __forceinline__ void activate(const unsigned long long* g, int act, unsigned long long (&a)[4],
+                                         unsigned long long (&slope)[4]) {
+#define EACH _Pragma("unroll") for (int i = 0; i < 4; ++i)
+    float x[4], y[4];
     if (act == 0) {
-        unpair(mul_pair(g, pair_of(-1.4426950408889634f)), x, y);
-        unpair(add_pair(pair(ex2_approx(x), ex2_approx(y)), pair_of(1.f)), x, y);
-        const unsigned long long s = pair(rcp_approx(x), rcp_approx(y));
-        a = mul_pair(g, s);
-        if (kSlope) slope = fma_pair(a, fma_pair(s, pair_of(-1.f), pair_of(1.f)), s);
+        EACH unpair(mul_pair(g[i], pair_of(-1.4426950408889634f)), x[i], y[i]);
+        EACH unpair(add_pair(pair(ex2_approx(x[i]), ex2_approx(y[i])), pair_of(1.f)), x[i], y[i]);
+        unsigned long long s[4];
+        EACH s[i] = pair(rcp_approx(x[i]), rcp_approx(y[i]));
+        EACH a[i] = mul_pair(g[i], s[i]);
+        if (kSlope) EACH slope[i] = fma_pair(a[i], fma_pair(s[i], pair_of(-1.f), pair_of(1.f)), s[i]);
         return;
     }
-    const unsigned long long z = mul_pair(g & 0x7FFFFFFF7FFFFFFFull, pair_of(0.70710678118654752f));
-    unsigned long long p = fma_pair(z, pair_of(0.0000430638f), pair_of(0.0002765672f));
-    p = fma_pair(p, z, pair_of(0.0001520143f));
-    p = fma_pair(p, z, pair_of(0.0092705272f));
-    p = fma_pair(p, z, pair_of(0.0422820123f));
-    p = fma_pair(p, z, pair_of(0.0705230784f));
-    p = fma_pair(p, z, pair_of(1.f));
-    p = mul_pair(p, p);
-    p = mul_pair(p, p);
-    p = mul_pair(p, p);
-    p = mul_pair(p, p);
-    unpair(p, x, y);
-    const unsigned long long half = fma_pair(pair(rcp_approx(x), rcp_approx(y)), pair_of(-0.5f), pair_of(0.5f));
-    const unsigned long long cdf = add_pair(half | (g & 0x8000000080000000ull), pair_of(0.5f));  // half >= 0
-    a = mul_pair(g, cdf);
+    unsigned long long z[4], p[4];
+    EACH z[i] = mul_pair(g[i] & 0x7FFFFFFF7FFFFFFFull, pair_of(0.70710678118654752f));
+    EACH p[i] = fma_pair(z[i], pair_of(0.0000430638f), pair_of(0.0002765672f));
+    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0001520143f));
+    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0092705272f));
+    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0422820123f));
+    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0705230784f));
+    EACH p[i] = fma_pair(p[i], z[i], pair_of(1.f));
+    EACH p[i] = mul_pair(p[i], p[i]);
+    EACH p[i] = mul_pair(p[i], p[i]);
+    EACH p[i] = mul_pair(p[i], p[i]);
+    EACH p[i] = mul_pair(p[i], p[i]);
+    EACH unpair(p[i], x[i], y[i]);
+    EACH p[i] = fma_pair(pair(rcp_approx(x[i]), rcp_approx(y[i])), pair_of(-0.5f), pair_of(0.5f));  // >= 0
+    EACH p[i] = add_pair(p[i] | (g[i] & 0x8000000080000000ull), pair_of(0.5f));                     // Phi(g)
+    EACH a[i] = mul_pair(g[i], p[i]);
     if (kSlope) {
-        unpair(mul_pair(mul_pair(g, g), pair_of(-0.72134752044448170f)), x, y);
-        slope = fma_pair(mul_pair(g, pair_of(0.39894228040143268f)), pair(ex2_approx(x), ex2_approx(y)), cdf);
+        EACH unpair(mul_pair(mul_pair(g[i], g[i]), pair_of(-0.72134752044448170f)), x[i], y[i]);
+        EACH slope[i] = fma_pair(mul_pair(g[i], pair_of(0.39894228040143268f)), pair(ex2_approx(x[i]), ex2_approx(y[i])), p[i]);
     }
+#undef EACH
 }
 
 // Adds 32 bias columns, one a lane, to every lane's row of 32: through the warp's
@@ -437,21 +444,25 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         if (prm.bias1) add_bias(u, wbias, b1, lane);
                         if (OP == kGate) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                unsigned long long f, s;
-                                activate<false>(a[e], prm.act, f, s);
-                                a[e] = mul_pair(f, u[e]);
+                            for (int e = 0; e < 16; e += 4) {
+                                unsigned long long f[4], s[4];
+                                activate<false>(a + e, prm.act, f, s);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) a[e + i] = mul_pair(f[i], u[e + i]);
                             }
                         } else {
                             unsigned long long dh[16];
                             cd.get(dh);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                unsigned long long f, s;
-                                activate<true>(a[e], prm.act, f, s);
-                                a[e] = mul_pair(f, u[e]);
-                                u[e] = mul_pair(mul_pair(dh[e], u[e]), s);  // dg
-                                dh[e] = mul_pair(dh[e], f);                 // du
+                            for (int e = 0; e < 16; e += 4) {
+                                unsigned long long f[4], s[4];
+                                activate<true>(a + e, prm.act, f, s);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    a[e + i] = mul_pair(f[i], u[e + i]);
+                                    u[e + i] = mul_pair(mul_pair(dh[e + i], u[e + i]), s[i]);  // dg
+                                    dh[e + i] = mul_pair(dh[e + i], f[i]);                     // du
+                                }
                             }
                             put(&maps.out[1], u, col, row0);
                             put(&maps.out[2], dh, col, row0);
