@@ -168,13 +168,14 @@ struct ResnormShape {
     int pre, post;  // 0 none, 1 layer norm, 2 rms norm
     float eps;
     double drop_p;
-    // Sixteen-byte accesses: the channel count divides by 8 and every tensor is aligned.
+    // Sixteen-byte accesses: every tensor is aligned, and a row that starts anywhere in
+    // a chunk of eight channels takes at most 1024 chunks.
     bool wide(const ResnormPtrs& p) const {
         const void* all[] = {p.x,  p.f,  p.scale, p.post_w, p.post_b, p.pre_w, p.pre_b,
                              p.r,  p.n,  p.dr,    p.dn,     p.dx,     p.df};
         uintptr_t bits = 0;
         for (const void* q : all) bits |= reinterpret_cast<uintptr_t>(q);
-        return channels % 8 == 0 && (bits & 15u) == 0;
+        return (bits & 15u) == 0 && (channels % 8 == 0 || channels <= 8192 - 14);
     }
 };
 size_t resnorm_bwd_workspace_bytes(const ResnormShape& sh);

@@ -9,33 +9,36 @@ namespace fswin {
 
 namespace resn {
 
-constexpr int kThreads = 256;
-
-template <typename TX, int W, int L, int V>
-__global__ void __launch_bounds__(L > 32 ? L : kThreads) fwd_kernel(const __grid_constant__ Params prm) {
-    __shared__ float scratch[L > 32 ? L / 32 : 1];
+template <typename TX, int W, int L, int V, bool S>
+__global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W * V <= 16 ? 3 : 2) : 1)
+    fwd_kernel(const __grid_constant__ Params prm) {
+    __shared__ float scratch[kScratch];
     const ResnormPtrs& p = prm.p;
-    constexpr int kGroups = L > 32 ? 1 : kThreads / L;
-    const int lane = L > 32 ? threadIdx.x : threadIdx.x % L;
-    Row<W, L, V> g;
-    g.init(lane, prm.C);
+    constexpr int kGroups = groups_of<L>();
+    const unsigned int own = threadIdx.x / L;
+    // the same for all rows of this group (grid_of)
+    const int shift = !S ? 0 : static_cast<int>((static_cast<unsigned long long>(blockIdx.x * kGroups + own) * prm.C) & 7u);
+    Row<W, L, V, S> g;
+    g.init(threadIdx.x % L, prm.C, shift);
     unsigned long long seed = 0, offset = 0;
     if (prm.drop) {
         seed = static_cast<unsigned long long>(p.rng[0]);
         offset = static_cast<unsigned long long>(p.rng[1]);
     }
     const TX* gate = static_cast<const TX*>(p.gate);
-    const unsigned int own = L > 32 ? 0 : threadIdx.x / L;
     // whole warps stay in the loop together: their reductions need every lane
     for (unsigned int base = blockIdx.x * kGroups; base < prm.rows; base += gridDim.x * kGroups) {
         const unsigned int row = base + own;
         const bool live = row < prm.rows;
+        // rows past the last are formed from the last one's, and not stored; a shifted
+        // group must not read a row of another shift
         const unsigned int at_row = live ? row : prm.rows - 1u;
         const long long at = static_cast<long long>(at_row) * prm.C;
         float x[W * V], y[W * V];
-        g.load(static_cast<const TX*>(p.x) + at, x);
+        if (S) g.zero(x);
+        if (!S || live) g.load(static_cast<const TX*>(p.x) + at, x);
         const float gt = gate ? static_cast<float>(gate[fdiv(prm.tokens, at_row)]) : 1.f;
-        if (gt != 0.f) {
+        if (gt != 0.f && (!S || live)) {
             g.load(static_cast<const __nv_bfloat16*>(p.f) + at, y);
         } else {  // a dropped sample takes nothing from its branch, whatever that holds
 #pragma unroll
@@ -45,25 +48,22 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) fwd_kernel(const __grid
             normalise(g, y, prm.post, prm, scratch);
             float w[W * V];
             if (p.post_w) {
-                g.load(static_cast<const TX*>(p.post_w), w);
+                g.load(static_cast<const TX*>(p.post_w), w, !S);
 #pragma unroll
                 for (int e = 0; e < W * V; ++e) y[e] *= w[e];
             }
             if (p.post_b) {
-                g.load(static_cast<const TX*>(p.post_b), w);
+                g.load(static_cast<const TX*>(p.post_b), w, !S);
 #pragma unroll
                 for (int e = 0; e < W * V; ++e) y[e] += w[e];
             }
         }
         if (prm.drop) {
-            float k[W * V];
-            g.mask(prm, at_row, seed, offset, k);
-#pragma unroll
-            for (int e = 0; e < W * V; ++e) y[e] = k[e] != 0.f ? y[e] * k[e] : 0.f;
+            drop(y, g.mask(prm, at_row, seed, offset), prm.keep_scale);
         }
         if (p.scale) {
             float w[W * V];
-            g.load(static_cast<const TX*>(p.scale), w);
+            g.load(static_cast<const TX*>(p.scale), w, !S);
 #pragma unroll
             for (int e = 0; e < W * V; ++e) y[e] *= w[e];
         }
@@ -76,12 +76,12 @@ __global__ void __launch_bounds__(L > 32 ? L : kThreads) fwd_kernel(const __grid
         // the norm takes the sum before it is rounded to the stream's type
         normalise(g, x, prm.pre, prm, scratch);
         if (p.pre_w) {
-            g.load(static_cast<const TX*>(p.pre_w), y);
+            g.load(static_cast<const TX*>(p.pre_w), y, !S);
 #pragma unroll
             for (int e = 0; e < W * V; ++e) x[e] *= y[e];
         }
         if (p.pre_b) {
-            g.load(static_cast<const TX*>(p.pre_b), y);
+            g.load(static_cast<const TX*>(p.pre_b), y, !S);
 #pragma unroll
             for (int e = 0; e < W * V; ++e) x[e] += y[e];
         }
@@ -94,39 +94,49 @@ struct Launch {
     const Params& prm;
     int num_sms;
     cudaStream_t stream;
-    template <int W, int L, int V>
+    template <int W, int L, int V, bool S>
     cudaError_t go() const {
-        constexpr int threads = L > 32 ? L : kThreads, groups = L > 32 ? 1 : kThreads / L;
-        const long long blocks = (static_cast<long long>(prm.rows) + groups - 1) / groups;
-        const long long most = static_cast<long long>(num_sms) * (2048 / threads);
-        fwd_kernel<TX, W, L, V><<<static_cast<unsigned>(blocks < most ? blocks : most), threads, 0, stream>>>(prm);
+        const unsigned grid = grid_of(prm.rows, groups_of<L>(), static_cast<unsigned>(num_sms) * (2048 / threads_of<L>()), prm.C);
+        fwd_kernel<TX, W, L, V, S><<<grid, threads_of<L>(), 0, stream>>>(prm);
         return cudaGetLastError();
     }
     // Row shapes: eight-channel chunks, at most four a lane, the fewest idle lanes
     // for the channel counts of Swin stages (96 k: chunks divide by 12).
     cudaError_t wide() const {
         const int n = prm.C / 8;
-        if (n <= 4) return go<8, 4, 1>();
-        if (n <= 8) return go<8, 4, 2>();
-        if (n <= 12) return go<8, 4, 3>();
-        if (n <= 16) return go<8, 8, 2>();
-        if (n <= 24) return go<8, 8, 3>();
-        if (n <= 32) return go<8, 16, 2>();
-        if (n <= 48) return go<8, 16, 3>();
-        if (n <= 64) return go<8, 32, 2>();
-        if (n <= 96) return go<8, 32, 3>();
-        if (n <= 128) return go<8, 32, 4>();
-        if (n <= 256) return go<8, 64, 4>();
-        if (n <= 512) return go<8, 128, 4>();
-        return go<8, 256, 4>();
+        if (n <= 4) return go<8, 4, 1, false>();
+        if (n <= 8) return go<8, 4, 2, false>();
+        if (n <= 12) return go<8, 4, 3, false>();
+        if (n <= 16) return go<8, 8, 2, false>();
+        if (n <= 24) return go<8, 8, 3, false>();
+        if (n <= 32) return go<8, 16, 2, false>();
+        if (n <= 48) return go<8, 16, 3, false>();
+        if (n <= 64) return go<8, 32, 2, false>();
+        if (n <= 96) return go<8, 32, 3, false>();
+        if (n <= 128) return go<8, 32, 4, false>();
+        if (n <= 256) return go<8, 64, 4, false>();
+        if (n <= 512) return go<8, 128, 4, false>();
+        return go<8, 256, 4, false>();
+    }
+    cudaError_t shifted() const {  // one chunk more than the channels fill
+        const int n = (prm.C + 14) / 8;
+        if (n <= 8) return go<8, 8, 1, true>();
+        if (n <= 32) return go<8, 32, 1, true>();
+        if (n <= 128) return go<8, 128, 1, true>();
+        if (n <= 512) return go<8, 256, 2, true>();
+        return go<8, 256, 4, true>();
     }
     cudaError_t narrow() const {
         const int n = prm.C;
-        if (n <= 32) return go<1, 8, 4>();
-        if (n <= 128) return go<1, 32, 4>();
-        if (n <= 512) return go<1, 128, 4>();
-        if (n <= 2048) return go<1, 256, 8>();
-        return go<1, 1024, 8>();
+        if (n <= 32) return go<1, 8, 4, false>();
+        if (n <= 128) return go<1, 32, 4, false>();
+        if (n <= 512) return go<1, 128, 4, false>();
+        if (n <= 2048) return go<1, 256, 8, false>();
+        return go<1, 1024, 8, false>();
+    }
+    cudaError_t run(bool wide_rows) const {
+        if (!wide_rows) return narrow();
+        return prm.C % 8 ? shifted() : wide();
     }
 };
 
@@ -137,12 +147,8 @@ cudaError_t launch_resnorm_fwd(const ResnormShape& sh, const ResnormPtrs& p, int
     Params prm{};
     fill_params(sh, p, &prm);
     const bool wide = sh.wide(p);
-    if (sh.stream_f32) {
-        const Launch<float> l{prm, num_sms, stream};
-        return wide ? l.wide() : l.narrow();
-    }
-    const Launch<__nv_bfloat16> l{prm, num_sms, stream};
-    return wide ? l.wide() : l.narrow();
+    if (sh.stream_f32) return Launch<float>{prm, num_sms, stream}.run(wide);
+    return Launch<__nv_bfloat16>{prm, num_sms, stream}.run(wide);
 }
 
 }  // namespace fswin

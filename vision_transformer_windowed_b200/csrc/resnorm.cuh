@@ -56,109 +56,210 @@ __device__ __forceinline__ uint4 philox(unsigned long long counter, unsigned lon
 
 // ---------------------------------------------------------------- rows in registers
 // A row is held by a group of L lanes, V chunks of W channels a lane: chunk
-// lane + L i.  W = 8 (16-byte bf16 accesses) where the channel count and every
-// pointer allow it, else W = 1.  `has` bit i: chunk i lies inside the row; the
-// others read as zero and are not written.
-template <int W, int L, int V>
+// lane + L i.  W = 8: 16-byte bf16 accesses (every tensor 16-byte aligned).  Where the
+// channel count is no multiple of 8 a row starts `shift` elements behind a 16-byte
+// boundary; its chunks then start at that boundary, and its first and last are
+// partly another row's (read and written element by element).  A group only walks rows
+// of one shift, so that its lanes always hold the same channels.  W = 1: tensors at any
+// element.  Elements outside the row read as zero and are not written.  S: rows that
+// may be shifted; the others' kernels are free of the element-wise accesses, which keep
+// the loads of a row from being issued together (forward of 12544 x 16 rows of 96
+// channels 80 -> 130 us with them).
+template <int W, int L, int V, bool S>
 struct Row {
     static constexpr int E = W * V;
     int col[V];
-    unsigned int has;
-    __device__ __forceinline__ void init(int lane, int C) {
-        has = 0;
+    int C;
+    unsigned int full, edge;  // chunks wholly, and (S) partly, inside the row
+    __device__ __forceinline__ void init(int lane, int channels, int shift) {
+        C = channels;
+        full = edge = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            col[i] = (lane + L * i) * W;
-            if (col[i] < C) has |= 1u << i;
+            col[i] = (lane + L * i) * W - (S ? shift : 0);
+            if (col[i] >= 0 && col[i] + W <= C) full |= 1u << i;
+            else if (S && col[i] + W > 0 && col[i] < C) edge |= 1u << i;
         }
     }
-    __device__ __forceinline__ bool in(int i) const { return (has >> i) & 1u; }
+    __device__ __forceinline__ bool in(int e) const {  // element e of the lane's
+        const int i = e / W;
+        return ((full >> i) & 1u) || (S && ((edge >> i) & 1u) && col[i] + e % W >= 0 && col[i] + e % W < C);
+    }
 
+    __device__ __forceinline__ static void zero(float (&x)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+    }
+
+    // aligned: the row's chunks are 16-byte aligned in this tensor (parameters of a
+    // shifted row are not)
     template <typename T>
-    __device__ __forceinline__ void load(const T* row, float (&x)[E], float fill = 0.f) const {
+    __device__ __forceinline__ void load(const T* row, float (&x)[E], bool aligned = true) const {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) x[i * W + e] = fill;
-            if (!in(i)) continue;
+            for (int e = 0; e < W; ++e) x[i * W + e] = 0.f;
             if constexpr (W == 1) {
-                x[i] = static_cast<float>(row[col[i]]);
-            } else if constexpr (sizeof(T) == 2) {
-                const uint4 v = *reinterpret_cast<const uint4*>(row + col[i]);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if ((full >> i) & 1u) x[i] = static_cast<float>(row[col[i]]);
+            } else if (((full >> i) & 1u) && (!S || aligned)) {
+                if constexpr (sizeof(T) == 2) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(row + col[i]);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[i * W + 2 * e] = bf16lo_to_f32(w[e]);
-                    x[i * W + 2 * e + 1] = bf16hi_to_f32(w[e]);
-                }
-            } else {
+                    for (int e = 0; e < 4; ++e) {
+                        x[i * W + 2 * e] = bf16lo_to_f32(w[e]);
+                        x[i * W + 2 * e + 1] = bf16hi_to_f32(w[e]);
+                    }
+                } else {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 v = *reinterpret_cast<const float4*>(row + col[i] + 4 * q);
-                    x[i * W + 4 * q] = v.x;
-                    x[i * W + 4 * q + 1] = v.y;
-                    x[i * W + 4 * q + 2] = v.z;
-                    x[i * W + 4 * q + 3] = v.w;
+                    for (int q = 0; q < 2; ++q) {
+                        const float4 v = *reinterpret_cast<const float4*>(row + col[i] + 4 * q);
+                        x[i * W + 4 * q] = v.x;
+                        x[i * W + 4 * q + 1] = v.y;
+                        x[i * W + 4 * q + 2] = v.z;
+                        x[i * W + 4 * q + 3] = v.w;
+                    }
                 }
+            } else if (S && (((full | edge) >> i) & 1u)) {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (col[i] + e >= 0 && col[i] + e < C) x[i * W + e] = static_cast<float>(row[col[i] + e]);
             }
         }
     }
     template <typename T>
-    __device__ __forceinline__ void store(T* row, const float (&x)[E]) const {
+    __device__ __forceinline__ void store(T* row, const float (&x)[E], bool aligned = true) const {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (!in(i)) continue;
+            const float* y = x + i * W;
             if constexpr (W == 1) {
-                row[col[i]] = static_cast<T>(x[i]);
-            } else if constexpr (sizeof(T) == 2) {
-                const float* y = x + i * W;
-                *reinterpret_cast<uint4*>(row + col[i]) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                                     pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            } else {
-                const float* y = x + i * W;
-                *reinterpret_cast<float4*>(row + col[i]) = make_float4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<float4*>(row + col[i] + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                if ((full >> i) & 1u) row[col[i]] = static_cast<T>(x[i]);
+            } else if (((full >> i) & 1u) && (!S || aligned)) {
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint4*>(row + col[i]) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                                         pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                } else {
+                    *reinterpret_cast<float4*>(row + col[i]) = make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<float4*>(row + col[i] + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                }
+            } else if (S && (((full | edge) >> i) & 1u)) {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (col[i] + e >= 0 && col[i] + e < C) row[col[i] + e] = static_cast<T>(y[e]);
             }
         }
     }
-    // Factors keep_scale or 0 of the row's elements.
-    __device__ __forceinline__ void mask(const Params& prm, unsigned int row, unsigned long long seed,
-                                         unsigned long long offset, float (&k)[E]) const {
+    // v in elements of the row, 0 outside it.
+    __device__ __forceinline__ float inside(int e, float v) const {
+        if constexpr (S) return in(e) ? v : 0.f;
+        else return ((full >> (e / W)) & 1u) ? v : 0.f;
+    }
+
+    // Bit e: element e of the lane's is kept.
+    __device__ __forceinline__ uint32_t mask(const Params& prm, unsigned int row, unsigned long long seed,
+                                             unsigned long long offset) const {
+        static_assert(E <= 32, "a bit an element");
+        uint32_t bits = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const unsigned long long at = static_cast<unsigned long long>(row) * prm.C + col[i];
+            // a partly foreign first chunk starts in the row before: row C + col is never negative
+            const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(row) * prm.C + col[i]);
             if constexpr (W == 1) {
                 const uint4 w = philox(at >> 2, offset, seed);
                 const uint32_t s = static_cast<uint32_t>(at) & 3u;
                 const uint32_t word = s == 0 ? w.x : (s == 1 ? w.y : (s == 2 ? w.z : w.w));
-                k[i] = word >= prm.thr ? prm.keep_scale : 0.f;
-            } else {  // C is a multiple of 8, so the chunk starts at a multiple of 8
+                if (word >= prm.thr) bits |= 1u << i;
+            } else {  // chunks start at multiples of 8
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint4 w = philox((at >> 2) + q, offset, seed);
-                    k[i * W + 4 * q] = w.x >= prm.thr ? prm.keep_scale : 0.f;
-                    k[i * W + 4 * q + 1] = w.y >= prm.thr ? prm.keep_scale : 0.f;
-                    k[i * W + 4 * q + 2] = w.z >= prm.thr ? prm.keep_scale : 0.f;
-                    k[i * W + 4 * q + 3] = w.w >= prm.thr ? prm.keep_scale : 0.f;
+                    if (w.x >= prm.thr) bits |= 1u << (i * W + 4 * q);
+                    if (w.y >= prm.thr) bits |= 2u << (i * W + 4 * q);
+                    if (w.z >= prm.thr) bits |= 4u << (i * W + 4 * q);
+                    if (w.w >= prm.thr) bits |= 8u << (i * W + 4 * q);
                 }
             }
+        }
+        return bits;
+    }
+};
+// x of the kept elements times keep_scale, 0 (whatever x holds) of the dropped ones.
+template <int E>
+__device__ __forceinline__ void drop(float (&x)[E], uint32_t bits, float keep_scale) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = (bits >> e) & 1u ? x[e] * keep_scale : 0.f;
+}
+
+// A bf16 row as it was loaded, until its values are wanted: half the registers.
+template <int W, int L, int V, bool S>
+struct Held {
+    static constexpr bool kRaw = W == 8 && !S;
+    uint4 raw[kRaw ? V : 1];
+    float x[kRaw ? 1 : W * V];
+    __device__ __forceinline__ void zero() {
+        if constexpr (kRaw) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            Row<W, L, V, S>::zero(x);
+        }
+    }
+    __device__ __forceinline__ void load(const Row<W, L, V, S>& g, const __nv_bfloat16* row) {
+        if constexpr (kRaw) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if ((g.full >> i) & 1u) raw[i] = *reinterpret_cast<const uint4*>(row + g.col[i]);
+            }
+        } else {
+            g.load(row, x);
+        }
+    }
+    __device__ __forceinline__ void take(float (&y)[W * V]) const {
+        if constexpr (kRaw) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[i * W + 2 * e] = bf16lo_to_f32(w[e]);
+                    y[i * W + 2 * e + 1] = bf16hi_to_f32(w[e]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < W * V; ++e) y[e] = x[e];
         }
     }
 };
 
-// Sum of a value over the L lanes of a row, the same in every lane.  Groups of
-// more than a warp are the whole block.
+constexpr int kThreads = 256;  // of a block, or L where a row takes more
+template <int L>
+__host__ __device__ constexpr int threads_of() {
+    return L > kThreads ? L : kThreads;
+}
+template <int L>
+__host__ __device__ constexpr int groups_of() {
+    return threads_of<L>() / L;
+}
+// Shared floats of the row sums: one a warp.
+constexpr int kScratch = 32;
+
+// Sum of a value over the L lanes of a row, the same in every lane; groups of several
+// warps meet at a barrier of their own.
 template <int L>
 __device__ __forceinline__ float row_sum(float v, float* scratch) {
 #pragma unroll
     for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if constexpr (L > 32) {
-        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-        __syncthreads();
+        constexpr int kWarps = L / 32;
+        const int group = threadIdx.x / L, warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) scratch[warp] = v;
+        named_bar_sync(1 + group, L);
         v = 0.f;
 #pragma unroll
-        for (int w = 0; w < L / 32; ++w) v += scratch[w];
-        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) v += scratch[group * kWarps + w];
+        named_bar_sync(1 + group, L);
     }
     return v;
 }
@@ -166,8 +267,8 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 // Normalises a row in place of `x` (chunks outside the row stay zero) and returns
 // 1 / deviation: mean and centred squares in two passes over registers, so a large
 // mean costs no digits.
-template <int W, int L, int V>
-__device__ __forceinline__ float normalise(const Row<W, L, V>& g, float (&x)[W * V], int kind, const Params& prm,
+template <int W, int L, int V, bool S>
+__device__ __forceinline__ float normalise(const Row<W, L, V, S>& g, float (&x)[W * V], int kind, const Params& prm,
                                            float* scratch) {
     if (kind == kLayer) {
         float s = 0.f;
@@ -175,7 +276,7 @@ __device__ __forceinline__ float normalise(const Row<W, L, V>& g, float (&x)[W *
         for (int e = 0; e < W * V; ++e) s += x[e];
         const float mean = row_sum<L>(s, scratch) * prm.inv_c;
 #pragma unroll
-        for (int e = 0; e < W * V; ++e) x[e] = g.in(e / W) ? x[e] - mean : 0.f;
+        for (int e = 0; e < W * V; ++e) x[e] -= g.inside(e, mean);  // x is 0 outside
     }
     float q = 0.f;
 #pragma unroll
@@ -189,6 +290,20 @@ __device__ __forceinline__ float normalise(const Row<W, L, V>& g, float (&x)[W *
 // Blocks of the backward, each with a partial sum of the parameters' gradients:
 // two a SM of a B200.
 constexpr int kMaxBwdBlocks = 2 * 148;
+
+// Rows of one shift follow each other at this distance: a row starts (row C) mod 8
+// elements behind a 16-byte boundary.
+inline unsigned int shift_period(int C) { return C % 8 == 0 ? 1u : (C % 4 == 0 ? 2u : (C % 2 == 0 ? 4u : 8u)); }
+
+// Blocks for `rows` rows, `groups` a block: at most `most` (rounded down), a multiple of
+// what keeps every group at one shift.
+inline unsigned int grid_of(unsigned int rows, int groups, unsigned int most, int C) {
+    const unsigned int period = shift_period(C), step = period / static_cast<unsigned>(groups) > 1 ? period / groups : 1u;
+    unsigned int n = (rows + groups - 1) / groups;
+    n = (n + step - 1) / step * step;
+    const unsigned int cap = most / step * step;
+    return n < cap ? n : cap;
+}
 
 inline void fill_params(const ResnormShape& sh, const ResnormPtrs& p, Params* out) {
     out->p = p;
