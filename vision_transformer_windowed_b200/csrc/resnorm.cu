@@ -27,12 +27,6 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W 
     }
     const TX* gate = static_cast<const TX*>(p.gate);
     // whole warps stay in the loop together: their reductions need every lane
-    // the gate of the group's row in the block at `base`, loaded a row ahead: f is read or not by it
-    auto gate_of = [&](unsigned int base) {
-        const unsigned int row = base + own < prm.rows ? base + own : prm.rows - 1u;
-        return gate ? static_cast<float>(gate[fdiv(prm.tokens, row)]) : 1.f;
-    };
-    float gt_next = gate_of(blockIdx.x * kGroups);
     for (unsigned int base = blockIdx.x * kGroups; base < prm.rows; base += gridDim.x * kGroups) {
         const unsigned int row = base + own;
         const bool live = row < prm.rows;
@@ -43,8 +37,7 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W 
         float x[W * V], y[W * V];
         if (S) g.zero(x);
         if (!S || live) g.load(static_cast<const TX*>(p.x) + at, x);
-        const float gt = gt_next;
-        gt_next = gate_of(base + gridDim.x * kGroups);
+        const float gt = gate ? static_cast<float>(gate[fdiv(prm.tokens, at_row)]) : 1.f;
         if (gt != 0.f && (!S || live)) {
             g.load(static_cast<const __nv_bfloat16*>(p.f) + at, y);
         } else {  // a dropped sample takes nothing from its branch, whatever that holds

@@ -113,12 +113,6 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 24 ? 2 :
     for (int k = 0; k < kGrads; ++k)
         if (wanted[k]) slot(k).clear();
 
-    // the gate of the group's row in the block at `base`, loaded a row ahead: f is read or not by it
-    auto gate_of = [&](unsigned int base) {
-        const unsigned int row = base + own < prm.rows ? base + own : prm.rows - 1u;
-        return gate ? static_cast<float>(gate[fdiv(prm.tokens, row)]) : 1.f;
-    };
-    float gt_next = gate_of(blockIdx.x * kGroups);
     for (unsigned int base = blockIdx.x * kGroups; base < prm.rows; base += gridDim.x * kGroups) {
         const unsigned int row = base + own;
         const bool live = row < prm.rows;
@@ -129,8 +123,7 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 24 ? 2 :
         const long long at = static_cast<long long>(at_row) * prm.C;
         float d[E];  // dr', in the end dx
         Held<W, L, V, S> f, dn;
-        const float gt = gt_next;
-        gt_next = gate_of(base + gridDim.x * kGroups);
+        const float gt = gate ? static_cast<float>(gate[fdiv(prm.tokens, at_row)]) : 1.f;
         g.zero(d);
         if (live && p.dr) g.load(static_cast<const TX*>(p.dr) + at, d);
         if (reads && branch && (gt != 0.f || p.dgate)) f.load(g, static_cast<const __nv_bfloat16*>(p.f) + at);
