@@ -14,9 +14,12 @@
 //   kLinear: y = h Wd^T + bd
 //   kGrad:   g, u again, dh = dy Wd; h, dg = dh o u o act'(g), du = dh o act(g)
 //   kDx:     dx = dg Wg + du Wu, one contraction over both
-//   kDw:     dWg = dg^T x, dWu = du^T x, dWd = dy^T h, the tokens split over CTAs with
-//            fp32 partial results that a second kernel adds in order; a 16-column
-//            product with a tile of ones gives the bias gradients
+//   kDw:     dWg = dg^T x, dWu = du^T x, dWd^T = h^T dy, the tokens split over CTAs with
+//            fp32 partial results that a second kernel adds in order; 16-column
+//            products with a tile of ones give dg's and du's bias gradients, two
+//            warps add up dy's columns as they pass.  Tiles of 256 x 192, both
+//            accumulators to one: the copies into shared memory bound this product,
+//            and a larger tile reads less
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,18 +43,18 @@ constexpr int kABytes = kBlockM * kBlockK * 2;
 constexpr int kStages = 4;                        // at most
 constexpr int kDwMaxN = 192;
 // A stage: A, and B of up to 256 rows; kGrad: x, three times 64 weight rows, dy; kDw:
-// A and up to 192 columns.
+// twice A's rows and up to 192 columns.
 __host__ __device__ constexpr int stage_bytes(int op) {
-    return op == kGrad ? 2 * kABytes + 3 * 8192 : (op == kDw ? kABytes + kDwMaxN * 128 : 3 * kABytes);
+    return op == kGrad ? 2 * kABytes + 3 * 8192 : (op == kDw ? 2 * kABytes + kDwMaxN * 128 : 3 * kABytes);
 }
-__host__ __device__ constexpr int stages_of(int op) { return op == kGrad ? 3 : kStages; }
+__host__ __device__ constexpr int stages_of(int op) { return op == kGrad || op == kDw ? 3 : kStages; }
 constexpr int kStoreBytes = 32 * 64;              // a warp's 32 rows x 32 bf16 columns
 constexpr int kRingBytes = 12 * kABytes;
-constexpr int kOnesOff = kStages * (kABytes + kDwMaxN * 128);  // kDw: 16 rows x 64 of 1.0 behind its ring
+constexpr int kOnesOff = stages_of(kDw) * stage_bytes(kDw);  // kDw: 16 rows x 64 of 1.0 behind its ring
 constexpr int kOnesBytes = 2048;
 constexpr int kStoreOff = kRingBytes;
 constexpr int kBarOff = kStoreOff + 16 * kStoreBytes;
-constexpr uint32_t kColOnes = 240;                 // bias gradient columns of kDw
+constexpr uint32_t kColOnes = 240;                // bias gradient columns of kDw, beside each half's
 
 struct Bars {
     uint64_t full[kStages], free_[kStages], acc_full[2], acc_free[2], done;
@@ -66,15 +69,16 @@ static_assert(stage_bytes(kGrad) % 1024 == 0 && stage_bytes(kDw) % 1024 == 0 && 
 static_assert(sizeof(Bars) <= 256, "barrier block overflows its slot");
 static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may have");
 
-struct Maps {
-    CUtensorMap a[3], b[3], out[3];
+struct Problem {       // kDw: one of the three weight gradients
+    int m, n, tiles_n, first;  // first: its first tile in the launch
+    FastDiv by_n;      // tiles_n
+    int turned;        // the result lies as [n][m], and the bias gradient is of the n columns
+    float* part;       // [splits][m][n], or [splits][n][m]
+    float* bias_part;  // [splits][m], or [splits][2][n]; or null
 };
 
-struct Problem {       // kDw: one of the three weight gradients
-    int m, n, tiles_n, tiles, first;  // first: its first tile in the launch
-    FastDiv by_n;      // tiles_n
-    float* part;       // [splits][m][n]
-    float* bias_part;  // [splits][m], or null
+struct Maps {
+    CUtensorMap a[3], b[3], out[3];
 };
 
 struct Params {
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->free_[i], 1);
+            mbar_init(&bars->free_[i], OP == kDw ? 3 : 1);  // kDw: the products, and warps 2 and 3
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->acc_full[i], 1);
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             x.pr = q >= prm.pr[2].first ? 2 : (q >= prm.pr[1].first ? 1 : 0);
             const Problem& p = prm.pr[x.pr];
             const int i = q - p.first, mt = static_cast<int>(fdiv(p.by_n, static_cast<uint32_t>(i)));
-            x.m0 = mt * kBlockM;
+            x.m0 = mt * 2 * kBlockM;
             x.n0 = (i - mt * p.tiles_n) * prm.bn;
             x.kb0 = x.split * prm.blocks_per_split;
             x.nkb = min(prm.blocks_per_split, kblocks - x.kb0);
@@ -256,6 +260,9 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
         const int w = left < prm.bn ? left : prm.bn;
         return (w + 15) & ~15;
     };
+
+    // kDw: 128-row halves of a tile that hold rows of the result.
+    auto halves_of = [&](const Tile& x) { return prm.pr[x.pr].m - x.m0 > kBlockM ? 2 : 1; };
 
     if (warp == 0) {
         {
@@ -292,9 +299,11 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         tma_load_2d(s, &maps.a[seg], bar, kk, x.m0);
                         for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[seg], bar, x.n0 + 64 * b, kk);
                     } else {
-                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
-                        for (int b = 0; b < 2; ++b) tma_load_2d(s + b * 8192, &maps.a[x.pr], bar, x.m0 + 64 * b, k0);
-                        for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
+                        const int halves = halves_of(x);
+                        mbar_arrive_expect_tx(bar, halves * kABytes + prm.bn * 128);
+                        for (int b = 0; b < 2 * halves; ++b) tma_load_2d(s + b * 8192, &maps.a[x.pr], bar, x.m0 + 64 * b, k0);
+                        for (int b = 0; b < prm.bn / 64; ++b)
+                            tma_load_2d(sb + kABytes + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
                     }
                     __syncwarp();
                     if (++st == stages) {
@@ -310,8 +319,9 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             bool ok = true;
             for (unsigned int t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
                 const Tile x = tile_of(t);
-                const uint32_t acc = tmem + 256 * (n & 1u);
-                if (!mbar_wait_warp(&bars->acc_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8102)) break;
+                const uint32_t buf = OP == kDw ? 0u : n & 1u, turn = OP == kDw ? n : n >> 1;
+                const uint32_t acc = tmem + 256 * buf;
+                if (!mbar_wait_warp(&bars->acc_free[buf], (turn & 1u) ^ 1u, ctl, 0x8102)) break;
                 tc_fence_after();
                 const int width = width_of(x);
                 const uint32_t id = OP == kGate   ? make_idesc_bf16(kBlockM, 2 * prm.bn, false, false)
@@ -320,7 +330,8 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                                                   : make_idesc_bf16(kBlockM, width, false, OP == kDx);
                 const uint32_t id_dh = make_idesc_bf16(kBlockM, 64, false, true);
                 const uint32_t id_ones = make_idesc_bf16(kBlockM, 16, true, false);
-                const bool bias = OP == kDw && x.n0 == 0 && prm.pr[x.pr].bias_part != nullptr;
+                const bool bias = OP == kDw && x.n0 == 0 && prm.pr[x.pr].bias_part != nullptr && !prm.pr[x.pr].turned;
+                const int halves = OP == kDw ? halves_of(x) : 1;
                 for (int i = 0; i < x.nkb; ++i) {
                     if (!(ok = mbar_wait_warp(&bars->full[st], ph, ctl, 0x8103))) break;
                     tc_fence_after();
@@ -332,9 +343,13 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                     for (int k = 0; issue && k < steps; ++k) {
                         const uint32_t more = i > 0 || k > 0;
                         if (OP == kDw) {
-                            const uint64_t da = make_sdesc(s, 8192, 1024, kSw128) + 128 * k;
-                            umma_ss(acc, da, make_sdesc(sb, 8192, 1024, kSw128) + 128 * k, id, more);
-                            if (bias) umma_ss(acc + kColOnes, da, make_sdesc(smem_u32(ones), 16, 1024, kSw128) + 2 * k, id_ones, more);
+                            for (int h = 0; h < halves; ++h) {
+                                const uint64_t da = make_sdesc(s + h * kABytes, 8192, 1024, kSw128) + 128 * k;
+                                umma_ss(acc + 256 * h, da, make_sdesc(sb + kABytes, 8192, 1024, kSw128) + 128 * k, id, more);
+                                if (bias)
+                                    umma_ss(acc + 256 * h + kColOnes, da, make_sdesc(smem_u32(ones), 16, 1024, kSw128) + 2 * k,
+                                            id_ones, more);
+                            }
                         } else {
                             const uint64_t da = make_sdesc(s, 16, 1024, kSw128) + 2 * k;
                             const uint64_t db = OP == kDx ? make_sdesc(sb, 8192, 1024, kSw128) + 128 * k
@@ -352,11 +367,64 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         ph ^= 1u;
                     }
                 }
-                if (ok && elect_one()) umma_commit(&bars->acc_full[n & 1u]);
+                if (ok && elect_one()) umma_commit(&bars->acc_full[buf]);
                 __syncwarp();
             }
             if (elect_one()) umma_commit(&bars->done);  // every product issued here has completed before the columns are freed
             mbar_wait_warp(&bars->done, 0, ctl, 0x81ff);
+        }
+    } else if (OP == kDw && warp < 4) {
+        // dy's columns: a warp adds 32 of a block's 64 tokens in the tiles of the first
+        // rows, an eighth of a box's columns a lane, four tokens at a time
+        uint32_t st = 0, ph = 0;
+        bool ok = true;
+        for (unsigned int t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x) {
+            const Tile x = tile_of(t);
+            const Problem& p = prm.pr[x.pr];
+            const bool adds = p.turned && x.m0 == 0 && p.bias_part;
+            float sum[kDwMaxN / 64][8] = {};
+            for (int i = 0; i < x.nkb; ++i) {
+                if (!(ok = mbar_wait_warp(&bars->full[st], ph, ctl, 0x8105))) break;
+                if (adds) {
+                    const uint8_t* b = smem + st * kStageBytes + 2 * kABytes;
+#pragma unroll
+                    for (int c = 0; c < kDwMaxN / 64; ++c) {
+                        if (c >= prm.bn / 64) break;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const int row = (warp - 2) * 32 + r * 4 + (lane >> 3);
+                            const uint4 v = *reinterpret_cast<const uint4*>(b + c * 8192 + row * 128 + (((lane ^ row) & 7) << 4));
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                sum[c][2 * e] += bf16lo_to_f32(w[e]);
+                                sum[c][2 * e + 1] += bf16hi_to_f32(w[e]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->free_[st]);
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!adds) continue;
+            float* dst = p.bias_part + (static_cast<long long>(x.split) * 2 + warp - 2) * p.n + x.n0;
+#pragma unroll
+            for (int c = 0; c < kDwMaxN / 64; ++c) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum[c][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[c][e], 8);
+                    sum[c][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[c][e], 16);
+                }
+                const int col = c * 64 + lane * 8;  // of the tile
+                if (lane < 8 && col < prm.bn && x.n0 + col < p.n) {
+                    *reinterpret_cast<float4*>(dst + col) = make_float4(sum[c][0], sum[c][1], sum[c][2], sum[c][3]);
+                    *reinterpret_cast<float4*>(dst + col + 4) = make_float4(sum[c][4], sum[c][5], sum[c][6], sum[c][7]);
+                }
+            }
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quad = ew & 3, first = 32 * (ew >> 2);  // its first columns
@@ -397,31 +465,44 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
         };
         for (unsigned int t = blockIdx.x; t < prm.tiles; t += gridDim.x, ++n) {
             const Tile x = tile_of(t);
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[n & 1u], (n >> 1) & 1u, ctl, 0x8104));
+            const uint32_t tbuf = OP == kDw ? 0u : n & 1u, turn = OP == kDw ? n : n >> 1;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[tbuf], turn & 1u, ctl, 0x8104));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t acc = tmem + 256 * (n & 1u) + (static_cast<uint32_t>(quad * 32) << 16);
+            const uint32_t acc = tmem + 256 * tbuf + (static_cast<uint32_t>(quad * 32) << 16);
             const int row0 = x.m0 + quad * 32;
             if (OP == kDw) {
                 const Problem& p = prm.pr[x.pr];
-                const int row = x.m0 + row_in, width = width_of(x);
-                float* dst = p.part + (static_cast<long long>(x.split) * p.m + row) * p.n + x.n0;
-                for (int c = first; c < width; c += kStep) {
-                    uint32_t v[32];
-                    tmem_ld32(acc + c, v);
-                    tmem_wait_ld();
-                    if (row < p.m) {
+                const int width = width_of(x);
+                for (int h = 0; h < halves_of(x); ++h) {
+                    const int row = x.m0 + h * kBlockM + row_in;
+                    float* part = p.part + static_cast<long long>(x.split) * p.m * p.n;
+                    for (int c = first; c < width; c += kStep) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + 256 * h + c, v);
+                        tmem_wait_ld();
+                        const int col = x.n0 + c;
+                        if (row >= p.m) {
+                            // nothing to store
+                        } else if (p.turned) {  // a warp's 32 rows adjoin
+                            float* dst = part + static_cast<long long>(col) * p.m + row;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            if (x.n0 + c + e < p.n)
-                                *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                            for (int e = 0; e < 32; ++e)
+                                if (col + e < p.n) dst[static_cast<long long>(e) * p.m] = __uint_as_float(v[e]);
+                        } else {
+                            float* dst = part + static_cast<long long>(row) * p.n + col;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                if (col + e < p.n)
+                                    *reinterpret_cast<uint4*>(dst + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
                     }
-                }
-                if (first == 0 && x.n0 == 0 && p.bias_part) {
-                    uint32_t v[16];
-                    tmem_ld16(acc + kColOnes, v);
-                    tmem_wait_ld();
-                    if (row < p.m) p.bias_part[static_cast<long long>(x.split) * p.m + row] = __uint_as_float(v[0]);
+                    if (first == 0 && x.n0 == 0 && p.bias_part && !p.turned) {
+                        uint32_t v[16];
+                        tmem_ld16(acc + 256 * h + kColOnes, v);
+                        tmem_wait_ld();
+                        if (row < p.m) p.bias_part[static_cast<long long>(x.split) * p.m + row] = __uint_as_float(v[0]);
+                    }
                 }
             } else {
                 const int left = prm.n - x.n0, width = left < prm.bn ? left : prm.bn;
@@ -473,7 +554,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->acc_free[n & 1u]);
+            if (lane == 0) mbar_arrive(&bars->acc_free[tbuf]);
         }
         bulk_wait_all();
     }
@@ -489,7 +570,7 @@ struct SumParams {
     __nv_bfloat16* out[6];
     long long size[6];
     long long blocks[7];  // first block of each result
-    int splits;
+    int splits[6];
 };
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumParams p) {
     int i = 0;
@@ -497,7 +578,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumPar
     const long long e = ((blockIdx.x - p.blocks[i]) * 256 + threadIdx.x) * 4;
     if (e >= p.size[i]) return;  // sizes are multiples of 8
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.splits; ++k) {
+    for (int k = 0; k < p.splits[i]; ++k) {
         const float4 v = *reinterpret_cast<const float4*>(p.part[i] + k * p.size[i] + e);
         s.x += v.x;
         s.y += v.y;
@@ -525,10 +606,11 @@ inline int tile_width(int n, int most, int step) {
 // Splits of the tokens for the weight gradients: of 1 .. 16 the one with the least
 // work on the busiest SM (waves / splits), more splits costing 1 % each for their
 // partial results; no split shorter than four blocks.
+constexpr int kMaxSplits = 16;
 inline int pick_splits(int tiles, int kblocks, int num_sms) {
     int best = 1;
     double cost = 1e30;
-    for (int s = 1; s <= 16; ++s) {
+    for (int s = 1; s <= kMaxSplits; ++s) {
         const int per = (kblocks + s - 1) / s;
         if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;
         const double waves = static_cast<double>((static_cast<long long>(tiles) * s + num_sms - 1) / num_sms);
@@ -540,7 +622,6 @@ inline int pick_splits(int tiles, int kblocks, int num_sms) {
     }
     return best;
 }
-constexpr int kMaxSplits = 16;
 
 }  // namespace mlp
 
@@ -564,7 +645,7 @@ BwdLayout bwd_layout(const MlpShape& sh) {
         L.part[i] = o;
         o += round256(cf);
         L.bias[i] = o;
-        o += round256(static_cast<size_t>(i == 2 ? sh.channels : sh.hidden) * 4 * mlp::kMaxSplits);
+        o += round256(static_cast<size_t>(i == 2 ? sh.channels : sh.hidden) * 8 * mlp::kMaxSplits);  // two a split at most
     }
     L.total = o;
     return L;
@@ -666,40 +747,39 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     if ((e = launch<kDx>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
     // weights and biases
     prm.k = T;
-    prm.bn = kDwMaxN;
-    const void *as[3] = {dg, du, p.dy}, *bs[3] = {p.x, p.x, h};
+    prm.bn = tile_width(C, kDwMaxN, 64);
+    const void *as[3] = {dg, du, h}, *bs[3] = {p.x, p.x, p.dy};
     void* const outs[6] = {p.dw_gate, p.dw_up, p.dw_down, p.db_gate, p.db_up, p.db_down};
-    int first = 0;
+    const int tiles_n = (C + prm.bn - 1) / prm.bn, tiles = (F + 2 * kBlockM - 1) / (2 * kBlockM) * tiles_n;
     for (int i = 0; i < 3; ++i) {
         Problem& q = prm.pr[i];
-        q.m = i == 2 ? C : F;
-        q.n = i == 2 ? F : C;
-        q.tiles_n = (q.n + prm.bn - 1) / prm.bn;
-        q.tiles = (q.m + kBlockM - 1) / kBlockM * q.tiles_n;
-        q.by_n = make_fastdiv(q.tiles_n);
-        q.first = first;
-        first += q.tiles;
+        q.m = F;
+        q.n = C;
+        q.tiles_n = tiles_n;
+        q.by_n = make_fastdiv(tiles_n);
+        q.first = i * tiles;
+        q.turned = i == 2;
         q.part = reinterpret_cast<float*>(p.ws + L.part[i]);
         q.bias_part = outs[3 + i] ? reinterpret_cast<float*>(p.ws + L.bias[i]) : nullptr;
-        if (encode_matrix(&maps.a[i], as[i], T, q.m, kBlockK, 64, true) ||
-            encode_matrix(&maps.b[i], bs[i], T, q.n, kBlockK, 64, true))
+        if (encode_matrix(&maps.a[i], as[i], T, F, kBlockK, 64, true) || encode_matrix(&maps.b[i], bs[i], T, C, kBlockK, 64, true))
             return cudaErrorInvalidValue;
     }
     const int kblocks = (T + kBlockK - 1) / kBlockK;
-    prm.splits = pick_splits(first, kblocks, num_sms);
+    prm.splits = pick_splits(3 * tiles, kblocks, num_sms);
     prm.blocks_per_split = (kblocks + prm.splits - 1) / prm.splits;
-    prm.tiles = static_cast<unsigned>(first) * prm.splits;
     prm.by_splits = make_fastdiv(prm.splits);
+    prm.tiles = static_cast<unsigned>(3 * tiles) * prm.splits;
     if ((e = launch<kDw>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
     SumParams sum{};
-    sum.splits = prm.splits;
     int count = 0;
     long long blocks = 0;
     for (int i = 0; i < 6; ++i) {
         if (!outs[i]) continue;
-        sum.part[count] = i < 3 ? prm.pr[i].part : prm.pr[i - 3].bias_part;
+        const Problem& q = prm.pr[i % 3];
+        sum.part[count] = i < 3 ? q.part : q.bias_part;
+        sum.splits[count] = i == 5 ? 2 * prm.splits : prm.splits;
         sum.out[count] = static_cast<__nv_bfloat16*>(outs[i]);
-        sum.size[count] = i < 3 ? static_cast<long long>(C) * F : prm.pr[i - 3].m;
+        sum.size[count] = i < 3 ? static_cast<long long>(C) * F : (i == 5 ? C : F);
         sum.blocks[count] = blocks;
         blocks += (sum.size[count] / 4 + 255) / 256;
         ++count;
