@@ -124,3 +124,14 @@ def test_no_tokens():
     g = ops.gated_mlp_bwd(dy.cuda(), **d)
     torch.cuda.synchronize()
     assert y.numel() == 0 and (g.dw_gate == 0).all() and (g.dw_down == 0).all() and (g.db_down == 0).all()
+
+
+def test_long_contractions_over_many_tokens():
+    # tiles of 256 rows in every product that has them, the last rows' half empty
+    t, dy = draw(19001, 264, 1544)
+    d = {k: v.cuda() for k, v in t.items()}
+    y = ops.gated_mlp_fwd(**d)
+    g = ops.gated_mlp_bwd(dy.cuda(), **d)
+    want, bound = mlp.full(**d, act="silu", dy=dy.cuda())
+    cpu = lambda x: {k: v.cpu() for k, v in x.items()}  # noqa: E731
+    compare(dict(y=y, **g._asdict()), cpu(want), cpu(bound))

@@ -1,10 +1,10 @@
 // Gated feed-forward block: y = h W_down^T + b_down, h = act(x W_gate^T + b_gate) o (x W_up^T + b_up),
 // and its backward, as persistent tensor-core kernels over one pipeline.
 //
-// Pipeline (one CTA an SM, 12 warps): warp 0 copies operand blocks of 64
+// Pipeline (one CTA an SM, 12 or 20 warps): warp 0 copies operand blocks of 64
 // contraction channels into a ring with TMA (128-byte swizzle), warp 1 issues
-// tcgen05 products into one of two 256-column TMEM accumulators, warps 4-11 turn
-// the other accumulator into the result.  Operands are taken as they lie in memory:
+// tcgen05 products into one of two 256-column TMEM accumulators, the warps from 4 on
+// turn the other accumulator into the result.  Operands are taken as they lie in memory:
 // contraction-major, or (weights and activations of the gradient products)
 // row-major with the contraction over rows, which the matrix descriptors express.
 // A contraction that does not fill its last block ends at its last 16 channels.
@@ -34,23 +34,23 @@ namespace mlp {
 
 enum : int { kGate, kLinear, kGrad, kDx, kDw };
 // Warps of the epilogue: sixteen where it computes the activation (kGate: four a
-// scheduler hide each other's latencies, 176 -> 110 us at 524288 x 96 x 256), else eight.
+// scheduler hide each other's latencies, 176 -> 130 us at 524288 x 96 x 256), else eight.
 __host__ __device__ constexpr int epi_warps(int op) { return op == kGate ? 16 : 8; }
 __host__ __device__ constexpr int threads_of(int op) { return 128 + 32 * epi_warps(op); }
 constexpr int kBlockK = 64;
 constexpr int kBlockM = 128;
 constexpr int kABytes = kBlockM * kBlockK * 2;
 constexpr int kStages = 4;                        // at most
-constexpr int kDwMaxN = 192;
-// A stage: A, and B of up to 256 rows; kGrad: x, three times 64 weight rows, dy; kDw:
-// twice A's rows and up to 192 columns.
-__host__ __device__ constexpr int stage_bytes(int op) {
-    return op == kGrad ? 2 * kABytes + 3 * 8192 : (op == kDw ? 2 * kABytes + kDwMaxN * 128 : 3 * kABytes);
+constexpr int kTallMaxN = 192;
+// A stage: A, and B of up to 256 rows; kGrad: x, three times 64 weight rows, dy; tall
+// tiles: twice A's rows and up to 192 columns.
+__host__ __device__ constexpr int stage_bytes(int op, bool tall) {
+    return op == kGrad ? 2 * kABytes + 3 * 8192 : (tall ? 2 * kABytes + kTallMaxN * 128 : 3 * kABytes);
 }
-__host__ __device__ constexpr int stages_of(int op) { return op == kGrad || op == kDw ? 3 : kStages; }
+__host__ __device__ constexpr int stages_of(int op, bool tall) { return op == kGrad || tall ? 3 : kStages; }
 constexpr int kStoreBytes = 32 * 64;              // a warp's 32 rows x 32 bf16 columns
 constexpr int kRingBytes = 12 * kABytes;
-constexpr int kOnesOff = stages_of(kDw) * stage_bytes(kDw);  // kDw: 16 rows x 64 of 1.0 behind its ring
+constexpr int kOnesOff = stages_of(kDw, true) * stage_bytes(kDw, true);  // kDw: 16 rows x 64 of 1.0 behind its ring
 constexpr int kOnesBytes = 2048;
 constexpr int kStoreOff = kRingBytes;
 constexpr int kBarOff = kStoreOff + 16 * kStoreBytes;
@@ -62,10 +62,11 @@ struct Bars {
     int abort_flag;
 };
 constexpr int kSmemBytes = kBarOff + 256 + 1024;
-static_assert(stages_of(kGate) * stage_bytes(kGate) <= kRingBytes && stages_of(kGrad) * stage_bytes(kGrad) <= kRingBytes &&
+static_assert(stages_of(kGate, false) * stage_bytes(kGate, false) <= kRingBytes &&
+                  stages_of(kGrad, false) * stage_bytes(kGrad, false) <= kRingBytes &&
                   kOnesOff + kOnesBytes <= kRingBytes,
               "the ring overflows its place");
-static_assert(stage_bytes(kGrad) % 1024 == 0 && stage_bytes(kDw) % 1024 == 0 && kOnesOff % 1024 == 0, "tile alignment");
+static_assert(stage_bytes(kGrad, false) % 1024 == 0 && stage_bytes(kDw, true) % 1024 == 0 && kOnesOff % 1024 == 0, "tile alignment");
 static_assert(sizeof(Bars) <= 256, "barrier block overflows its slot");
 static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may have");
 
@@ -190,10 +191,12 @@ struct Cols {
     }
 };
 
-template <int OP>
+// kTall: tiles of 256 rows, both accumulators to one (kDw, and kLinear and kDx over long
+// contractions).
+template <int OP, bool kTall>
 __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
     constexpr int kEpiWarps = epi_warps(OP), kThreads = threads_of(OP);
-    constexpr int stages = stages_of(OP), kStageBytes = stage_bytes(OP);
+    constexpr int stages = stages_of(OP, kTall), kStageBytes = stage_bytes(OP, kTall), kTileM = kTall ? 2 * kBlockM : kBlockM;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem(smem_raw);
     Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
@@ -242,13 +245,13 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             x.pr = q >= prm.pr[2].first ? 2 : (q >= prm.pr[1].first ? 1 : 0);
             const Problem& p = prm.pr[x.pr];
             const int i = q - p.first, mt = static_cast<int>(fdiv(p.by_n, static_cast<uint32_t>(i)));
-            x.m0 = mt * 2 * kBlockM;
+            x.m0 = mt * kTileM;
             x.n0 = (i - mt * p.tiles_n) * prm.bn;
             x.kb0 = x.split * prm.blocks_per_split;
             x.nkb = min(prm.blocks_per_split, kblocks - x.kb0);
         } else {
             const int mt = static_cast<int>(fdiv(prm.by_n, t));
-            x.m0 = mt * kBlockM;
+            x.m0 = mt * kTileM;
             x.n0 = (static_cast<int>(t) - mt * prm.tiles_n) * prm.bn;
         }
         return x;
@@ -261,8 +264,10 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
         return (w + 15) & ~15;
     };
 
-    // kDw: 128-row halves of a tile that hold rows of the result.
-    auto halves_of = [&](const Tile& x) { return prm.pr[x.pr].m - x.m0 > kBlockM ? 2 : 1; };
+    // 128-row halves of a tile that hold rows of the result.
+    auto halves_of = [&](const Tile& x) {
+        return kTall && (OP == kDw ? prm.pr[x.pr].m : prm.m) - x.m0 > kBlockM ? 2 : 1;
+    };
 
     if (warp == 0) {
         {
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                 for (int i = 0; i < x.nkb; ++i) {
                     if (!(ok = mbar_wait_warp(&bars->free_[st], ph ^ 1u, ctl, 0x8101))) break;
                     uint64_t* bar = &bars->full[st];
-                    const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
+                    const uint32_t s = sbase + st * kStageBytes, sb = s + (kTall ? 2 : 1) * kABytes;
                     const int k0 = (x.kb0 + i) * kBlockK;
                     if (!elect_one()) {
                         // the elected lane copies
@@ -283,8 +288,9 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
                         tma_load_2d(sb + prm.bn * 128, &maps.b[1], bar, k0, x.n0);
                     } else if (OP == kLinear) {
-                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
-                        tma_load_2d(s, &maps.a[0], bar, k0, x.m0);
+                        const int halves = halves_of(x);
+                        mbar_arrive_expect_tx(bar, halves * kABytes + prm.bn * 128);
+                        for (int h = 0; h < halves; ++h) tma_load_2d(s + h * kABytes, &maps.a[0], bar, k0, x.m0 + h * kBlockM);
                         tma_load_2d(sb, &maps.b[0], bar, k0, x.n0);
                     } else if (OP == kGrad) {
                         mbar_arrive_expect_tx(bar, 2 * kABytes + 3 * 64 * 128);
@@ -295,15 +301,16 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         tma_load_2d(s + kABytes + 3 * 8192, &maps.a[1], bar, k0, x.m0);
                     } else if (OP == kDx) {
                         const int seg = i >= kblocks ? 1 : 0, kk = k0 - seg * kblocks * kBlockK;
-                        mbar_arrive_expect_tx(bar, kABytes + prm.bn * 128);
-                        tma_load_2d(s, &maps.a[seg], bar, kk, x.m0);
+                        const int halves = halves_of(x);
+                        mbar_arrive_expect_tx(bar, halves * kABytes + prm.bn * 128);
+                        for (int h = 0; h < halves; ++h) tma_load_2d(s + h * kABytes, &maps.a[seg], bar, kk, x.m0 + h * kBlockM);
                         for (int b = 0; b < prm.bn / 64; ++b) tma_load_2d(sb + b * 8192, &maps.b[seg], bar, x.n0 + 64 * b, kk);
                     } else {
                         const int halves = halves_of(x);
                         mbar_arrive_expect_tx(bar, halves * kABytes + prm.bn * 128);
                         for (int b = 0; b < 2 * halves; ++b) tma_load_2d(s + b * 8192, &maps.a[x.pr], bar, x.m0 + 64 * b, k0);
                         for (int b = 0; b < prm.bn / 64; ++b)
-                            tma_load_2d(sb + kABytes + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
+                            tma_load_2d(sb + b * 8192, &maps.b[x.pr], bar, x.n0 + 64 * b, k0);
                     }
                     __syncwarp();
                     if (++st == stages) {
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             bool ok = true;
             for (unsigned int t = blockIdx.x; t < prm.tiles && ok; t += gridDim.x, ++n) {
                 const Tile x = tile_of(t);
-                const uint32_t buf = OP == kDw ? 0u : n & 1u, turn = OP == kDw ? n : n >> 1;
+                const uint32_t buf = kTall ? 0u : n & 1u, turn = kTall ? n : n >> 1;
                 const uint32_t acc = tmem + 256 * buf;
                 if (!mbar_wait_warp(&bars->acc_free[buf], (turn & 1u) ^ 1u, ctl, 0x8102)) break;
                 tc_fence_after();
@@ -331,11 +338,11 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                 const uint32_t id_dh = make_idesc_bf16(kBlockM, 64, false, true);
                 const uint32_t id_ones = make_idesc_bf16(kBlockM, 16, true, false);
                 const bool bias = OP == kDw && x.n0 == 0 && prm.pr[x.pr].bias_part != nullptr && !prm.pr[x.pr].turned;
-                const int halves = OP == kDw ? halves_of(x) : 1;
+                const int halves = halves_of(x);
                 for (int i = 0; i < x.nkb; ++i) {
                     if (!(ok = mbar_wait_warp(&bars->full[st], ph, ctl, 0x8103))) break;
                     tc_fence_after();
-                    const uint32_t s = sbase + st * kStageBytes, sb = s + kABytes;
+                    const uint32_t s = sbase + st * kStageBytes, sb = s + (kTall ? 2 : 1) * kABytes;
                     const int kb = OP == kDx && i >= kblocks ? i - kblocks : x.kb0 + i;
                     const int left = prm.k - kb * kBlockK;
                     const int steps = left >= kBlockK ? kBlockK / 16 : (left + 15) / 16;
@@ -345,16 +352,16 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                         if (OP == kDw) {
                             for (int h = 0; h < halves; ++h) {
                                 const uint64_t da = make_sdesc(s + h * kABytes, 8192, 1024, kSw128) + 128 * k;
-                                umma_ss(acc + 256 * h, da, make_sdesc(sb + kABytes, 8192, 1024, kSw128) + 128 * k, id, more);
+                                umma_ss(acc + 256 * h, da, make_sdesc(sb, 8192, 1024, kSw128) + 128 * k, id, more);
                                 if (bias)
                                     umma_ss(acc + 256 * h + kColOnes, da, make_sdesc(smem_u32(ones), 16, 1024, kSw128) + 2 * k,
                                             id_ones, more);
                             }
                         } else {
-                            const uint64_t da = make_sdesc(s, 16, 1024, kSw128) + 2 * k;
                             const uint64_t db = OP == kDx ? make_sdesc(sb, 8192, 1024, kSw128) + 128 * k
                                                           : make_sdesc(sb, 16, 1024, kSw128) + 2 * k;
-                            umma_ss(acc, da, db, id, more);
+                            for (int h = 0; h < halves; ++h)
+                                umma_ss(acc + 256 * h, make_sdesc(s + h * kABytes, 16, 1024, kSw128) + 2 * k, db, id, more);
                             if (OP == kGrad)
                                 umma_ss(acc + 128, make_sdesc(s + kABytes + 3 * 8192, 16, 1024, kSw128) + 2 * k,
                                         make_sdesc(sb + 2 * 64 * 128, 8192, 1024, kSw128) + 128 * k, id_dh, more);
@@ -382,13 +389,13 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             const Tile x = tile_of(t);
             const Problem& p = prm.pr[x.pr];
             const bool adds = p.turned && x.m0 == 0 && p.bias_part;
-            float sum[kDwMaxN / 64][8] = {};
+            float sum[kTallMaxN / 64][8] = {};
             for (int i = 0; i < x.nkb; ++i) {
                 if (!(ok = mbar_wait_warp(&bars->full[st], ph, ctl, 0x8105))) break;
                 if (adds) {
                     const uint8_t* b = smem + st * kStageBytes + 2 * kABytes;
 #pragma unroll
-                    for (int c = 0; c < kDwMaxN / 64; ++c) {
+                    for (int c = 0; c < kTallMaxN / 64; ++c) {
                         if (c >= prm.bn / 64) break;
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
             if (!adds) continue;
             float* dst = p.bias_part + (static_cast<long long>(x.split) * 2 + warp - 2) * p.n + x.n0;
 #pragma unroll
-            for (int c = 0; c < kDwMaxN / 64; ++c) {
+            for (int c = 0; c < kTallMaxN / 64; ++c) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     sum[c][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[c][e], 8);
@@ -465,12 +472,11 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
         };
         for (unsigned int t = blockIdx.x; t < prm.tiles; t += gridDim.x, ++n) {
             const Tile x = tile_of(t);
-            const uint32_t tbuf = OP == kDw ? 0u : n & 1u, turn = OP == kDw ? n : n >> 1;
+            const uint32_t tbuf = kTall ? 0u : n & 1u, turn = kTall ? n : n >> 1;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[tbuf], turn & 1u, ctl, 0x8104));
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + 256 * tbuf + (static_cast<uint32_t>(quad * 32) << 16);
-            const int row0 = x.m0 + quad * 32;
             if (OP == kDw) {
                 const Problem& p = prm.pr[x.pr];
                 const int width = width_of(x);
@@ -506,10 +512,12 @@ __global__ void __launch_bounds__(threads_of(OP), 1) mlp_kernel(const __grid_con
                 }
             } else {
                 const int left = prm.n - x.n0, width = left < prm.bn ? left : prm.bn;
-                for (int c = first; c < width; c += kStep) {
-                    const int col = x.n0 + c;
+                // kTall: the halves' columns one after the other
+                for (int i = first, all = halves_of(x) * ((width + 31) & ~31); i < all; i += kStep) {
+                    const int h = kTall && i >= ((width + 31) & ~31) ? 1 : 0, c = i - h * ((width + 31) & ~31);
+                    const int col = x.n0 + c, row0 = x.m0 + h * kBlockM + quad * 32;
                     Cols ca, cu, cd;
-                    ca.load(acc + c);
+                    ca.load(acc + 256 * h + c);
                     if (OP == kGate || OP == kGrad) cu.load(acc + prm.bn + c);
                     if (OP == kGrad) cd.load(acc + 128 + c);
                     const float b0 = OP == kDx ? 0.f : bias_at(prm.bias0, col + lane, prm.n);
@@ -588,12 +596,12 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumPar
     *reinterpret_cast<uint2*>(p.out[i] + e) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
-template <int OP>
+template <int OP, bool kTall = OP == kDw>
 cudaError_t launch(const Maps& maps, const Params& prm, int num_sms, cudaStream_t stream) {
     static SmemOptIn optin;
-    if (cudaError_t e = optin.ensure(reinterpret_cast<const void*>(mlp_kernel<OP>), kSmemBytes)) return e;
+    if (cudaError_t e = optin.ensure(reinterpret_cast<const void*>(mlp_kernel<OP, kTall>), kSmemBytes)) return e;
     const unsigned int grid = prm.tiles < static_cast<unsigned>(num_sms) ? prm.tiles : num_sms;
-    mlp_kernel<OP><<<grid, threads_of(OP), kSmemBytes, stream>>>(maps, prm);
+    mlp_kernel<OP, kTall><<<grid, threads_of(OP), kSmemBytes, stream>>>(maps, prm);
     return cudaGetLastError();
 }
 
@@ -601,6 +609,26 @@ cudaError_t launch(const Maps& maps, const Params& prm, int num_sms, cudaStream_
 inline int tile_width(int n, int most, int step) {
     const int tiles = (n + most - 1) / most;
     return ((n + tiles - 1) / tiles + step - 1) / step * step;
+}
+
+// Tiles of a kLinear or kDx launch whose m, n, k and segments are set.  Tall ones read
+// less into shared memory but leave their epilogue uncovered, so they are for long
+// contractions (dx at 32768 x 384 x 1024, 32 blocks: 56 -> 48 us; at 131072 x 192 x 512,
+// 16 blocks: 61 -> 63 us), and for enough rows to give every SM a tile.
+inline bool take_tall(Params* p, int step, int num_sms) {
+    const long long blocks = static_cast<long long>((p->k + kBlockK - 1) / kBlockK) * (p->segments ? p->segments : 1);
+    p->bn = tile_width(p->n, kTallMaxN, step);
+    p->tiles_n = (p->n + p->bn - 1) / p->bn;
+    long long rows = (static_cast<long long>(p->m) + 2 * kBlockM - 1) / (2 * kBlockM);
+    const bool tall = blocks >= 24 && rows * p->tiles_n >= num_sms;
+    if (!tall) {
+        p->bn = tile_width(p->n, 256, step);
+        p->tiles_n = (p->n + p->bn - 1) / p->bn;
+        rows = (static_cast<long long>(p->m) + kBlockM - 1) / kBlockM;
+    }
+    p->tiles = static_cast<unsigned>(rows * p->tiles_n);
+    p->by_n = make_fastdiv(p->tiles_n);
+    return tall;
 }
 
 // Splits of the tokens for the weight gradients: of 1 .. 16 the one with the least
@@ -686,16 +714,13 @@ cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     if (e != cudaSuccess) return e;
     prm.n = C;
     prm.k = F;
-    prm.bn = tile_width(C, 256, 32);
-    prm.tiles_n = (C + prm.bn - 1) / prm.bn;
-    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
-    prm.by_n = make_fastdiv(prm.tiles_n);
+    const bool tall = take_tall(&prm, 32, num_sms);
     prm.bias0 = static_cast<const __nv_bfloat16*>(p.b_down);
     if (encode_matrix(&maps.a[0], p.ws, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.b[0], p.w_down, C, F, prm.bn, kBlockK, true) ||
         encode_matrix(&maps.out[0], p.y, T, C, 32, 32, false))
         return cudaErrorInvalidValue;
-    return launch<kLinear>(maps, prm, num_sms, stream);
+    return tall ? launch<kLinear, true>(maps, prm, num_sms, stream) : launch<kLinear>(maps, prm, num_sms, stream);
 }
 
 cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
@@ -734,20 +759,18 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     prm.n = C;
     prm.k = F;
     prm.segments = 2;
-    prm.bn = tile_width(C, 256, 64);
-    prm.tiles_n = (C + prm.bn - 1) / prm.bn;
-    prm.tiles = static_cast<unsigned>(rows_m) * prm.tiles_n;
-    prm.by_n = make_fastdiv(prm.tiles_n);
+    const bool tall = take_tall(&prm, 64, num_sms);
     if (encode_matrix(&maps.a[0], dg, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.a[1], du, T, F, kBlockM, kBlockK, true) ||
         encode_matrix(&maps.b[0], p.w_gate, F, C, kBlockK, 64, true) ||
         encode_matrix(&maps.b[1], p.w_up, F, C, kBlockK, 64, true) ||
         encode_matrix(&maps.out[0], p.dx, T, C, 32, 32, false))
         return cudaErrorInvalidValue;
-    if ((e = launch<kDx>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
+    e = tall ? launch<kDx, true>(maps, prm, num_sms, stream) : launch<kDx>(maps, prm, num_sms, stream);
+    if (e != cudaSuccess) return e;
     // weights and biases
     prm.k = T;
-    prm.bn = tile_width(C, kDwMaxN, 64);
+    prm.bn = tile_width(C, kTallMaxN, 64);
     const void *as[3] = {dg, du, h}, *bs[3] = {p.x, p.x, p.dy};
     void* const outs[6] = {p.dw_gate, p.dw_up, p.dw_down, p.db_gate, p.db_up, p.db_down};
     const int tiles_n = (C + prm.bn - 1) / prm.bn, tiles = (F + 2 * kBlockM - 1) / (2 * kBlockM) * tiles_n;
