@@ -82,11 +82,7 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
                                             volatile int* abort_flag, uint64_t limit_ns, unsigned int where) {
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        // the clock and the flag only every few tries: a waiting warp's polls take issue
-        // slots from the working ones
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > limit_ns) {
             atomicCAS(status, 0u, (kErrTimeout << 24) | (where & 0xFFFFFFu));
