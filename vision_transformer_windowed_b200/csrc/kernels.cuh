@@ -196,6 +196,10 @@ struct MlpPtrs {
 };
 size_t mlp_fwd_workspace_bytes(const MlpShape& sh);
 size_t mlp_bwd_workspace_bytes(const MlpShape& sh);
+// Where all weights fit into shared memory the forward is one kernel, without workspace.
+bool mlp_fits(const MlpShape& sh);
+cudaError_t launch_mlp_small_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
+                                 int num_sms, cudaStream_t stream);
 cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
                            int num_sms, cudaStream_t stream);
 cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,

@@ -24,9 +24,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "kernels.cuh"
-#include "ptx.cuh"
-#include "rows.cuh"
+#include "mlp.cuh"
 
 namespace fswin {
 
@@ -97,78 +95,8 @@ struct Params {
     unsigned long long limit_ns;
 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ unsigned long long pair_of(float x) { return pair(x, x); }
-
-// act(g) and, for the gradient, act'(g) of two values.
-// silu: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).
-// gelu: g Phi(g), Phi(g) + g phi(g), Phi from the error function's approximation 7.1.28
-// of M. Abramowitz and I. A. Stegun, "Handbook of Mathematical Functions",
-//   erf(z) = 1 - (1 + a1 z + ... + a6 z^6)^-16, z >= 0 (absolute error 3e-7, far below
-// the result's bf16 step): one reciprocal and no exponential; large z overflow to a
-// reciprocal of zero, the limit.
-// Four pairs at a time, step by step beside each other: one pair's steps depend on each
-// other.
-template <bool kSlope>
-__device__ __forceinline__ void activate(const unsigned long long* g, int act, unsigned long long (&a)[4],
-                                         unsigned long long (&slope)[4]) {
-#define EACH _Pragma("unroll") for (int i = 0; i < 4; ++i)
-    float x[4], y[4];
-    if (act == 0) {
-        EACH unpair(mul_pair(g[i], pair_of(-1.4426950408889634f)), x[i], y[i]);
-        EACH unpair(add_pair(pair(ex2_approx(x[i]), ex2_approx(y[i])), pair_of(1.f)), x[i], y[i]);
-        unsigned long long s[4];
-        EACH s[i] = pair(rcp_approx(x[i]), rcp_approx(y[i]));
-        EACH a[i] = mul_pair(g[i], s[i]);
-        if (kSlope) EACH slope[i] = fma_pair(a[i], fma_pair(s[i], pair_of(-1.f), pair_of(1.f)), s[i]);
-        return;
-    }
-    unsigned long long z[4], p[4];
-    EACH z[i] = mul_pair(g[i] & 0x7FFFFFFF7FFFFFFFull, pair_of(0.70710678118654752f));
-    EACH p[i] = fma_pair(z[i], pair_of(0.0000430638f), pair_of(0.0002765672f));
-    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0001520143f));
-    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0092705272f));
-    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0422820123f));
-    EACH p[i] = fma_pair(p[i], z[i], pair_of(0.0705230784f));
-    EACH p[i] = fma_pair(p[i], z[i], pair_of(1.f));
-    EACH p[i] = mul_pair(p[i], p[i]);
-    EACH p[i] = mul_pair(p[i], p[i]);
-    EACH p[i] = mul_pair(p[i], p[i]);
-    EACH p[i] = mul_pair(p[i], p[i]);
-    EACH unpair(p[i], x[i], y[i]);
-    EACH p[i] = fma_pair(pair(rcp_approx(x[i]), rcp_approx(y[i])), pair_of(-0.5f), pair_of(0.5f));  // >= 0
-    EACH p[i] = add_pair(p[i] | (g[i] & 0x8000000080000000ull), pair_of(0.5f));                     // Phi(g)
-    EACH a[i] = mul_pair(g[i], p[i]);
-    if (kSlope) {
-        EACH unpair(mul_pair(mul_pair(g[i], g[i]), pair_of(-0.72134752044448170f)), x[i], y[i]);
-        EACH slope[i] = fma_pair(mul_pair(g[i], pair_of(0.39894228040143268f)), pair(ex2_approx(x[i]), ex2_approx(y[i])), p[i]);
-    }
-#undef EACH
-}
-
 // Adds 32 bias columns, one a lane, to every lane's row of 32: through the warp's
 // shared memory, from which each lane reads them all.
-__device__ __forceinline__ float bias_at(const __nv_bfloat16* bias, int c, int n) {
-    return bias && c < n ? __bfloat162float(bias[c]) : 0.f;
-}
 __device__ __forceinline__ void add_bias(unsigned long long (&x)[16], float* place, float mine, int lane) {
     __syncwarp();
     place[lane] = mine;
@@ -682,12 +610,13 @@ BwdLayout bwd_layout(const MlpShape& sh) {
 }  // namespace
 
 size_t mlp_fwd_workspace_bytes(const MlpShape& sh) {
-    return round256(static_cast<size_t>(sh.tokens) * sh.hidden * 2);
+    return mlp_fits(sh) ? 256 : round256(static_cast<size_t>(sh.tokens) * sh.hidden * 2);
 }
 size_t mlp_bwd_workspace_bytes(const MlpShape& sh) { return bwd_layout(sh).total; }
 
 cudaError_t launch_mlp_fwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* status, unsigned long long limit_ns,
                            int num_sms, cudaStream_t stream) {
+    if (mlp_fits(sh)) return launch_mlp_small_fwd(sh, p, status, limit_ns, num_sms, stream);
     using namespace mlp;
     const int T = static_cast<int>(sh.tokens), C = sh.channels, F = sh.hidden;
     const int rows_m = (T + kBlockM - 1) / kBlockM;
