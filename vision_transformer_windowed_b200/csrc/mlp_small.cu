@@ -4,12 +4,14 @@
 //
 // One persistent CTA an SM, 24 warps.  Warp 0 copies the weights once and then x, 128
 // tokens a tile, two tiles ahead.  Warp 1 issues the products, 64 hidden channels (a
-// chunk) at a time: g and u of chunk i + 1 in one product of 128 columns, then y += h Wd^T
+// chunk) at a time: g and u of chunk i + 2 in one product of 128 columns, then y += h Wd^T
 // of chunk i with h taken from tensor memory.  Warps 4-19 compute h, eight warps the even
 // chunks and eight the odd ones; it replaces their u columns as bf16.  Warps 20-23 store
-// y.  Tensor memory: two chunks of g and u (128 columns each), two tiles of y.
+// y.  Tensor memory: three chunks of g and u (128 columns each), so that a group of warps
+// finds its next chunk ready (two chunks and two tiles of y: 129 us in place of 118), and
+// one tile of y, or two of up to 64 channels.
 //
-// The activation's arithmetic bounds it: 524288 x 96 x 256 with gelu take 129 us, where
+// The activation's arithmetic bounds it: 524288 x 96 x 256 with gelu take 118 us, where
 // the two products apart take 187 (h alone is 268 MB, written and read).
 #include "mlp.cuh"
 
@@ -28,10 +30,12 @@ constexpr int kWorkers = 16, kStorers = 4;  // warps
 constexpr int kThreads = 128 + 32 * (kWorkers + kStorers);
 constexpr int kStoreBytes = 32 * 64;        // a warp's 32 rows x 32 bf16 columns
 constexpr int kMaxSmem = 232448;
-constexpr uint32_t kColY = 256;             // y's accumulators, behind the chunks'
+constexpr uint32_t kBufs = 3;               // chunks of g and u in tensor memory
+constexpr uint32_t kColY = 128 * kBufs;     // y's accumulators, behind theirs
 
 struct Bars {
-    uint64_t weights, x_full[2], x_free[2], gu_full[2], h_ready[2], y_full[2], y_free[2], done;
+    // gu_full: one for each buffer and group of warps, which so waits for every phase of its own
+    uint64_t weights, x_full[2], x_free[2], gu_full[2 * kBufs], h_ready[kBufs], y_full[2], y_free[2], done;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -51,6 +55,13 @@ struct Params {
     unsigned long long limit_ns;
 };
 
+// Waits for this warp's loads from tensor memory; the values are not used before it.
+__device__ __forceinline__ void settle(uint32_t (&a)[16], uint32_t (&b)[16]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));
+}
+
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params prm) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem(smem_raw);
@@ -63,11 +74,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->x_full[i], 1);
             mbar_init(&bars->x_free[i], 1);
-            mbar_init(&bars->gu_full[i], 1);
-            mbar_init(&bars->h_ready[i], kWorkers / 2);
             mbar_init(&bars->y_full[i], 1);
             mbar_init(&bars->y_free[i], kStorers);
         }
+        for (uint32_t i = 0; i < 2 * kBufs; ++i) mbar_init(&bars->gu_full[i], 1);
+        for (uint32_t i = 0; i < kBufs; ++i) mbar_init(&bars->h_ready[i], kWorkers / 2);
         mbar_init(&bars->done, 1);
         bars->abort_flag = 0;
         fence_mbar_init();
@@ -90,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
     const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
     const unsigned int count = (prm.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;  // tiles of this CTA
     const int chunks = prm.chunks, blocks = prm.blocks;
+    const unsigned int all = count * chunks;  // chunks of this CTA
+    const uint32_t y_bufs = prm.n_y <= 64 ? 2u : 1u;
 
     if (warp == 0) {
         const uint32_t down_bytes = prm.n_y * kChunk * 2;
@@ -120,63 +133,89 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         const uint32_t id_gu = make_idesc_bf16(kTileM, 2 * kChunk, false, false);
         const uint32_t id_y = make_idesc_bf16(kTileM, prm.n_y, false, false);
         const int steps = (prm.C + 15) / 16;
-        // g and u of chunk c of tile n, the CTA's chunk number i
-        auto issue_gu = [&](unsigned int n, int c, unsigned int i) {
-            const uint32_t s = n & 1u;
-            if (c == 0 && !mbar_wait_warp(&bars->x_full[s], (n >> 1) & 1u, ctl, 0x8202)) return false;
+        // g and u of the next chunk, into its buffer
+        struct {
+            unsigned int n, i;
+            int c;
+            uint32_t buf, bar;
+        } next{0, 0, 0, 0, 0};
+        auto issue_gu = [&]() {
+            const uint32_t s = next.n & 1u;
+            if (next.c == 0 && !mbar_wait_warp(&bars->x_full[s], (next.n >> 1) & 1u, ctl, 0x8202)) return false;
             tc_fence_after();
+            const bool last = next.c == chunks - 1;
             if (elect_one()) {
-                const uint32_t x = sbase + prm.off_x + s * blocks * kTileBytes, w = sbase + c * blocks * kTileBytes;
+                const uint32_t x = sbase + prm.off_x + s * blocks * kTileBytes, w = sbase + next.c * blocks * kTileBytes;
                 for (int k = 0; k < steps; ++k) {
                     const uint32_t at = (k >> 1) * kTileBytes;
-                    umma_ss(tmem + 128 * (i & 1u), make_sdesc(x + at, 16, 512, kSw64) + 2 * (k & 1),
+                    umma_ss(tmem + 128 * next.buf, make_sdesc(x + at, 16, 512, kSw64) + 2 * (k & 1),
                             make_sdesc(w + at, 16, 512, kSw64) + 2 * (k & 1), id_gu, k > 0);
                 }
-                umma_commit(&bars->gu_full[i & 1u]);
-                if (c == chunks - 1) umma_commit(&bars->x_free[s]);
+                umma_commit(&bars->gu_full[next.bar]);
+                if (last) umma_commit(&bars->x_free[s]);
             }
             __syncwarp();
+            next.n += last ? 1u : 0u;
+            next.c = last ? 0 : next.c + 1;
+            next.buf = next.buf == kBufs - 1 ? 0 : next.buf + 1;
+            next.bar = next.bar == 2 * kBufs - 1 ? 0 : next.bar + 1;
+            ++next.i;
             return true;
         };
-        bool ok = mbar_wait_warp(&bars->weights, 0, ctl, 0x8203) && issue_gu(0, 0, 0);
-        unsigned int i = 0;
+        bool ok = mbar_wait_warp(&bars->weights, 0, ctl, 0x8203);
+        for (uint32_t i = 0; i + 1 < kBufs && next.i < all && ok; ++i) ok = issue_gu();
+        uint32_t buf = 0, turn = 0, yb = 0, yturn = 0;
         for (unsigned int n = 0; n < count && ok; ++n) {
-            const uint32_t y = tmem + kColY + 128 * (n & 1u);
-            for (int c = 0; c < chunks; ++c, ++i) {
-                // the next chunk's buffer: its h has gone into a product already issued
-                const bool last = c == chunks - 1;
-                if (!(last && n + 1 == count) && !(ok = issue_gu(last ? n + 1 : n, last ? 0 : c + 1, i + 1))) break;
-                if (c == 0 && !(ok = mbar_wait_warp(&bars->y_free[n & 1u], ((n >> 1) & 1u) ^ 1u, ctl, 0x8204))) break;
-                if (!(ok = mbar_wait_warp(&bars->h_ready[i & 1u], (i >> 1) & 1u, ctl, 0x8205))) break;
+            const uint32_t y = tmem + kColY + 64 * yb;
+            for (int c = 0; c < chunks; ++c) {
+                // into the buffer whose h has gone into a product already issued
+                if (next.i < all && !(ok = issue_gu())) break;
+                if (c == 0 && !(ok = mbar_wait_warp(&bars->y_free[yb], (yturn & 1u) ^ 1u, ctl, 0x8204))) break;
+                if (!(ok = mbar_wait_warp(&bars->h_ready[buf], turn & 1u, ctl, 0x8205))) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t h = tmem + 128 * (i & 1u) + kChunk;
+                    const uint32_t h = tmem + 128 * buf + kChunk;
                     const uint64_t w = make_sdesc(sbase + prm.off_down + c * prm.n_y * kChunk * 2, 16, 1024, kSw128);
                     const int left = (prm.F - c * kChunk + 15) / 16;
                     for (int k = 0; k < (left < 4 ? left : 4); ++k)
                         umma_ts(y, h + 32 * (k >> 1) + 8 * (k & 1), w + 2 * k, id_y, c > 0 || k > 0);
-                    if (last) umma_commit(&bars->y_full[n & 1u]);
+                    if (c == chunks - 1) umma_commit(&bars->y_full[yb]);
                 }
                 __syncwarp();
+                if (++buf == kBufs) {
+                    buf = 0;
+                    ++turn;
+                }
+            }
+            if (++yb == y_bufs) {
+                yb = 0;
+                ++yturn;
             }
         }
         if (elect_one()) umma_commit(&bars->done);  // every product issued here has completed before the columns are freed
         mbar_wait_warp(&bars->done, 0, ctl, 0x82ff);
     } else if (warp >= 4 && warp < 4 + kWorkers) {
         const int ew = warp - 4, group = ew >> 3, half = (ew >> 2) & 1;
-        const uint32_t base = tmem + 128 * group + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * half;
-        const unsigned int all = count * chunks;
+        const uint32_t own = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * half;
         int c = group % chunks;
+        uint32_t buf = group, bar = group, turn = 0;
         for (unsigned int i = group; i < all; i += 2, c = (c + 2) % chunks) {
-            if (!mbar_wait_warp(&bars->gu_full[group], (i >> 1) & 1u, ctl, 0x8206)) break;
+            if (!mbar_wait_warp(&bars->gu_full[bar], turn & 1u, ctl, 0x8206)) break;
+            const uint32_t base = own + 128 * buf;
             tc_fence_after();
             const float* b = bias + c * 2 * kChunk + 32 * half;
+            // 16 channels at a time; the second sixteen's g arrives while the first are computed
+            uint32_t gv[2][16], uv[16];
+            tmem_ld16(base, gv[0]);
+            tmem_ld16(base + kChunk, uv);
+            settle(gv[0], uv);
+            tmem_ld16(base + 16, gv[1]);
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                uint32_t gv[16], uv[16];
-                tmem_ld16(base + 16 * sub, gv);
-                tmem_ld16(base + kChunk + 16 * sub, uv);
-                tmem_wait_ld();
+                if (sub == 1) {
+                    tmem_ld16(base + kChunk + 16, uv);
+                    settle(gv[1], uv);
+                }
                 uint32_t out[8];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {  // eight channels
@@ -184,19 +223,19 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float4 v = *reinterpret_cast<const float4*>(b + 16 * sub + 8 * q + 4 * e);
-                        g[2 * e] = add_pair(pair(gv[8 * q + 4 * e], gv[8 * q + 4 * e + 1]), pair(v.x, v.y));
-                        g[2 * e + 1] = add_pair(pair(gv[8 * q + 4 * e + 2], gv[8 * q + 4 * e + 3]), pair(v.z, v.w));
+                        const uint32_t* t = gv[sub] + 8 * q + 4 * e;
+                        g[2 * e] = add_pair(pair(t[0], t[1]), pair(v.x, v.y));
+                        g[2 * e + 1] = add_pair(pair(t[2], t[3]), pair(v.z, v.w));
                     }
                     activate<false>(g, prm.act, f, s);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float4 v = *reinterpret_cast<const float4*>(b + kChunk + 16 * sub + 8 * q + 4 * e);
-                        const unsigned long long u0 = add_pair(pair(uv[8 * q + 4 * e], uv[8 * q + 4 * e + 1]), pair(v.x, v.y));
-                        const unsigned long long u1 = add_pair(pair(uv[8 * q + 4 * e + 2], uv[8 * q + 4 * e + 3]), pair(v.z, v.w));
+                        const uint32_t* t = uv + 8 * q + 4 * e;
                         float lo, hi;
-                        unpair(mul_pair(f[2 * e], u0), lo, hi);
+                        unpair(mul_pair(f[2 * e], add_pair(pair(t[0], t[1]), pair(v.x, v.y))), lo, hi);
                         out[4 * q + 2 * e] = pack_bf16x2(lo, hi);
-                        unpair(mul_pair(f[2 * e + 1], u1), lo, hi);
+                        unpair(mul_pair(f[2 * e + 1], add_pair(pair(t[2], t[3]), pair(v.z, v.w))), lo, hi);
                         out[4 * q + 2 * e + 1] = pack_bf16x2(lo, hi);
                     }
                 }
@@ -205,16 +244,22 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->h_ready[group]);
+            if (lane == 0) mbar_arrive(&bars->h_ready[buf]);
+            buf = buf + 2 >= kBufs ? buf + 2 - kBufs : buf + 2;
+            bar += 2;
+            if (bar >= 2 * kBufs) {
+                bar -= 2 * kBufs;
+                ++turn;
+            }
         }
     } else if (warp >= 4 + kWorkers) {
         const int quad = warp & 3;
         const float* b = bias + 2 * padded;
-        uint32_t sbuf = 0;
+        uint32_t sbuf = 0, yb = 0, yturn = 0;
         for (unsigned int n = 0; n < count; ++n) {
-            if (!mbar_wait_warp(&bars->y_full[n & 1u], (n >> 1) & 1u, ctl, 0x8207)) break;
+            if (!mbar_wait_warp(&bars->y_full[yb], yturn & 1u, ctl, 0x8207)) break;
             tc_fence_after();
-            const uint32_t acc = tmem + kColY + 128 * (n & 1u) + (static_cast<uint32_t>(quad * 32) << 16);
+            const uint32_t acc = tmem + kColY + 64 * yb + (static_cast<uint32_t>(quad * 32) << 16);
             const int row = static_cast<int>(blockIdx.x + n * gridDim.x) * kTileM + quad * 32;
             for (int c = 0; c < prm.C; c += 32, ++sbuf) {
                 uint32_t v[32];
@@ -222,6 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
                 bulk_wait_read_but1();  // the buffer's last store has read it
                 __syncwarp();
                 tmem_wait_ld();
+                if (c + 32 >= prm.C) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->y_free[yb]);
+                }
                 const int buf = prm.off_store + (quad * 2 + static_cast<int>(sbuf & 1u)) * kStoreBytes;
                 uint8_t* dst = smem + buf + lane * 64;
                 const int sw = (lane >> 1) & 3;
@@ -244,9 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
                     bulk_commit();
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->y_free[n & 1u]);
+            if (++yb == y_bufs) {
+                yb = 0;
+                ++yturn;
+            }
         }
         bulk_wait_all();
     }
