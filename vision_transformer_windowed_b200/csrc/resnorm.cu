@@ -9,8 +9,16 @@ namespace fswin {
 
 namespace resn {
 
-template <typename TX, int W, int L, int V, bool S>
-__global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W * V <= 16 ? 3 : 2) : 1)
+// Blocks an SM that the registers have to leave room for: the loads of many rows in flight
+// are what hides the memory's latency.
+template <int W, int L, int V, bool kPost>
+__host__ __device__ constexpr int resident() {
+    return L > 256 ? 1 : (kPost ? (W * V <= 16 ? 3 : 2) : (W * V <= 16 ? 4 : (W * V <= 24 ? 3 : 2)));
+}
+
+// kPost: with a post norm, which takes the branch's row in fp32 beside the stream's.
+template <typename TX, int W, int L, int V, bool S, bool kPost>
+__global__ void __launch_bounds__(threads_of<L>(), resident<W, L, V, kPost>())
     fwd_kernel(const __grid_constant__ Params prm) {
     __shared__ float scratch[kScratch];
     const ResnormPtrs& p = prm.p;
@@ -34,17 +42,17 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W 
         // group must not read a row of another shift
         const unsigned int at_row = live ? row : prm.rows - 1u;
         const long long at = static_cast<long long>(at_row) * prm.C;
-        float x[W * V], y[W * V];
-        if (S) g.zero(x);
-        if (!S || live) g.load(static_cast<const TX*>(p.x) + at, x);
+        Stream<TX, W, L, V, S> held;
+        Held<W, L, V, S> f;
+        if (!S || live) held.load(g, static_cast<const TX*>(p.x) + at);
+        else held.zero();
         const float gt = gate ? static_cast<float>(gate[fdiv(prm.tokens, at_row)]) : 1.f;
-        if (gt != 0.f && (!S || live)) {
-            g.load(static_cast<const __nv_bfloat16*>(p.f) + at, y);
-        } else {  // a dropped sample takes nothing from its branch, whatever that holds
-#pragma unroll
-            for (int e = 0; e < W * V; ++e) y[e] = 0.f;
-        }
-        if (prm.post != kNone) {
+        // a dropped sample takes nothing from its branch, whatever that holds
+        if (gt != 0.f && (!S || live)) f.load(g, static_cast<const __nv_bfloat16*>(p.f) + at);
+        else f.zero();
+        float x[W * V], y[W * V];
+        f.take(y);
+        if constexpr (kPost) {
             normalise(g, y, prm.post, prm, scratch);
             float w[W * V];
             if (p.post_w) {
@@ -67,6 +75,7 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 32 ? (W 
 #pragma unroll
             for (int e = 0; e < W * V; ++e) y[e] *= w[e];
         }
+        held.take(x);
         if (gt != 0.f) {
 #pragma unroll
             for (int e = 0; e < W * V; ++e) x[e] = fmaf(gt, y[e], x[e]);
@@ -97,7 +106,8 @@ struct Launch {
     template <int W, int L, int V, bool S>
     cudaError_t go() const {
         const unsigned grid = grid_of(prm.rows, groups_of<L>(), static_cast<unsigned>(num_sms) * (2048 / threads_of<L>()), prm.C);
-        fwd_kernel<TX, W, L, V, S><<<grid, threads_of<L>(), 0, stream>>>(prm);
+        if (prm.post != kNone) fwd_kernel<TX, W, L, V, S, true><<<grid, threads_of<L>(), 0, stream>>>(prm);
+        else fwd_kernel<TX, W, L, V, S, false><<<grid, threads_of<L>(), 0, stream>>>(prm);
         return cudaGetLastError();
     }
     // Row shapes: eight-channel chunks, at most four a lane, the fewest idle lanes

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "geometry.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -232,6 +234,20 @@ struct Held {
         }
     }
 };
+
+// A row of the stream, bf16 or fp32, likewise.
+template <int W, int L, int V, bool S>
+struct HeldF32 {
+    float x[W * V];
+    __device__ __forceinline__ void zero() { Row<W, L, V, S>::zero(x); }
+    __device__ __forceinline__ void load(const Row<W, L, V, S>& g, const float* row) { g.load(row, x); }
+    __device__ __forceinline__ void take(float (&y)[W * V]) const {
+#pragma unroll
+        for (int e = 0; e < W * V; ++e) y[e] = x[e];
+    }
+};
+template <typename TX, int W, int L, int V, bool S>
+using Stream = std::conditional_t<sizeof(TX) == 2, Held<W, L, V, S>, HeldF32<W, L, V, S>>;
 
 constexpr int kThreads = 256;  // of a block, or L where a row takes more
 template <int L>
