@@ -109,7 +109,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
 // loop whole and elects a lane for the instructions themselves: descriptors and
 // coordinates then are the same in every lane and stay in uniform registers, which
 // these instructions read.  From a loop of one lane each operand is moved there first
-// (80 cycles a product in place of 40).
+// (attention forward with a bias table, M = 32: 628 us in place of 541).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));

@@ -11,6 +11,12 @@
 // they are consecutive, at constant offsets from one pointer.  That is one shared
 // load a score beside the one exponential a score, which the special function
 // unit serves at half the rate of those loads.
+//
+// Times on one B200 (3 heads): forward of 32 x 128 x 128 tokens, M = 32, shifted: 537 us,
+// 294 TFLOP/s, the exponentials alone 274 us; of 2 x 200 x 334, M = 16: 80 us.  Backward of
+// 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 857 us (300 TFLOP/s), post 23 us
+// (6.6 TB/s), sums 5 us.  Forward and main are bound by instruction issue and by the
+// waits between their links, not by the tensor products or the memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
