@@ -235,8 +235,8 @@ FS_API fs_status fs_winattn_relbias_bwd(const fs_winattn_shape* shape, const voi
  * deviations are fp32; n is the norm of r before r is rounded, and the backward
  * forms it again from the stored r.
  * Layout: x, f, r, n and their gradients [samples, tokens, channels], contiguous,
- * any alignment of their element (16-byte aligned tensors with channels a multiple
- * of 8 take 16-byte accesses); gate [samples]; parameters [channels]; rng: int64
+ * any alignment of their element (16-byte aligned tensors take 16-byte accesses, but
+ * for the ends of rows whose channels are no multiple of 8); gate [samples]; parameters [channels]; rng: int64
  * [2] in DEVICE memory, read when the kernel runs.  r may be x, n may be f, dx may
  * be dr, df may be dn (the same buffer, not a shifted one).
  * Shapes: 1 <= channels <= 8192, samples * tokens < 2^31 (both >= 0), eps >= 0 and
@@ -286,8 +286,9 @@ FS_API fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, c
  * computed.  Weight and bias gradients are summed over the tokens in fp32 in a fixed
  * order: results do not vary from run to run.
  * workspace: at least fs_gated_mlp_{fwd,bwd}_workspace_bytes(shape) bytes, 256-byte
- * aligned (2 bytes forward and 6 backward a token and hidden channel, and backward 192
- * bytes a weight of one matrix).
+ * aligned (forward 2 bytes a token and hidden channel, or 256 in all where the weights
+ * fit into an SM's shared memory; backward 6 bytes a token and hidden channel and 192 a
+ * weight of one matrix).
  */
 typedef enum { FS_ACT_SILU = 0, FS_ACT_GELU = 1 } fs_act;
 typedef struct {

@@ -252,7 +252,10 @@ def test_refused_feed_forward():
             ops.gated_mlp_fwd(*args, **kw)
     with pytest.raises(_lib.FswinError):
         ops.gated_mlp_fwd(cuda(5, 92), cuda(256, 92), cuda(256, 92), cuda(92, 256))
+    wide = cuda(5, 264), cuda(256, 264), cuda(256, 264), cuda(264, 256)  # weights beyond shared memory: h has a workspace
     with pytest.raises(_lib.FswinError):
-        ops.gated_mlp_fwd(x, w, w, wd, workspace=cuda(256, dtype=torch.uint8))
+        ops.gated_mlp_fwd(*wide, workspace=cuda(256, dtype=torch.uint8))
+    with pytest.raises(_lib.FswinError):
+        ops.gated_mlp_bwd(x, x, w, w, wd, workspace=cuda(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="dy has shape"):
         ops.gated_mlp_bwd(cuda(4, 96), x, w, w, wd)
