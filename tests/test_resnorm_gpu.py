@@ -171,3 +171,21 @@ def test_empty_batch():
     g = ops.residual_norm_bwd(dr.cuda(), dn.cuda(), r, d["f"], **{k: d[k] for k in PARAMS}, pre="layer")
     torch.cuda.synchronize()
     assert r.numel() == 0 and (g.dpre_weight == 0).all() and (g.dscale == 0).all() and g.dgate.numel() == 0
+
+
+@pytest.mark.parametrize("C,rows", [(1, 3400), (7, 3400), (33, 1200), (100, 1300), (513, 250), (1001, 300), (4098, 120),
+                                    (8178, 7), (8179, 7), (8190, 7)])
+def test_rows_off_a_boundary_many_a_group(C, rows):
+    """Channel counts that no chunk divides: every group of lanes walks several rows, the last group's is a part."""
+    check(3, rows, C, F32, "layer", "rms", p=0.2)
+    check(3, rows, C, BF16, "rms", None)
+
+
+@pytest.mark.parametrize("C", [33, 1001])
+def test_in_place_rows_off_a_boundary(C):
+    t, dr, dn = draw(2, 37, C, BF16, "layer", None)
+    d = cuda(t)
+    r, n = ops.residual_norm_fwd(**d, pre="layer")
+    x, f = d["x"].clone(), d["f"].clone()
+    r2, n2 = ops.residual_norm_fwd(**{**d, "x": x, "f": f}, pre="layer", r=x, n=f)
+    assert r2 is x and n2 is f and torch.equal(r2, r) and torch.equal(n2, n)

@@ -16,7 +16,6 @@ namespace fswin {
 namespace resn {
 
 enum : int { kNone = 0, kLayer = 1, kRms = 2 };
-constexpr int kMaxChannels = 8192;
 
 struct Params {
     ResnormPtrs p;
