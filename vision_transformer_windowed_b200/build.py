@@ -13,7 +13,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfswin.so")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "small.cu", "block.cu", "noalloc.cu", "wide.cu", "lrbias.cu", "relbias.cu",
            "relbias_small.cu", "resnorm.cu", "resnorm_bwd.cu", "mlp.cu", "mlp_small.cu"]
-HEADERS = ["dgeo.cuh", "geometry.cuh", "kernels.cuh", "ptx.cuh", "relbias.cuh", "resnorm.cuh",
+HEADERS = ["dgeo.cuh", "geometry.cuh", "kernels.cuh", "mlp.cuh", "ptx.cuh", "relbias.cuh", "resnorm.cuh",
            "rows.cuh", "schedule.cuh", "tile_io.cuh"]
 
 

@@ -8,7 +8,7 @@
 // written once: 64 x 256 rows of 384 channels, fp32 stream, with dropout, layer scale and
 // gate take 32 us, 3.5 TB/s: four reductions one after the other a row, with 16 warps an
 // SM to hide them, and the arithmetic of the mask; 3 x 1111 rows of 1001 channels with
-// both norms 34 us.  The parameters' gradients add up over the rows of a block (a lane
+// both norms 30 us (a chunk a lane: 34).  The parameters' gradients add up over the rows of a block (a lane
 // always holds the same channels), then over the block's row groups, and a second launch
 // adds the blocks' sums in order: no atomics, the same bits every run.
 #include "resnorm.cuh"
@@ -316,8 +316,8 @@ struct LaunchBwd {
     cudaError_t shifted() const {  // one chunk more than the channels fill
         const int n = (prm.C + 14) / 8;
         if (n <= 8) return go<8, 8, 1, true>();
-        if (n <= 32) return go<8, 32, 1, true>();
-        if (n <= 128) return go<8, 128, 1, true>();
+        if (n <= 32) return go<8, 16, 2, true>();
+        if (n <= 128) return go<8, 64, 2, true>();
         if (n <= 512) return go<8, 256, 2, true>();
         return go<8, 512, 2, true>();
     }
