@@ -200,3 +200,19 @@ def test_empty_batch_zeroes_the_table_gradient():
     inp = draw(0, 16, 16, 2, 8)
     got = run(inp, 8, 0)
     assert got["o"].numel() == 0 and (got["dtable"] == 0).all()
+
+
+@pytest.mark.parametrize("cfg", [(1, 8, 8, 700, 8, 0), (1, 8, 8, 500, 4, 0), (1, 16, 16, 200, 16, 0)])
+def test_more_heads_than_ctas(cfg):
+    inp = draw(*cfg[:5])
+    compare(run(inp, *cfg[4:]), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], *cfg[4:], dout=inp["dout"]))
+
+
+@pytest.mark.parametrize("cfg", [(1, 8, 8, 2, 4, 0), (1, 16, 16, 2, 8, 4), (1, 32, 32, 2, 16, 8)])
+def test_one_bucket_for_every_pair(cfg):
+    """A constant bias: the softmax does not see it, and its gradient is the sum of all dS, zero but for roundings."""
+    B, H, W, heads, M, s = cfg
+    buckets = torch.zeros((2 * M - 1, 2 * M - 1), dtype=torch.int32)
+    inp = draw(B, H, W, heads, M, 1)
+    compare(run(inp, M, s, buckets), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, buckets=buckets,
+                                                  dout=inp["dout"]))
