@@ -189,3 +189,21 @@ def test_in_place_rows_off_a_boundary(C):
     x, f = d["x"].clone(), d["f"].clone()
     r2, n2 = ops.residual_norm_fwd(**{**d, "x": x, "f": f}, pre="layer", r=x, n=f)
     assert r2 is x and n2 is f and torch.equal(r2, r) and torch.equal(n2, n)
+
+
+@pytest.mark.parametrize("stream", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pre,post", [("layer", None), ("rms", "layer"), ("layer", "rms")])
+@pytest.mark.parametrize("C,rows", [(33, 40), (36, 257), (97, 21), (1001, 3), (96, 5), (8, 70)])
+def test_no_epsilon_and_groups_past_the_last_row(C, rows, pre, post, stream):
+    """eps = 0 with a row count that leaves groups of lanes without a row: what those hold joins no sum."""
+    t, dr, dn = draw(1, rows, C, stream, pre, post, gate=False)
+    opt = dict(pre=pre, post=post, eps=0.0)
+    d = cuda(t)
+    r, n = ops.residual_norm_fwd(**d, **opt)
+    want = resnorm.step(**t, **opt)
+    close("r", r, want["r"], want["terms"]["r"])
+    close("n", n, want["n"], want["terms"]["n"])
+    at = resnorm.step(**{**t, "x": r.cpu().double() - (want["r"] - t["x"].double())}, **opt, dr=dr, dn=dn)
+    g = ops.residual_norm_bwd(dr.cuda(), dn.cuda(), r, d["f"], **{k: d[k] for k in PARAMS}, **opt)
+    for name, got in g._asdict().items():
+        close(name, got, at[name], at["terms"].get(name))

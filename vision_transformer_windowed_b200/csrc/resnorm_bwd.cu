@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 24 ? 2 :
     for (unsigned int base = blockIdx.x * kGroups; base < prm.rows; base += gridDim.x * kGroups) {
         const unsigned int row = base + own;
         const bool live = row < prm.rows;
-        // rows past the last are formed from the last one's r and f, and not stored; a
-        // shifted group must not read a row of another shift
+        // rows past the last are formed from the last one's r and f, and neither stored nor
+        // added up; a shifted group must not read a row of another shift, and its row of
+        // zeros has no deviation (with eps = 0 it normalises to NaN)
         const unsigned int at_row = live ? row : prm.rows - 1u;
         const bool reads = !S || live;
         const long long at = static_cast<long long>(at_row) * prm.C;
@@ -138,8 +139,8 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 24 ? 2 :
             else dn.zero();
             const float inv = normalise(g, hat, prm.pre, prm, scratch);
             dn.take(t);
-            if (wanted[kPreW]) slot(kPreW).add([&](int e) { return t[e] * hat[e]; });
-            if (wanted[kPreB]) slot(kPreB).add([&](int e) { return t[e]; });
+            if (live && wanted[kPreW]) slot(kPreW).add([&](int e) { return t[e] * hat[e]; });
+            if (live && wanted[kPreB]) slot(kPreB).add([&](int e) { return t[e]; });
             if (p.pre_w) {
                 float w[E];
                 g.load(static_cast<const TX*>(p.pre_w), w, !S);
@@ -194,14 +195,14 @@ __global__ void __launch_bounds__(threads_of<L>(), L <= 256 && W * V <= 24 ? 2 :
             for (int e = 0; e < E; ++e) d[e] *= gt;
         }
         if (p.scale) {
-            if (wanted[kScaleG]) slot(kScaleG).add([&](int e) { return d[e] * y[e]; });
+            if (live && wanted[kScaleG]) slot(kScaleG).add([&](int e) { return d[e] * y[e]; });
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] *= sc[e];
         }
         if (prm.drop) drop(d, keep, prm.keep_scale);
         if (post) {
-            if (wanted[kPostW]) slot(kPostW).add([&](int e) { return d[e] * hat[e]; });
-            if (wanted[kPostB]) slot(kPostB).add([&](int e) { return d[e]; });
+            if (live && wanted[kPostW]) slot(kPostW).add([&](int e) { return d[e] * hat[e]; });
+            if (live && wanted[kPostB]) slot(kPostB).add([&](int e) { return d[e]; });
             if (p.post_w) {
                 float w[E];
                 g.load(static_cast<const TX*>(p.post_w), w, !S);
