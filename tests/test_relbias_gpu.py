@@ -216,3 +216,39 @@ def test_one_bucket_for_every_pair(cfg):
     inp = draw(B, H, W, heads, M, 1)
     compare(run(inp, M, s, buckets), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, buckets=buckets,
                                                   dout=inp["dout"]))
+
+
+def places(M):
+    """Row and column displacement of every entry of a table without a bucket map."""
+    e = torch.arange((2 * M - 1) ** 2)
+    return e // (2 * M - 1) - (M - 1), e % (2 * M - 1) - (M - 1)
+
+
+@pytest.mark.parametrize("cfg", [(1, 16, 16, 1, 16, 0), (1, 32, 32, 1, 16, 8), (1, 32, 32, 1, 32, 0), (1, 64, 64, 1, 64, 0)])
+def test_a_small_entry_of_the_table_gradient_beside_large_ones(cfg):
+    """Keys to the right of their query get e^-25 of the weight: their entries of dtable are some 1e-9 of the others',
+    and as exact by the oracle's bound, which has no part of the others in it."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(*cfg[:5])
+    inp["dout"] = inp["dout"] * 64
+    right = places(M)[1] < 0
+    inp["table"][:, right] -= 25
+    ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"])
+    got = run(inp, M, s)["dtable"].double().cpu()
+    assert 0 < ref["dtable"][:, right].abs().max() < 1e-6 * ref["dtable"].abs().max()
+    assert ((got - ref["dtable"]).abs() <= err["dtable"] * (1 + 1e-3))[:, right].all()
+
+
+@pytest.mark.parametrize("cfg", [(1, 16, 16, 1, 16, 0), (1, 32, 32, 1, 32, 0), (1, 64, 64, 1, 64, 0)])
+def test_a_gradient_that_is_not_finite_reaches_its_own_displacements_only(cfg):
+    """The window's first token as query only has displacements that are not positive."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(*cfg[:5])
+    clean = run(inp, M, s)["dtable"]
+    inp["dout"][0, 0, 0] = INF
+    got = run(inp, M, s)["dtable"]
+    di, dj = places(M)
+    apart = ((di > 0) | (dj > 0)).cuda()
+    assert torch.isnan(got[:, ~apart]).all() and torch.isfinite(got[:, apart]).all()
+    # the first token adds nothing to those entries, finite or not
+    assert torch.equal(got[:, apart], clean[:, apart])

@@ -14,7 +14,7 @@
 //
 // Times on one B200 (3 heads): forward of 32 x 128 x 128 tokens, M = 32, shifted: 537 us,
 // 294 TFLOP/s, the exponentials alone 274 us; of 2 x 200 x 334, M = 16: 80 us.  Backward of
-// 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 857 us (300 TFLOP/s), post 23 us
+// 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 875 us (294 TFLOP/s), post 23 us
 // (6.6 TB/s), sums 5 us.  Forward and main are bound by instruction issue and by the
 // waits between their links, not by the tensor products or the memory.
 #include <cuda.h>
@@ -621,32 +621,46 @@ __host__ __device__ constexpr int sums_off(int kv_stages) { return stage_off(kv_
 // `quad` takes the blocks whose row displacement is quad modulo 4, so no two warps
 // touch one sum and every sum has a fixed order.  Lane (g, kp, m) walks block g's
 // keys 4 kk + kp and query quads kk + m (mod w / 4): eight bytes a load, and its
-// four columns e belong to displacement 4 m + e - kp, or w less once the quads wrap.
-// Blocks of equal displacement follow each other and add up in registers first.
+// four columns e belong to displacement 4 m + e - kp, or w less once the quads wrap,
+// each with a register of its own: a small sum beside a large one keeps its digits, and
+// a value that is not finite stays with its own.  Blocks of equal displacement follow
+// each other and add up there first.  What is added is dS as the products take it, in
+// bf16: it lies in shared memory only so, and half a step of a term, 2^-8, is what the
+// products' results (dQ, dK) carry too; the sums are fp32.
 template <int kBW>  // 4, 8, 16, 32, 64: the geometry's box width
 struct Diag {
     static constexpr int w = kBW < 32 ? kBW : 32;
     static constexpr int quads = w / 4;
     static constexpr int conc = 32 / w;         // blocks a warp walks at once
     static constexpr int nseg = kTile / w;
-    unsigned long long A[2], all[2];  // columns (0, 1), (2, 3): before the quads wrap, and all of them
+    unsigned long long A[2], B[2];  // columns (0, 1), (2, 3): before the quads wrap, and after
 
-    __device__ __forceinline__ void clear() { A[0] = A[1] = all[0] = all[1] = 0; }
+    __device__ __forceinline__ void clear() { A[0] = A[1] = B[0] = B[1] = 0; }
+    // One predicate a load.  (A sum of all columns and one with a weight of 0 or 1, and the
+    // second from their difference, took 858 us in place of 875 at 16 x 128 x 128 tokens, M =
+    // 32, and 176 in place of 173 at 2 x 200 x 334, M = 16: the difference lost the digits of
+    // a small sum beside a large one.)
+    __device__ __forceinline__ void add(unsigned long long v0, unsigned long long v1, int quad) {
+        asm("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %6, %7;\n\t"
+            "@p add.rn.f32x2 %0, %0, %4;\n\t@p add.rn.f32x2 %1, %1, %5;\n\t"
+            "@!p add.rn.f32x2 %2, %2, %4;\n\t@!p add.rn.f32x2 %3, %3, %5;\n\t}"
+            : "+l"(A[0]), "+l"(A[1]), "+l"(B[0]), "+l"(B[1])
+            : "l"(v0), "l"(v1), "r"(quad), "n"(quads));
+    }
     // Shared address of the lane's first load of a key segment's rows: key kp, query
     // column 0; and the lane's offsets from there for every kk (the swizzle of key row
     // r: 16-byte chunk index xor r & 7).
-    __device__ __forceinline__ void walk(uint32_t rows, const uint32_t (&off)[quads], uint32_t flip,
-                                         const unsigned long long (&before)[quads]) {
+    __device__ __forceinline__ void walk(uint32_t rows, const uint32_t (&off)[quads], uint32_t flip, int m) {
 #pragma unroll
         for (int kk = 0; kk < quads; ++kk) {
             uint32_t x, y;
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(rows + (off[kk] ^ flip)));
             const unsigned long long v0 = pair(x << 16, x & 0xFFFF0000u), v1 = pair(y << 16, y & 0xFFFF0000u);
-            all[0] = add_pair(all[0], v0);
-            all[1] = add_pair(all[1], v1);
             if (quads > 1) {
-                A[0] = fma_pair(v0, before[kk], A[0]);
-                A[1] = fma_pair(v1, before[kk], A[1]);
+                add(v0, v1, kk + m);
+            } else {
+                A[0] = add_pair(A[0], v0);
+                A[1] = add_pair(A[1], v1);
             }
         }
     }
@@ -656,12 +670,10 @@ struct Diag {
     // a step of their own.
     __device__ __forceinline__ void flush(float* dst, int m) {
         float a[4], b[4];
-        unpair(quads > 1 ? A[0] : all[0], a[0], a[1]);
-        unpair(quads > 1 ? A[1] : all[1], a[2], a[3]);
-        unpair(all[0], b[0], b[1]);
-        unpair(all[1], b[2], b[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] -= a[e];  // the wrapped ones
+        unpair(A[0], a[0], a[1]);
+        unpair(A[1], a[2], a[3]);
+        unpair(B[0], b[0], b[1]);
+        unpair(B[1], b[2], b[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             dst[e] += a[e];
@@ -676,11 +688,8 @@ struct Diag {
                                                 int quad, int lane, int side) {
         const int kp = lane & 3, m = (lane >> 2) & (quads - 1), gi = lane / (4 * quads);
         uint32_t off[quads];
-        unsigned long long before[quads];  // (1, 1) until the quads wrap, then (0, 0)
 #pragma unroll
         for (int kk = 0; kk < quads; ++kk) {
-            const float f = kk + m < quads ? 1.f : 0.f;
-            before[kk] = pair(f, f);
             const uint32_t r = 4 * kk + kp, p = (kk + m) & (quads - 1);
             off[kk] = ((r >> 3) << 10) + ((r & 7) << 7) + ((((p >> 1) ^ (r & 7)) << 4) | ((p & 1) << 3));
         }
@@ -704,7 +713,7 @@ struct Diag {
             // 4 .. 7 have the swizzle's bit 2 set
             const uint32_t rows = ds + ((q0 >> 6) << 14) + (((a * w) >> 3) << 10) + (w == 4 ? ((a & 1) << 9) : 0);
             const uint32_t flip = (((q0 & 63) >> 3) ^ (w == 4 ? ((a & 1) << 2) : 0)) << 4 | (w == 4 ? ((q0 & 4) << 1) : 0);
-            d.walk(rows, off, flip, before);
+            d.walk(rows, off, flip, m);
         };
         if (kBW == 64) {  // two rows of two 32-column segments
 #pragma unroll 1
