@@ -3,7 +3,7 @@ on the error of an implementation with bf16 operands and results and fp32 arithm
 
 Half a step of bf16 is 2^-8 of the value; EPS32 = 2^-16 of the sum of the absolute terms covers fp32 products and sums
 (a tensor-core sum over K terms and over the splits: below 2^-16 for K up to some 10^5 random terms), the activation's
-approximation (absolute error 1.5e-7 of the error function) and its exponential."""
+approximation (relative error 1e-5 of Phi) and its exponential."""
 from __future__ import annotations
 
 import math

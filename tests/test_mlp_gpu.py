@@ -135,3 +135,39 @@ def test_long_contractions_over_many_tokens():
     want, bound = mlp.full(**d, act="silu", dy=dy.cuda())
     cpu = lambda x: {k: v.cpu() for k, v in x.items()}  # noqa: E731
     compare(dict(y=y, **g._asdict()), cpu(want), cpu(bound))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("C", [8, 136])
+def test_every_digit_of_the_activation(C, act):
+    """One hidden unit at every bf16 value from -12.5 to 12.5: y = act(g) and dx = act'(g), right to the rounding of the
+    product's operand and of the result.  Sizes whose forward is one kernel, and two.  2^-14 of a value's terms for the
+    fp32 steps (an exponent of up to 113 in fp32: 113 2^-24 ln 2 < 2^-17.6, and a few steps of 2^-20)."""
+    bits = torch.arange(0, 0x4148 + 1, dtype=torch.int32).to(torch.int16)  # 0 .. 12.5
+    g = bits.view(BF16)
+    g = torch.cat([g[g >= 2.0 ** -20], -g[g >= 2.0 ** -20], torch.zeros(1, dtype=BF16)])
+    assert g.max() == 12.5 and len(g) > 6000
+    x = torch.zeros((len(g), C), dtype=BF16)
+    x[:, 0] = g
+    w_gate, w_up, w_down = (torch.zeros(n, dtype=BF16) for n in ((8, C), (8, C), (C, 8)))
+    w_gate[0, 0] = w_down[0, 0] = 1
+    b_up = torch.ones(8, dtype=BF16)
+    d = [t.cuda() for t in (x, w_gate, w_up, w_down)]
+    y = ops.gated_mlp_fwd(*d, b_up=b_up.cuda(), act=act)[:, 0].double().cpu()
+    dy = torch.zeros_like(d[0])
+    dy[:, 0] = 1
+    dx = ops.gated_mlp_bwd(dy, *d, b_up=b_up.cuda(), act=act).dx[:, 0].double().cpu()
+    a = g.double()
+    if act == "silu":
+        s = torch.sigmoid(a)
+        want, slope, terms = a * s, s * (1 + a * (1 - s)), s * (1 + a.abs() * (1 - s))
+    else:
+        cdf = 0.5 * torch.erfc(-a / 2 ** 0.5)
+        phi = torch.exp(-0.5 * a * a) / (2 * torch.pi) ** 0.5
+        want, slope, terms = a * cdf, cdf + a * phi, cdf + a.abs() * phi
+    half = torch.finfo(BF16).eps / 2
+    # h is rounded, and y is h; dg is rounded, and dx is dg
+    over = (y - want).abs() - (half + 2.0 ** -14) * want.abs()
+    assert over.max() <= 0, f"act({float(a[over.argmax()])}): {float(y[over.argmax()])}, {float(want[over.argmax()])}"
+    over = (dx - slope).abs() - half * slope.abs() - 2.0 ** -14 * terms
+    assert over.max() <= 0, f"act'({float(a[over.argmax()])}): {float(dx[over.argmax()])}, {float(slope[over.argmax()])}"
