@@ -192,8 +192,13 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
  * the bucket and n_buckets must be (2M-1)^2 (else FS_ERR_SHAPE).  A bucket outside
  * [0, n_buckets) adds no bias and takes no gradient.  An entry of -inf keeps its
  * pairs apart; a query left without a key has o = 0, lse = -inf and no gradient.
- * Finite entries beyond 8.5e37 in magnitude act as that value; a query whose
- * log-sum-exp lies beyond 1e30 in magnitude takes part in no gradient.
+ * Finite entries beyond 8.5e37 in magnitude act as that value.  A query whose every
+ * key has a large entry (the type's lowest value as a mask, say) has the softmax of its
+ * biased scores as fp32 holds them, the uniform one where a step of fp32 exceeds the
+ * scores (from about 1e9 on), forward and backward alike.  (The backward forms such a
+ * row's maximum and sum again, key by key, which is slow.)  Where the scores q . k alone
+ * make a log-sum-exp beyond 2800 in magnitude, the gradient carries fp32's step there
+ * (2^-11 of a probability, growing with it), and has no part of the query beyond 7e29.
  *
  * Forward: o and lse (lse may be NULL: inference), overwritten.
  * Backward: dq, dk, dv and dtable (bf16 [heads][n_buckets]: the gradient summed in
@@ -202,7 +207,7 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
  * reductions whose order varies from run to run; everything else, and at M <= 8
  * every output, is the same from run to run.  workspace: at least
  * fs_winattn_relbias_bwd_workspace_bytes(shape) bytes, 256-byte aligned (M >= 16:
- * 136 bytes per token-head on the padded grid; and 4 bytes a displacement for
+ * 144 bytes per token-head on the padded grid; and 4 bytes a displacement for
  * every head and CTA).  Other arguments, layouts, ownership and errors as
  * fs_winattn_fwd / fs_winattn_bwd.  At M = 8 and M = 4, where windows share a
  * tile, values that are not finite stay inside their own window.

@@ -252,3 +252,57 @@ def test_a_gradient_that_is_not_finite_reaches_its_own_displacements_only(cfg):
     assert torch.isnan(got[:, ~apart]).all() and torch.isfinite(got[:, apart]).all()
     # the first token adds nothing to those entries, finite or not
     assert torch.equal(got[:, apart], clean[:, apart])
+
+LOWEST = torch.finfo(torch.bfloat16).min
+FAR = [(1, 8, 12, 2, 4, 0), (2, 16, 16, 2, 8, 0), (1, 20, 13, 2, 8, 4), (1, 16, 32, 2, 16, 0), (1, 32, 32, 2, 16, 4),
+       (1, 40, 36, 2, 16, 12), (1, 64, 64, 2, 32, 16), (1, 64, 64, 2, 64, 0), (1, 64, 70, 2, 64, 16)]
+
+
+@pytest.mark.parametrize("cfg", FAR)
+def test_lowest_value_for_every_key_of_a_row(cfg):
+    """The type's lowest value as a mask.  Head 0: every entry, each row is the uniform one.  Head 1: all but the keys
+    of the rows below, so that only the queries of a window's last row have none but masked keys."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(*cfg[:5])
+    inp["table"][0] = LOWEST
+    inp["table"][1, places(M)[0] >= 0] = LOWEST
+    ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"])
+    compare(run(inp, M, s), ref, err, keys=("o", "dq", "dk", "dv", "dtable"))
+
+
+@pytest.mark.parametrize("cfg", FAR)
+@pytest.mark.parametrize("value", [-1e9, 1e9, -3e20])
+def test_large_entries_for_every_key_of_a_row(cfg, value):
+    """Half a step of fp32 at 1e9 log2(e) is 64, more than any score: as with the lowest value.  The bits are the same,
+    but for dq, whose sums at M >= 16 come in any order."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(*cfg[:5])
+    inp["table"][0] = LOWEST
+    inp["table"][1, places(M)[1] > 0] = LOWEST
+    inp["table"][1, places(M)[1] <= 0] = -INF
+    want = run(inp, M, s)
+    inp["table"][0] = value
+    inp["table"][1, places(M)[1] > 0] = value
+    inp["table"][1, places(M)[1] <= 0] = value - 3 * abs(value)
+    got = run(inp, M, s)
+    assert all(torch.isfinite(got[key]).all() for key in ("o", "dq", "dk", "dv", "dtable"))
+    for key in ("o", "dk", "dv"):
+        assert torch.equal(got[key][..., 0, :], want[key][..., 0, :]), key
+    rows = torch.isfinite(want["lse"][..., 1])  # queries with a key to their left in their region
+    assert 0 < rows.sum() < rows.numel() and torch.equal(got["o"][..., 1, :][rows], want["o"][..., 1, :][rows])
+    assert torch.equal(got["dtable"][0], want["dtable"][0])
+    size = want["dq"].float().abs().max()
+    assert (got["dq"].float() - want["dq"].float())[:, :, :, 0].abs().max() <= 2.0 ** -7 * size
+
+
+@pytest.mark.parametrize("cfg", FAR)
+@pytest.mark.parametrize("value", [-9984.0, 9984.0])
+def test_a_bias_of_ten_thousand_for_every_key(cfg, value, monkeypatch):
+    """A constant: the plain softmax, from scores that fp32 holds to half a step of 2^-10 beside it (base 2), each way
+    and in the row's own maximum: less than 2^-9 of a probability."""
+    B, H, W, heads, M, s = cfg
+    inp = draw(*cfg[:5])
+    inp["table"][:] = value
+    monkeypatch.setattr(relbias, "EPS_P", 2.0 ** -9)
+    ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"])
+    compare(run(inp, M, s), ref, err)

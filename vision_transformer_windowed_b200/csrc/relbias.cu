@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace bwd {
 
 struct WsLayout {
-    size_t acc, rowv, part, disp, total;
+    size_t acc, rowv, far, part, disp, total;
     int streams;  // partial sums of the table gradient a head
 };
 
@@ -517,6 +517,7 @@ __host__ inline WsLayout ws_layout(const Geo& g) {
     if (g.N >= kTile) {
         L.acc = o;  o += round256(ht * kTile * kHeadDim * 4);  // fp32 dQ [heads][tiles][128][32], 16-byte chunks permuted
         L.rowv = o; o += round256(ht * kTile * 8);             // per (head, tile): -lse log2(e) [128], -D [128]
+        L.far = o;  o += round256(ht * kTile * 8);             // far_row's terms, of rows whose -lse log2(e) is -inf
         const int W = workers(g);
         L.streams = W * streams_per_head((g.tiles + W - 1) / W, g.heads, kSms);
     } else {
@@ -530,7 +531,7 @@ __host__ inline WsLayout ws_layout(const Geo& g) {
 
 struct Params {
     Geo g;
-    const uint8_t *o, *dout;
+    const uint8_t *q, *k, *o, *dout;
     uint8_t *dq, *dk, *dv;
     const float* lse;
     const __nv_bfloat16* table;
@@ -538,6 +539,7 @@ struct Params {
     int n_buckets;
     float* acc;
     float* rowv;
+    float2* far;
     float* part;
     unsigned int* status;
     unsigned long long limit_ns;
@@ -548,7 +550,7 @@ struct Params {
 
 // prep: per (tile, head), thread = slot row: D = dO . O and the row's log-sum-exp
 // in base-2 units, and the zeroed dQ accumulator row.  Memory only.
-__global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(128, 16) prep_kernel(const __grid_constant__ Params p) {
     const Geo& g = p.g;
     const long long T = blockIdx.x / g.heads;
     const int h = static_cast<int>(blockIdx.x - T * g.heads);
@@ -556,7 +558,8 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Param
     const int r = threadIdx.x;
     int pi, pj;
     long long tok;
-    float D = 0.f, lse2 = INFINITY;  // a row outside the grid: no probability
+    float D = 0.f;
+    float2 l = make_float2(-INFINITY, 0.f);  // a row outside the grid: no probability
     uint4* acc = reinterpret_cast<uint4*>(p.acc + ht * kTile * kHeadDim);
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c * 128 + r] = make_uint4(0, 0, 0, 0);
@@ -574,9 +577,19 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Param
                             fmaf(bf16hi_to_f32(xs[e]), bf16hi_to_f32(ys[e]), d[e]));
         }
         D = (d[0] + d[1]) + (d[2] + d[3]);
-        lse2 = grad_lse2(__ldg(p.lse + tok));
+        const float lse = __ldg(p.lse + tok);
+        l.x = -grad_lse2(lse);
+        if (finite_beyond(lse * 1.4426950408889634f, kFar))
+            l = far_row(g, p.q, p.k, p.table + static_cast<long long>(h) * p.n_buckets, p.buckets, p.n_buckets, T, r, h,
+                        lse * 1.4426950408889634f);
     }
-    p.rowv[ht * 2 * kTile + r] = -lse2;  // negated: the main kernel adds them, packed
+    // Rows with a second term have no probability for the main kernel; the one for far
+    // tables looks here for every row that has none.
+    if (l.y != 0.f || l.x == -INFINITY) {
+        p.far[ht * kTile + r] = l;
+        l.x = -INFINITY;
+    }
+    p.rowv[ht * 2 * kTile + r] = l.x;  // negated: the main kernel adds them, packed
     p.rowv[ht * 2 * kTile + kTile + r] = -D;
 }
 
@@ -742,7 +755,12 @@ struct Diag {
     }
 };
 
-template <int kBW, int kWorkers>
+// kFarTable: a second launch, in which CTAs of heads without far entries leave at once.  It
+// takes all rows, those with a second term (prep_kernel) among them, forms dK, dV and the
+// table's sums again, and adds dQ of those rows alone.  A branch of the one kernel, or a way
+// out of it, would be simpler, but made it slower for every call (16 x 128 x 128, M = 32:
+// 875 us; with either 912 to 915, and the second launch takes 5).
+template <int kBW, int kWorkers, bool kFarTable>
 __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     main_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
@@ -764,6 +782,10 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     const long long stride = static_cast<long long>(kWorkers) * prm.streams;
     const long long X0 = static_cast<long long>(kWorkers) * (blockIdx.x / g.heads) + wk;
     const long long item0 = static_cast<long long>(h) * g.tiles;
+    const __nv_bfloat16* table_h = prm.table + static_cast<long long>(h) * prm.n_buckets;
+    if (kFarTable &&
+        !__syncthreads_or(build_bias(tab, pitch, table_h, prm.buckets, prm.n_buckets, g.M, tid, kThreads)))
+        return;
 
     if (tid == 0) {
         for (int w = 0; w < kWorkers; ++w) {
@@ -786,8 +808,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         tmem_relinquish();
     }
     build_masks(g, &bars->masks, tid, kThreads);
-    build_bias(tab, pitch, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, g.M, tid,
-               kThreads);
+    if (!kFarTable) build_bias(tab, pitch, table_h, prm.buckets, prm.n_buckets, g.M, tid, kThreads);
     if (computes)
         for (int e = tid & 255; e < side * side; e += 256) sums[e] = 0.f;
     tc_fence_before();
@@ -945,6 +966,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                     break;
                 }
                 tc_fence_after();
+                const float2* terms = prm.far + (item0 + I.w0 + T) * kTile;
                 auto gradient_half = [&](auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
 #pragma unroll 1
@@ -966,8 +988,17 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                             for (int f = 0; f < 2; ++f) {
                                 const int i = e + f;
                                 float p0, p1, d0, d1;
-                                unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
-                                                f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                                if (kFarTable) {
+                                    float2 l0 = make_float2(f ? L.z : L.x, 0.f), l1 = make_float2(f ? L.w : L.y, 0.f);
+                                    if (l0.x == -INFINITY) l0 = __ldg(terms + 16 * c16 + 2 * i);
+                                    if (l1.x == -INFINITY) l1 = __ldg(terms + 16 * c16 + 2 * i + 1);
+                                    unpair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]), p0, p1);
+                                    p0 = far_exponent(p0, l0.x, l0.y);
+                                    p1 = far_exponent(p1, l1.x, l1.y);
+                                } else {
+                                    unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
+                                                    f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                                }
                                 p0 = ex2_approx(p0);
                                 p1 = ex2_approx(p1);
                                 unpair(mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]),
@@ -992,7 +1023,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                                 make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
                     }
                 };
-                if (I.kind) gradient_half(std::true_type{});
+                if (kFarTable || I.kind) gradient_half(std::true_type{});
                 else gradient_half(std::false_type{});
                 tmem_wait_st();
                 fence_proxy_async_smem();
@@ -1010,6 +1041,10 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                     tmem_ld32(trow + (wg == 0 ? kColDV : kColDK), v);
                     tmem_ld16(trow + kColDQ + 16 * wg, q);
                     tmem_wait_ld();
+                    if (kFarTable && reinterpret_cast<const float*>(neg_l)[r] != -INFINITY) {  // added by the first launch
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) q[e] = 0u;
+                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) acc[e] = add_pair(acc[e], pair(v[2 * e], v[2 * e + 1]));
                     // half of dQ's query row over the step's Q and dO tiles, 16-byte chunks
@@ -1211,6 +1246,8 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
     } else {
         bwd::Params prm{};
         prm.g = g;
+        prm.q = static_cast<const uint8_t*>(p.q);
+        prm.k = static_cast<const uint8_t*>(p.k);
         prm.o = static_cast<const uint8_t*>(p.o);
         prm.dout = static_cast<const uint8_t*>(p.dout);
         prm.dq = static_cast<uint8_t*>(p.dq);
@@ -1222,6 +1259,7 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
         prm.n_buckets = p.n_buckets;
         prm.acc = reinterpret_cast<float*>(p.ws + L.acc);
         prm.rowv = reinterpret_cast<float*>(p.ws + L.rowv);
+        prm.far = reinterpret_cast<float2*>(p.ws + L.far);
         prm.part = part;
         prm.status = status;
         prm.limit_ns = limit_ns;
@@ -1243,18 +1281,24 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
         e = cudaGetLastError();
         mark(1);
         if (e == cudaSuccess) {
-            static SmemOptIn optin[2][5];
+            static SmemOptIn optin[2][2][5];
             using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, bwd::Params);
-            static const Kernel kernels[2][5] = {
-                {bwd::main_kernel<4, 1>, bwd::main_kernel<8, 1>, bwd::main_kernel<16, 1>, bwd::main_kernel<32, 1>,
-                 bwd::main_kernel<64, 1>},
-                {bwd::main_kernel<4, 2>, bwd::main_kernel<8, 2>, bwd::main_kernel<16, 2>, bwd::main_kernel<32, 2>,
-                 nullptr},  // boxes of 64 tokens: M = 64 only
+            static const Kernel kernels[2][2][5] = {
+                // the nulls: boxes of 64 tokens, M = 64 only
+                {{bwd::main_kernel<4, 1, false>, bwd::main_kernel<8, 1, false>, bwd::main_kernel<16, 1, false>,
+                  bwd::main_kernel<32, 1, false>, bwd::main_kernel<64, 1, false>},
+                 {bwd::main_kernel<4, 2, false>, bwd::main_kernel<8, 2, false>, bwd::main_kernel<16, 2, false>,
+                  bwd::main_kernel<32, 2, false>, nullptr}},
+                {{bwd::main_kernel<4, 1, true>, bwd::main_kernel<8, 1, true>, bwd::main_kernel<16, 1, true>,
+                  bwd::main_kernel<32, 1, true>, bwd::main_kernel<64, 1, true>},
+                 {bwd::main_kernel<4, 2, true>, bwd::main_kernel<8, 2, true>, bwd::main_kernel<16, 2, true>,
+                  bwd::main_kernel<32, 2, true>, nullptr}},
             };
             const int kind = ilog2_exact(g.bw) - 2;
-            const Kernel kern = kernels[W - 1][kind];
-            e = optin[W - 1][kind].ensure(reinterpret_cast<const void*>(kern), kSmemLimit);
-            if (e == cudaSuccess) {
+            for (int far = 0; far < 2 && e == cudaSuccess; ++far) {
+                const Kernel kern = kernels[far][W - 1][kind];
+                e = optin[far][W - 1][kind].ensure(reinterpret_cast<const void*>(kern), kSmemLimit);
+                if (e != cudaSuccess) break;
                 kern<<<static_cast<unsigned>(prm.streams) * g.heads, 256 * W + 128, smem, stream>>>(maps.q, maps.k, maps.v,
                                                                                              maps.dout, prm);
                 e = cudaGetLastError();

@@ -13,6 +13,7 @@
 
 #include "geometry.cuh"
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace fswin {
 
@@ -51,21 +52,93 @@ __device__ __forceinline__ float bias_entry(const __nv_bfloat16* table_h, const 
     return v * 1.4426950408889634f;
 }
 
-__device__ __forceinline__ void build_bias(float* tab, int pitch, const __nv_bfloat16* table_h, const int* buckets,
+// Beyond this magnitude (base 2) a log-sum-exp is a far one: the fp32 steps on the way to
+// it are 2^-11 there, and the gradient's P = exp2(t - lse2) has them as a relative error.
+// Up to here that is below 2^-11, a quarter of what P's rounding to bf16 may add; at 2^24
+// it is a factor of two, at 2^31 zero or infinity.  An entry of half that makes a table a
+// far one.
+constexpr float kFar = 4096.f;
+__device__ __forceinline__ bool finite_beyond(float v, float limit) { return fabsf(v) > limit && !isinf(v); }
+
+// Returns whether this thread has met a far entry.
+__device__ __forceinline__ bool build_bias(float* tab, int pitch, const __nv_bfloat16* table_h, const int* buckets,
                                            int n_buckets, int M, int tid, int nt) {
     const int side = 2 * M - 1;
+    bool far = false;
     for (int e = tid; e < side * side; e += nt) {
         const int y = e / side, x = e - y * side;
-        tab[y * pitch + x] = bias_entry(table_h, buckets, n_buckets, e);
+        const float v = bias_entry(table_h, buckets, n_buckets, e);
+        tab[y * pitch + x] = v;
+        far |= finite_beyond(v, kFar / 2);
     }
+    return far;
 }
 
 // A row's log-sum-exp in base-2 units for the gradient's P = exp2(t - lse2).  +inf
-// (no probability) for a row without a key, and for one whose every entry is so
-// large that its log-sum-exp in fp32 no longer tells the row's scores apart.
+// (no probability) for a row without a key.
 __device__ __forceinline__ float grad_lse2(float lse) {
     const float v = lse * 1.4426950408889634f;
     return fabsf(v) > 1e30f ? INFINITY : v;  // a NaN stays one
+}
+
+// Rows whose every key has a large bias (the type's lowest value as a mask, say) have a
+// log-sum-exp in which the sum of their exponentials is lost.  For them P = exp2((t - m) -
+// log2 l) with the maximum m and the sum l of the row's own scores, formed again here, key
+// by key on the CUDA cores: rare, so it may be slow.  The result (x, y) stands for the two
+// terms of log2 P = (t + x) + y.  A far log-sum-exp that the scores alone make (no far
+// entry) stays what it is.
+// X, r: the row's tile and slot.  lse2: its log-sum-exp, far.
+static __device__ __noinline__ float2 far_row(const Geo& g, const uint8_t* q, const uint8_t* k,
+                                              const __nv_bfloat16* table_h, const int* buckets, int n_buckets,
+                                              long long X, int r, int h, float lse2) {
+    Win w = tile_win(g, X);
+    const int widx = r >> (g.lnbw + g.lBT);
+    if (widx) w = win_of(g, w.gw + widx);
+    int pi, pj;
+    tile_row_pos(g, X, r, &pi, &pj);
+    auto row_at = [&](const uint8_t* base, int i, int j) -> const uint4* {  // null outside the grid
+        int row = w.wr * g.M + i + g.s, col = w.wc * g.M + j + g.s;
+        if (row >= g.Hp) row -= g.Hp;
+        if (col >= g.Wp) col -= g.Wp;
+        if (row >= g.H || col >= g.W) return nullptr;
+        return reinterpret_cast<const uint4*>(
+            base + (((static_cast<long long>(w.b) * g.H + row) * g.W + col) * g.heads + h) * kRowBytes);
+    };
+    const bool cut_i = g.s && (w.wr + 1) * g.M == g.Hp, cut_j = g.s && w.wc + 1 == g.nWw;
+    const int edge = g.M - g.s;
+    const uint4* mine = row_at(q, pi, pj);  // the row is a token
+    float m = -INFINITY, l = 0.f;
+    bool far = false;
+    for (int u = 0; u < g.N; ++u) {
+        const int i = u / g.M, j = u - i * g.M;
+        if ((cut_i && (i >= edge) != (pi >= edge)) || (cut_j && (j >= edge) != (pj >= edge))) continue;
+        const uint4* key = row_at(k, i, j);
+        float s = 0.f;
+        for (int c = 0; key && c < 4; ++c) {
+            const uint4 a = __ldg(mine + c), b = __ldg(key + c);
+            const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s = fmaf(bf16lo_to_f32(as[e]), bf16lo_to_f32(bs[e]), fmaf(bf16hi_to_f32(as[e]), bf16hi_to_f32(bs[e]), s));
+        }
+        const float bias = bias_entry(table_h, buckets, n_buckets, (pi - i + g.M - 1) * (2 * g.M - 1) + pj - j + g.M - 1);
+        far |= finite_beyond(bias, kFar / 2);
+        const float t = fmaf(s, g.scale_log2, bias);
+        if (t > m) {
+            l = fmaf(l, ex2_approx(m - t), 1.f);
+            m = t;
+        } else if (t != -INFINITY) {
+            l += ex2_approx(t - m);  // a NaN stays one
+        }
+    }
+    if (!far) return make_float2(-grad_lse2(lse2 * 0.69314718055994530942f), 0.f);
+    return fabsf(m) > kFar ? make_float2(-m, -lg2_approx(l)) : make_float2(-(m + lg2_approx(l)), 0.f);
+}
+
+// log2 P of a far table's rows: P is at most 1, also where t rounds to another side than m did.
+__device__ __forceinline__ float far_exponent(float t, float x, float y) {
+    const float d = t + x;
+    return (d > 0.f ? 0.f : d) + y;  // a NaN stays one
 }
 
 // Every CTA serves one head (its table, and the table gradient it sums, belong to

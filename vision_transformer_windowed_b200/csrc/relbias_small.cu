@@ -12,6 +12,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "dgeo.cuh"
 #include "geometry.cuh"
 #include "kernels.cuh"
@@ -367,8 +369,8 @@ constexpr int kWarpMover = 4;
 constexpr int kSlotBytes = 4 * kTileBytes;          // q, k, v, dO tiles of one item
 constexpr int kOOff = 2 * kSlotBytes;               // o tile
 constexpr int kDSOff = kOOff + kTileBytes;          // dS: per window 64 keys x 64 queries, 128-byte swizzle
-constexpr int kVecOff = kDSOff + 2 * kTileBytes;    // lse2[128], D[128]
-constexpr int kTabOff = kVecOff + 2 * kTile * 4;
+constexpr int kVecOff = kDSOff + 2 * kTileBytes;    // -lse2[128], -D[128], far_row's second term[128]
+constexpr int kTabOff = kVecOff + 3 * kTile * 4;
 constexpr int kBarOff = (kTabOff + 15 * kP8 * 4 + 15) / 16 * 16;
 constexpr int kSmemBytes = kBarOff + 128 + 1024;
 static_assert(kDSOff % 1024 == 0, "128-byte swizzled operand must be 1024-byte aligned");
@@ -438,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    build_bias(tab, kP8, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, kM8, tid,
-               kThreads);
+    const __nv_bfloat16* table_h = prm.table + static_cast<long long>(h) * prm.n_buckets;
+    const bool met_far = build_bias(tab, kP8, table_h, prm.buckets, prm.n_buckets, kM8, tid, kThreads);
     tc_fence_before();
-    __syncthreads();
+    const bool far_table = __syncthreads_or(met_far) != 0;
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     const Ctl ctl{prm.status, &bars->abort_flag, prm.limit_ns};
@@ -532,17 +534,18 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
         const unsigned long long sl2_2 = pair(g.scale_log2, g.scale_log2);
         float* neg_l = reinterpret_cast<float*>(smem + kVecOff);  // -lse2 and -D of the tile's queries
         float* neg_d = neg_l + kTile;
+        float* far_y = neg_d + kTile;
         const int e_r = r & 63;
         const float* brow = tab + (kM8 - 1 - slot_i<kBW>(e_r)) * kP8 + kM8 - 1 - slot_j<kBW>(e_r);
         uint8_t* dsrow = smem + kDSOff + wi * 8192 + (e_r >> 3) * 1024 + (r & 7) * 128;
         uint32_t gph = 0;
         uint32_t groups = 0;
-        auto lse2_of = [&](long long j) {
+        auto lse_of = [&](long long j) {
             long long tok;
             const bool valid = row_of<kBW>(g, tile_at(j), r, h, &tok, &groups);
-            return valid ? grad_lse2(__ldg(prm.lse + tok)) : INFINITY;  // outside the grid: no probability
+            return valid ? __ldg(prm.lse + tok) : -INFINITY;  // outside the grid: no probability
         };
-        float lse2 = n > 0 ? lse2_of(0) : 0.f;
+        float lse = n > 0 ? lse_of(0) : 0.f;
         for (long long j = 0; j < n; ++j) {
             const uint32_t ph = static_cast<uint32_t>(j & 1);
             uint8_t* sl = smem + (j & 1) * kSlotBytes;
@@ -561,7 +564,15 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
                 }
                 neg_d[r] = -((d4[0] + d4[1]) + (d4[2] + d4[3]));
             }
-            neg_l[r] = -lse2;
+            neg_l[r] = -grad_lse2(lse);
+            if (far_table) {
+                float2 f = make_float2(-grad_lse2(lse), 0.f);
+                if (finite_beyond(lse * 1.4426950408889634f, kFar))
+                    f = far_row(g, prm.q, prm.k, table_h, prm.buckets, prm.n_buckets, tile_at(j), r, h,
+                                lse * 1.4426950408889634f);
+                neg_l[r] = f.x;
+                far_y[r] = f.y;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->o_free);
             fence_proxy_async_smem();
@@ -583,54 +594,66 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
                 __syncwarp();
             }
             const uint32_t grp4 = groups;
-            if (j + 1 < n) lse2 = lse2_of(j + 1);
+            if (j + 1 < n) lse = lse_of(j + 1);
             if (!wwait(&bars->s_full, ph, 0x7307)) break;
             tc_fence_after();
+            auto gradient = [&](auto far) {
+                constexpr bool kFarTable = decltype(far)::value;  // rows may have a second term
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 16 queries: one region
-                uint32_t sv[16], pv[16];
-                tmem_ld16(trow + kColS + 64 * wi + 16 * c, sv);
-                tmem_ld16(trow + kColDP + 64 * wi + 16 * c, pv);
-                unsigned long long t[8];
+                for (int c = 0; c < 4; ++c) {  // 16 queries: one region
+                    uint32_t sv[16], pv[16];
+                    tmem_ld16(trow + kColS + 64 * wi + 16 * c, sv);
+                    tmem_ld16(trow + kColDP + 64 * wi + 16 * c, pv);
+                    unsigned long long t[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[e] = pair(brow[slot_off<kBW>(16 * c + 2 * e)], brow[slot_off<kBW>(16 * c + 2 * e + 1)]);
-                tmem_wait_ld();
-                const bool on = kBW == 8 || ((grp4 >> c) & 1u);
-                uint32_t wp[8], wd[8];
+                    for (int e = 0; e < 8; ++e)
+                        t[e] = pair(brow[slot_off<kBW>(16 * c + 2 * e)], brow[slot_off<kBW>(16 * c + 2 * e + 1)]);
+                    tmem_wait_ld();
+                    const bool on = kBW == 8 || ((grp4 >> c) & 1u);
+                    uint32_t wp[8], wd[8];
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 L = *reinterpret_cast<const float4*>(neg_l + 64 * wi + 16 * c + 2 * e);
-                    const float4 D = *reinterpret_cast<const float4*>(neg_d + 64 * wi + 16 * c + 2 * e);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 L = *reinterpret_cast<const float4*>(neg_l + 64 * wi + 16 * c + 2 * e);
+                        const float4 D = *reinterpret_cast<const float4*>(neg_d + 64 * wi + 16 * c + 2 * e);
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const int i = e + f;
-                        float p0, p1;
-                        unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
-                                        f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
-                        p0 = ex2_approx(p0);
-                        p1 = ex2_approx(p1);
-                        unsigned long long d =
-                            mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]), f ? pair(D.z, D.w) : pair(D.x, D.y)),
-                                     pair(p0, p1));
-                        wp[i] = pack_bf16x2(p0, p1);  // P and dS join their products in bf16, the operands' type
-                        if (kBW == 4) {
-                            wp[i] = on ? wp[i] : 0u;
-                            d = on ? d : 0ull;
+                        for (int f = 0; f < 2; ++f) {
+                            const int i = e + f;
+                            float p0, p1;
+                            if (kFarTable) {
+                                const float* y = far_y + 64 * wi + 16 * c + 2 * i;
+                                unpair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]), p0, p1);
+                                p0 = far_exponent(p0, f ? L.z : L.x, y[0]);
+                                p1 = far_exponent(p1, f ? L.w : L.y, y[1]);
+                            } else {
+                                unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
+                                                f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
+                            }
+                            p0 = ex2_approx(p0);
+                            p1 = ex2_approx(p1);
+                            unsigned long long d =
+                                mul_pair(add_pair(pair(pv[2 * i], pv[2 * i + 1]), f ? pair(D.z, D.w) : pair(D.x, D.y)),
+                                         pair(p0, p1));
+                            wp[i] = pack_bf16x2(p0, p1);  // P and dS join their products in bf16, the operands' type
+                            if (kBW == 4) {
+                                wp[i] = on ? wp[i] : 0u;
+                                d = on ? d : 0ull;
+                            }
+                            dacc[8 * c + i] = add_pair(dacc[8 * c + i], d);
+                            float d0, d1;
+                            unpair(d, d0, d1);
+                            wd[i] = pack_bf16x2(d0, d1);
                         }
-                        dacc[8 * c + i] = add_pair(dacc[8 * c + i], d);
-                        float d0, d1;
-                        unpair(d, d0, d1);
-                        wd[i] = pack_bf16x2(d0, d1);
                     }
-                }
-                tmem_st8(trow + kColP + 8 * c, wp);
-                tmem_st8(trow + kColDS + 8 * c, wd);
+                    tmem_st8(trow + kColP + 8 * c, wp);
+                    tmem_st8(trow + kColDS + 8 * c, wd);
 #pragma unroll
-                for (int q4 = 0; q4 < 2; ++q4)
-                    *reinterpret_cast<uint4*>(dsrow + (((2 * c + q4) ^ (r & 7)) << 4)) =
-                        make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
-            }
+                    for (int q4 = 0; q4 < 2; ++q4)
+                        *reinterpret_cast<uint4*>(dsrow + (((2 * c + q4) ^ (r & 7)) << 4)) =
+                            make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
+                }
+            };
+            if (far_table) gradient(std::true_type{});
+            else gradient(std::false_type{});
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
@@ -831,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
     const Geo& g = prm.g;
     const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
     const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
-    build_bias(tab, kP4, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, 4, r,
-               kThreads);
+    const __nv_bfloat16* table_h = prm.table + static_cast<long long>(h) * prm.n_buckets;
+    build_bias(tab, kP4, table_h, prm.buckets, prm.n_buckets, 4, r, kThreads);
     __syncthreads();
     const int e_r = r & 15, flip = (lane >> 4) << 1, w0 = r & ~15;
     const float* brow = tab + ((e_r >> 2) + 3) * kP4 + (e_r & 3) + 3;
@@ -853,7 +876,11 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
         load_rows(tdo, prm.dout, tok, valid, warp, lane);
         load_rows(to, prm.o, tok, valid, warp, lane);
         cp_async_commit();
-        const float lse2 = valid ? grad_lse2(__ldg(prm.lse + tok)) : INFINITY;
+        const float lse = valid ? __ldg(prm.lse + tok) : -INFINITY;
+        const float lse2 = grad_lse2(lse);
+        float2 far = make_float2(-lse2, 0.f);
+        const bool is_far = finite_beyond(lse * 1.4426950408889634f, kFar);
+        if (is_far) far = far_row(g, prm.q, prm.k, table_h, prm.buckets, prm.n_buckets, X, r, h, lse * 1.4426950408889634f);
         cp_async_wait<0>();
         __syncwarp();
         float p[16];
@@ -863,8 +890,9 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 const int uu = u ^ flip;
-                p[u] = ex2_approx(fmaf(dot_row(tk, w0 + uu, a), g.scale_log2,
-                                       brow[-((uu >> 2) * kP4 + (uu & 3))] - lse2));
+                const float s = dot_row(tk, w0 + uu, a), b = brow[-((uu >> 2) * kP4 + (uu & 3))];
+                p[u] = ex2_approx(is_far ? far_exponent(fmaf(s, g.scale_log2, b), far.x, far.y)
+                                         : fmaf(s, g.scale_log2, b - lse2));
                 myp[e_r * kXPitch + uu] = p[u];
             }
         }
