@@ -259,3 +259,49 @@ def test_refused_feed_forward():
         ops.gated_mlp_bwd(x, x, w, w, wd, workspace=cuda(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="dy has shape"):
         ops.gated_mlp_bwd(cuda(4, 96), x, w, w, wd)
+
+
+# ------------------------------------------------------------------ threads
+def entry_points():
+    """Calls with every output and workspace given, so that no allocation precedes them; M = 16 and the feed-forward
+    read their tensors through TMA maps."""
+    from vision_transformer_windowed_b200.inputs import make_inputs
+
+    inp = {k: v.cuda() for k, v in make_inputs(1, 32, 32, 2, 32).items()}
+    q, k, v, dout, theta = (inp[n] for n in ("q", "k", "v", "dout", "theta"))
+    table = torch.zeros((2, 31 * 31), device="cuda", dtype=BF16)
+    o, lse, dq, dk, dv = (torch.empty_like(q), torch.empty(q.shape[:4], device="cuda"), *(torch.empty_like(q) for _ in "qkv"))
+    ws, ws_rb = ops.alloc_workspace(q, 16, 8), ops.alloc_relbias_workspace(q, 16, 8)
+    x, w, wd, y = (torch.ones(s, device="cuda", dtype=BF16) for s in ((5, 264), (256, 264), (264, 256), (5, 264)))
+    ws_mlp = torch.empty(1 << 16, device="cuda", dtype=torch.uint8)
+    dtheta, dtable = torch.empty_like(theta), torch.empty_like(table)
+    return dict(
+        rope_fwd=lambda: ops.winattn_fwd(q, k, v, theta, 16, 8, o=o, lse=lse),
+        rope_bwd=lambda: ops.winattn_bwd(q, k, v, o, dout, lse, theta, 16, 8, workspace=ws, dq=dq, dk=dk, dv=dv,
+                                         dtheta=dtheta),
+        relbias_fwd=lambda: ops.winattn_relbias_fwd(q, k, v, table, 16, 8, o=o, lse=lse),
+        relbias_bwd=lambda: ops.winattn_relbias_bwd(q, k, v, o, dout, lse, table, 16, 8, workspace=ws_rb, dq=dq, dk=dk,
+                                                    dv=dv, dtable=dtable),
+        mlp_fwd=lambda: ops.gated_mlp_fwd(x, w, w, wd, y=y, workspace=ws_mlp))
+
+
+def test_first_call_of_a_thread():
+    """A thread that has made no CUDA call yet, as the autograd engine's may be: the library's call is its first."""
+    from threading import Thread
+
+    for name, call in entry_points().items():
+        call()  # what a first call sets up is not at issue
+        torch.cuda.synchronize()
+        raised = []
+
+        def body():
+            try:
+                call()
+            except Exception as e:  # noqa: BLE001
+                raised.append(e)
+
+        t = Thread(target=body)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not raised, f"{name}: {raised[0]}"

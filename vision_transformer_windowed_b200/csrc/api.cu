@@ -28,6 +28,7 @@ unsigned int* g_status_ptr[kMaxDev] = {};
 int g_num_sms[kMaxDev] = {};
 int g_arch_ok[kMaxDev] = {};  // 0 unknown, 1 ok, -1 not sm_100
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_current = nullptr;
 cudaEvent_t g_phase_events[8] = {};
 int g_phase_n = 0;
 
@@ -58,6 +59,19 @@ fs_status device_state(unsigned int** status, int* num_sms) {
             return FS_ERR_CUDA;
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
+    if (!g_current) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return FS_ERR_CUDA;
+        g_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn);
+    }
+    // The encoder of tensor maps is a driver call and binds no context, as a runtime call
+    // does: a thread whose first CUDA call this is (an autograd worker's) has none yet.
+    CUcontext ctx = nullptr;
+    if (g_current(&ctx) != CUDA_SUCCESS) return FS_ERR_CUDA;
+    if (!ctx && cudaSetDevice(dev) != cudaSuccess) return FS_ERR_CUDA;
     *status = g_status_ptr[dev];
     *num_sms = g_num_sms[dev];
     return FS_OK;
