@@ -292,8 +292,9 @@ FS_API fs_status fs_resnorm_bwd(const fs_resnorm_shape* shape, const void* dr, c
  * order: results do not vary from run to run.
  * workspace: at least fs_gated_mlp_{fwd,bwd}_workspace_bytes(shape) bytes, 256-byte
  * aligned (forward 2 bytes a token and hidden channel, or 256 in all where the weights
- * fit into an SM's shared memory; backward 6 bytes a token and hidden channel and 192 a
- * weight of one matrix).
+ * fit into an SM's shared memory; backward 6 bytes a token and hidden channel, and 12 a
+ * weight of one matrix for each part, of 1 to 16, in which the tokens are summed: one up
+ * to 384 tokens, and about one where the weights alone give every SM work).
  */
 typedef enum { FS_ACT_SILU = 0, FS_ACT_GELU = 1 } fs_act;
 typedef struct {

@@ -162,3 +162,24 @@ def test_host_tensors_are_refused():
         ops.residual_norm_fwd(z(96), z(96))
     with pytest.raises(ValueError, match="act must be"):
         ops.gated_mlp_fwd(z(2, 96), z(256, 96), z(256, 96), z(96, 256), act="relu")
+
+
+def mlp_bwd_bytes(tokens, channels, hidden):
+    return _lib.fs_gated_mlp_bwd_workspace_bytes(_lib.MlpShape(tokens, channels, hidden, 0))
+
+
+@pytest.mark.parametrize("channels,hidden", [(8, 8), (96, 256), (1024, 4096), (4096, 16384), (16384, 65536)])
+def test_mlp_workspace_of_few_tokens(channels, hidden):
+    """Up to 384 tokens (a part has four blocks of 64 or more) are summed in one: h and its two gradients, and an fp32 copy of the gradients."""
+    for tokens in (1, 64, 384):
+        need = 6 * tokens * hidden + 12 * channels * hidden + 8 * (2 * hidden + channels)
+        assert need <= mlp_bwd_bytes(tokens, channels, hidden) <= need + 9 * 256
+
+
+@pytest.mark.parametrize("tokens", [449, 5000, 100000, 1 << 24])
+@pytest.mark.parametrize("channels,hidden", [(96, 256), (384, 1024), (1536, 4096), (16384, 65536)])
+def test_mlp_workspace_of_more_tokens(tokens, channels, hidden):
+    """As many copies as there are parts, 16 at most; with weights that give every SM work, hardly more than one."""
+    one = 12 * channels * hidden + 8 * (2 * hidden + channels)
+    parts = (mlp_bwd_bytes(tokens, channels, hidden) - 6 * tokens * hidden) / one
+    assert 1 <= parts <= (3 if channels * hidden >= 1 << 28 else 16) + 9 * 256 / one

@@ -566,15 +566,17 @@ inline bool take_tall(Params* p, int step, int num_sms) {
 
 // Splits of the tokens for the weight gradients: of 1 .. 16 the one with the least
 // work on the busiest SM (waves / splits), more splits costing 1 % each for their
-// partial results; no split shorter than four blocks.
+// partial results; no split shorter than four blocks.  From the shape alone (a B200's SMs),
+// so that the workspace holds the partial results of the splits that are taken, no more.
+constexpr int kSms = 148;
 constexpr int kMaxSplits = 16;
-inline int pick_splits(int tiles, int kblocks, int num_sms) {
+inline int pick_splits(int tiles, int kblocks) {
     int best = 1;
     double cost = 1e30;
     for (int s = 1; s <= kMaxSplits; ++s) {
         const int per = (kblocks + s - 1) / s;
         if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;
-        const double waves = static_cast<double>((static_cast<long long>(tiles) * s + num_sms - 1) / num_sms);
+        const double waves = static_cast<double>((static_cast<long long>(tiles) * s + kSms - 1) / kSms);
         const double c = waves * per * (1.0 + 0.01 * s);
         if (c < cost) {
             cost = c;
@@ -582,6 +584,21 @@ inline int pick_splits(int tiles, int kblocks, int num_sms) {
         }
     }
     return best;
+}
+
+// The weight gradients' launch: tiles of 256 hidden channels and bn channels, three times
+// over, each split.
+struct DwPlan {
+    int bn, tiles_n, tiles, kblocks, splits;
+};
+inline DwPlan dw_plan(const MlpShape& sh) {
+    DwPlan p;
+    p.bn = tile_width(sh.channels, kTallMaxN, 64);
+    p.tiles_n = (sh.channels + p.bn - 1) / p.bn;
+    p.tiles = (sh.hidden + 2 * kBlockM - 1) / (2 * kBlockM) * p.tiles_n;
+    p.kblocks = static_cast<int>((sh.tokens + kBlockK - 1) / kBlockK);
+    p.splits = pick_splits(3 * p.tiles, p.kblocks);
+    return p;
 }
 
 }  // namespace mlp
@@ -596,7 +613,8 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(const MlpShape& sh) {
     const size_t tf = round256(static_cast<size_t>(sh.tokens) * sh.hidden * 2);
-    const size_t cf = static_cast<size_t>(sh.channels) * sh.hidden * 4 * mlp::kMaxSplits;
+    const size_t splits = static_cast<size_t>(mlp::dw_plan(sh).splits);
+    const size_t cf = static_cast<size_t>(sh.channels) * sh.hidden * 4 * splits;
     BwdLayout L{};
     size_t o = 0;
     L.h = o;  o += tf;
@@ -606,7 +624,7 @@ BwdLayout bwd_layout(const MlpShape& sh) {
         L.part[i] = o;
         o += round256(cf);
         L.bias[i] = o;
-        o += round256(static_cast<size_t>(i == 2 ? sh.channels : sh.hidden) * 8 * mlp::kMaxSplits);  // two a split at most
+        o += round256(static_cast<size_t>(i == 2 ? sh.channels : sh.hidden) * 8 * splits);  // two a split at most
     }
     L.total = o;
     return L;
@@ -704,28 +722,27 @@ cudaError_t launch_mlp_bwd(const MlpShape& sh, const MlpPtrs& p, unsigned int* s
     if (e != cudaSuccess) return e;
     // weights and biases
     prm.k = T;
-    prm.bn = tile_width(C, kTallMaxN, 64);
+    const DwPlan plan = dw_plan(sh);
+    prm.bn = plan.bn;
     const void *as[3] = {dg, du, h}, *bs[3] = {p.x, p.x, p.dy};
     void* const outs[6] = {p.dw_gate, p.dw_up, p.dw_down, p.db_gate, p.db_up, p.db_down};
-    const int tiles_n = (C + prm.bn - 1) / prm.bn, tiles = (F + 2 * kBlockM - 1) / (2 * kBlockM) * tiles_n;
     for (int i = 0; i < 3; ++i) {
         Problem& q = prm.pr[i];
         q.m = F;
         q.n = C;
-        q.tiles_n = tiles_n;
-        q.by_n = make_fastdiv(tiles_n);
-        q.first = i * tiles;
+        q.tiles_n = plan.tiles_n;
+        q.by_n = make_fastdiv(plan.tiles_n);
+        q.first = i * plan.tiles;
         q.turned = i == 2;
         q.part = reinterpret_cast<float*>(p.ws + L.part[i]);
         q.bias_part = outs[3 + i] ? reinterpret_cast<float*>(p.ws + L.bias[i]) : nullptr;
         if (encode_matrix(&maps.a[i], as[i], T, F, kBlockK, 64, true) || encode_matrix(&maps.b[i], bs[i], T, C, kBlockK, 64, true))
             return cudaErrorInvalidValue;
     }
-    const int kblocks = (T + kBlockK - 1) / kBlockK;
-    prm.splits = pick_splits(3 * tiles, kblocks, num_sms);
-    prm.blocks_per_split = (kblocks + prm.splits - 1) / prm.splits;
+    prm.splits = plan.splits;
+    prm.blocks_per_split = (plan.kblocks + prm.splits - 1) / prm.splits;
     prm.by_splits = make_fastdiv(prm.splits);
-    prm.tiles = static_cast<unsigned>(3 * tiles) * prm.splits;
+    prm.tiles = static_cast<unsigned>(3 * plan.tiles) * prm.splits;
     if ((e = launch<kDw>(maps, prm, num_sms, stream)) != cudaSuccess) return e;
     SumParams sum{};
     int count = 0;
