@@ -305,3 +305,22 @@ def test_first_call_of_a_thread():
         t.join()
         torch.cuda.synchronize()
         assert not raised, f"{name}: {raised[0]}"
+
+
+# ------------------------------------------------------------------ second derivatives
+def test_no_second_derivative_by_mistake():
+    """The gradients have no gradient of their own: asking for one is refused, not answered with zero."""
+    from vision_transformer_windowed_b200.inputs import make_inputs
+
+    inp = {k: v.cuda().requires_grad_() for k, v in make_inputs(1, 16, 16, 2, 32).items()}
+    q, k, v, theta = (inp[n] for n in ("q", "k", "v", "theta"))
+    u = torch.randn((2, 256, 16), device="cuda", requires_grad=True)
+    table = torch.randn((2, 31 * 31), device="cuda").to(BF16).requires_grad_()
+    x, w, wd = (torch.randn(s, device="cuda").to(BF16).requires_grad_() for s in ((5, 64), (128, 64), (64, 128)))
+    for name, out, leaf in (("rope", ops.window_attention(q, k, v, theta, 16, 0), theta),
+                            ("low rank", ops.window_attention_lrbias(q, k, v, theta, u, u, 16, 0), u),
+                            ("relative bias", ops.window_attention_relbias(q, k, v, table, 16, 0), table),
+                            ("residual step", ops.residual_norm(x, x)[1], x), ("feed-forward", ops.gated_mlp(x, w, w, wd), w)):
+        grad = torch.autograd.grad(out.float().square().sum(), leaf, create_graph=True)[0]
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (grad.float().square().sum() + leaf.float().sum()).backward()

@@ -12,12 +12,16 @@ Shapes: q, k, v [B, H, W, heads, d] bf16 with d = 32 or 64, H >= M and W >= M.  
 need not be a multiple of the window M: the grid is then worked on padded at
 the bottom and right with zero tokens to the next multiple (the Swin layer's
 padding), and only the H x W real tokens are read and written.
+
+The autograd functions are differentiable once: a backward through their
+gradients raises.
 """
 from __future__ import annotations
 
 from collections import namedtuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -153,6 +157,7 @@ class WindowAttentionRoPE(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, theta, *ws = ctx.saved_tensors
         dq, dk, dv, dth = winattn_bwd(q, k, v, o, dout.contiguous(), lse, theta, ctx.M, ctx.s,
@@ -252,6 +257,7 @@ class WindowAttentionLowRankBias(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, u, w, *rest = ctx.saved_tensors
         theta = rest[0] if ctx.has_theta else None
@@ -403,6 +409,7 @@ class WindowAttentionRelativeBias(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, table, *rest = ctx.saved_tensors
         dq, dk, dv, dtable = winattn_relbias_bwd(q, k, v, o, dout.contiguous(), lse, table, ctx.M, ctx.s,
@@ -522,6 +529,7 @@ class ResidualNorm(torch.autograd.Function):
         return r, n
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dn):
         if dr is None and dn is None:
             return (None,) * 13
@@ -603,6 +611,7 @@ class GatedMlp(torch.autograd.Function):
         return gated_mlp_fwd(x, *params, act=act)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, *rest = ctx.saved_tensors
         params = [rest.pop(0) if there else None for there in ctx.present]
