@@ -207,3 +207,13 @@ def test_no_epsilon_and_groups_past_the_last_row(C, rows, pre, post, stream):
     g = ops.residual_norm_bwd(dr.cuda(), dn.cuda(), r, d["f"], **{k: d[k] for k in PARAMS}, **opt)
     for name, got in g._asdict().items():
         close(name, got, at[name], at["terms"].get(name))
+
+
+@pytest.mark.parametrize("B,T", [(70001, 1), (70001, 2), (66000, 3)])
+def test_more_samples_than_blocks_of_the_gate_sum(B, T):
+    g = torch.Generator().manual_seed(1)
+    f, dr = (torch.randn((B, T, 8), generator=g).to(BF16) for _ in "fd")
+    gate = torch.randn(B, generator=g).to(BF16)
+    got = ops.residual_norm_bwd(dr.cuda(), None, dr.cuda(), f.cuda(), gate=gate.cuda(), pre=None)
+    terms = f.double() * dr.double()
+    close("dgate", got.dgate, terms.sum((1, 2)), terms.abs().sum((1, 2)))

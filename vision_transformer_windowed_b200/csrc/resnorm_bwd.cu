@@ -262,20 +262,23 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Params
         }
         return;
     }
-    const unsigned int b = blockIdx.x - col_blocks * kGrads;
+    const unsigned int first = blockIdx.x - col_blocks * kGrads, step = gridDim.x - col_blocks * kGrads;
     const unsigned int n = prm.rows / static_cast<unsigned int>(p.samples);
-    const float* src = prm.rowdot + static_cast<unsigned long long>(b) * n;
-    float a = 0.f;
+    for (long long b = first; b < p.samples; b += step) {
+        const float* src = prm.rowdot + static_cast<unsigned long long>(b) * n;
+        float a = 0.f;
 #pragma unroll 4
-    for (unsigned int i = t; i < n; i += 256) a += src[i];
-    s[t] = a;
-    __syncthreads();
+        for (unsigned int i = t; i < n; i += 256) a += src[i];
+        s[t] = a;
+        __syncthreads();
 #pragma unroll
-    for (int o = 128; o > 0; o >>= 1) {
-        if (t < o) s[t] += s[t + o];
+        for (int o = 128; o > 0; o >>= 1) {
+            if (t < o) s[t] += s[t + o];
+            __syncthreads();
+        }
+        if (t == 0) static_cast<TX*>(p.dgate)[b] = static_cast<TX>(s[0]);
         __syncthreads();
     }
-    if (t == 0) static_cast<TX*>(p.dgate)[b] = static_cast<TX>(s[0]);
 }
 
 template <typename TX>
@@ -338,7 +341,8 @@ struct LaunchBwd {
         const ResnormPtrs& p = prm.p;
         if (!p.dpre_w && !p.dpre_b && !p.dscale && !p.dpost_w && !p.dpost_b && !p.dgate) return cudaSuccess;
         const int col_blocks = (prm.C + 31) / 32;
-        const unsigned samples = p.dgate ? static_cast<unsigned>(p.samples) : 0u;
+        // (samples up to 2^31 - 1 would not fit a grid with the columns)
+        const unsigned samples = !p.dgate ? 0u : static_cast<unsigned>(p.samples < (1 << 16) ? p.samples : 1 << 16);
         sum_kernel<TX><<<col_blocks * kGrads + samples, 256, 0, stream>>>(prm, col_blocks);
         return cudaGetLastError();
     }
