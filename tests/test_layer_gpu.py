@@ -261,6 +261,37 @@ def test_refused_feed_forward():
         ops.gated_mlp_bwd(cuda(4, 96), x, w, w, wd)
 
 
+@pytest.mark.parametrize("stream", [BF16, F32], ids=["bf16", "f32"])
+def test_each_gradient_against_differences(stream):
+    """Each input's gradient along a direction of its own against the slope of the layer's fp64 form: 24 half steps of
+    that gradient's fp64 norm (as for the whole gradient, which this direction sees no more of than its norm)."""
+    t, dn, dr = draw(2, 16, 16, 2, 8, stream, 104, seed=3)
+    leaves = {k: v.cuda().requires_grad_() for k, v in t.items()}
+    n2, r2 = layer(leaves, 8, 4, 0.0, None)
+    got = dict(zip(leaves, torch.autograd.grad([n2, r2], list(leaves.values()), [dn.cuda(), dr.cuda()])))
+    exact = {k: v.double().requires_grad_() for k, v in t.items()}
+    n2_, r2_ = plain(exact, 8, 4, 0.0, None)
+    want = dict(zip(exact, torch.autograd.grad([n2_, r2_], list(exact.values()), [dn.double(), dr.double()])))
+    base = {k: v.double() for k, v in t.items()}
+    for k, v in t.items():
+        # along the gradient, where the slope is its norm, and as far across, where it is none
+        along = want[k] / want[k].norm()
+        way = torch.randn(v.shape, generator=torch.Generator().manual_seed(len(k)), dtype=F64)
+        way -= (way * along).sum() * along
+        way = way / way.norm() + along
+
+        def at(h):
+            n, r = plain({**base, k: base[k] + h * way}, 8, 4, 0.0, None)
+            return float((n * dn.double()).sum() + (r * dr.double()).sum())
+
+        h = 1e-4
+        slope = (at(h) - at(-h)) / (2 * h)
+        size = float(want[k].norm())
+        ours = float((got[k].double().cpu() * way).sum())
+        assert abs(slope - size) <= 1e-3 * size, k
+        assert abs(slope - ours) <= 24 * HALF * size * float(way.norm()), f"{k}: {ours}, {slope}"
+
+
 # ------------------------------------------------------------------ threads
 def entry_points():
     """Calls with every output and workspace given, so that no allocation precedes them; M = 16 and the feed-forward

@@ -306,3 +306,47 @@ def test_a_bias_of_ten_thousand_for_every_key(cfg, value, monkeypatch):
     monkeypatch.setattr(relbias, "EPS_P", 2.0 ** -9)
     ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"])
     compare(run(inp, M, s), ref, err)
+
+
+# CTAs of a B200 that a forward fills with workers of their own (M >= 16: four a CTA and one CTA an SM, M <= 8: four
+# CTAs an SM); the backward has fewer of them.
+WORKERS = 4 * 148
+
+
+@pytest.mark.parametrize("copies,H,W,heads,M,s", [(580, 20, 20, 1, 4, 0), (300, 20, 17, 2, 4, 0), (450, 24, 24, 1, 8, 4),
+                                                 (230, 24, 20, 2, 8, 0), (155, 32, 48, 1, 16, 8), (90, 40, 33, 2, 16, 4),
+                                                 (230, 32, 32, 1, 16, 0), (60, 64, 64, 1, 32, 16), (120, 33, 64, 2, 32, 0),
+                                                 (60, 64, 64, 1, 64, 0), (30, 70, 64, 2, 64, 16)])
+def test_many_items_a_worker(copies, H, W, heads, M, s):
+    """Every worker walks three items or more, forward and backward.  The images are one image times powers of two, drawn
+    for each: q 2^a, k 2^-a, v 2^c, dout 2^e leave P as it is and scale o by 2^c, dv by 2^e, dq by 2^(c+e-a) and dk by
+    2^(c+e+a), exactly.  A tile taken from another item than its own shows."""
+    tiles = -(-copies * -(-H // M) * -(-W // M) * M * M // 128)
+    assert tiles >= 3 * WORKERS // heads
+    one = draw(1, H, W, heads, M)
+    g = torch.Generator().manual_seed(7)
+    a, c, e = (torch.randint(-3, 4, (copies,), generator=g).double() for _ in "ace")
+    power = lambda x: torch.exp2(x).view(-1, 1, 1, 1, 1)  # noqa: E731
+    scaled = lambda name, x: (one[name].double() * power(x)).to(torch.bfloat16)  # noqa: E731
+    many = dict(q=scaled("q", a), k=scaled("k", -a), v=scaled("v", c), dout=scaled("dout", e), table=one["table"])
+    ref, err = relbias.full(one["q"], one["k"], one["v"], one["table"], M, s, dout=one["dout"])
+    got = run(many, M, s)
+    for key, x in (("o", c), ("dq", c + e - a), ("dk", c + e + a), ("dv", e)):
+        back = got[key].double().cpu() * power(-x)
+        compare({key: back}, {key: ref[key].expand_as(back)}, {key: err[key]}, keys=(key,))
+        # (at M = 4 the two windows of a warp add in orders of their own, and dq at M >= 16 as its parts come)
+        if M > 4 and (key != "dq" or M == 8):
+            assert torch.equal(back, back[:1].expand_as(back)), key
+    compare(dict(lse=got["lse"]), dict(lse=ref["lse"].expand_as(got["lse"])), err, keys=("lse",))
+    total = float(torch.exp2(c + e).sum())
+    compare(dict(dtable=got["dtable"]), dict(dtable=ref["dtable"] * total), dict(dtable=err["dtable"] * total), keys=("dtable",))
+
+
+@pytest.mark.parametrize("cfg", [(1, 64, 64, 2, 64, 0), (1, 64, 70, 1, 64, 32)])
+def test_parity_by_buckets_largest_windows(cfg):
+    B, H, W, heads, M, s = cfg
+    buckets, n = ops.log_distance_buckets(M, exact=2, device="cpu")
+    buckets[0, 0], buckets[-1, -1], buckets[M - 1, 0] = -1, n, 2 ** 31 - 1
+    inp = draw(B, H, W, heads, M, n)
+    compare(run(inp, M, s, buckets), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, buckets=buckets,
+                                                  dout=inp["dout"]))
