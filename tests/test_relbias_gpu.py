@@ -350,3 +350,38 @@ def test_parity_by_buckets_largest_windows(cfg):
     inp = draw(B, H, W, heads, M, n)
     compare(run(inp, M, s, buckets), *relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, buckets=buckets,
                                                   dout=inp["dout"]))
+
+
+@pytest.mark.parametrize("copies,H,W,M,s", [(400, 20, 20, 4, 0), (300, 24, 24, 8, 4), (60, 32, 48, 16, 8), (40, 64, 40, 32, 8),
+                                            (30, 64, 64, 64, 0)])
+def test_one_head_of_large_entries_among_others(copies, H, W, M, s):
+    """Many items a worker, the middle head of three masked by the lowest value, captured and replayed: that head is the
+    oracle's uniform softmax in every image, the others' bits are those of a table without large entries."""
+    one = draw(1, H, W, 3, M)
+    many = {k: t if k == "table" else t.expand(copies, *t.shape[1:]).contiguous() for k, t in one.items()}
+    clean = run(many, M, s)
+    one["table"] = many["table"] = many["table"].clone()
+    one["table"][1] = LOWEST
+    ref, err = relbias.full(one["q"], one["k"], one["v"], one["table"], M, s, dout=one["dout"])
+    eager = run(many, M, s)
+    d = {k: t.cuda() for k, t in many.items()}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = ops.winattn_relbias_fwd(d["q"], d["k"], d["v"], d["table"], M, s)
+        dq, dk, dv, dt = ops.winattn_relbias_bwd(d["q"], d["k"], d["v"], o, d["dout"], lse, d["table"], M, s)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    replayed = dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv, dtable=dt)
+    for got in (eager, replayed):
+        for key in ("o", "dq", "dk", "dv"):
+            x = got[key].double().cpu()
+            compare({key: x}, {key: ref[key].expand_as(x)}, {key: err[key]}, keys=(key,))
+        compare(dict(dtable=got["dtable"]), dict(dtable=copies * ref["dtable"]), dict(dtable=copies * err["dtable"]),
+                keys=("dtable",))
+        for h in (0, 2):
+            for key in ("o", "lse", "dk", "dv"):
+                assert torch.equal(got[key][:, :, :, h], clean[key][:, :, :, h]), key
+            assert torch.equal(got["dtable"][h], clean["dtable"][h])
+    for key in ("o", "lse", "dk", "dv", "dtable"):
+        assert torch.equal(eager[key], replayed[key]), key
