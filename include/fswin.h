@@ -203,7 +203,8 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
  * Forward: o and lse (lse may be NULL: inference), overwritten.
  * Backward: dq, dk, dv and dtable (bf16 [heads][n_buckets]: the gradient summed in
  * fp32 over every window of the batch and every pair of the bucket, in a fixed
- * order), all overwritten.  At M >= 16 dq is accumulated in fp32 with bulk
+ * order; at M >= 16 each pair's term is rounded to bf16 first, as dq and dk take it),
+ * all overwritten.  At M >= 16 dq is accumulated in fp32 with bulk
  * reductions whose order varies from run to run; everything else, and at M <= 8
  * every output, is the same from run to run.  workspace: at least
  * fs_winattn_relbias_bwd_workspace_bytes(shape) bytes, 256-byte aligned (M >= 16:

@@ -8,11 +8,14 @@
 // of chunk i with h taken from tensor memory.  Warps 4-19 compute h, eight warps the even
 // chunks and eight the odd ones; it replaces their u columns as bf16.  Warps 20-23 store
 // y.  Tensor memory: three chunks of g and u (128 columns each), so that a group of warps
-// finds its next chunk ready (two chunks and two tiles of y: 129 us in place of 118), and
+// finds its next chunk ready (with two chunks and two tiles of y a tenth slower), and
 // one tile of y, or two of up to 64 channels.
 //
-// The activation's arithmetic bounds it: 524288 x 96 x 256 with gelu take 118 us, where
-// the two products apart take 187 (h alone is 268 MB, written and read).
+// 524288 x 96 x 256 with gelu take 126 us (two kernels 189: h alone is 268 MB, written and
+// read).  No unit is full (issue slots 64 %, special function 54 %, multiply-add 52 %, tensor
+// 29 %).  With a product in the activation's place it takes 100 us: what a chunk passes on
+// its way (product, tensor memory to registers and back, product) takes most of the time,
+// and the activation, which the other group's chunk hides in part, a quarter on top.
 #include "mlp.cuh"
 
 namespace fswin {

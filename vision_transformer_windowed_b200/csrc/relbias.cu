@@ -15,8 +15,10 @@
 // Times on one B200 (3 heads): forward of 32 x 128 x 128 tokens, M = 32, shifted: 537 us,
 // 294 TFLOP/s, the exponentials alone 274 us; of 2 x 200 x 334, M = 16: 80 us.  Backward of
 // 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 875 us (294 TFLOP/s), post 23 us
-// (6.6 TB/s), sums 5 us.  Forward and main are bound by instruction issue and by the
-// waits between their links, not by the tensor products or the memory.
+// (6.6 TB/s), sums 5 us, the second launch for far tables 5 us.  M = 64, 16 x 128 x 128: forward
+// 1302 us, main 6250 us; shifted by 32: 895 and 2346 us.  No unit is full (8 x 128 x 128, M =
+// 32, forward and main: issue slots 59 and 52 %, special function 59 and 22 %, tensor 14 and
+// 14 %, DRAM 5 %): the waits between the links of a chain are what is left.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -549,7 +551,8 @@ struct Params {
 };
 
 // prep: per (tile, head), thread = slot row: D = dO . O and the row's log-sum-exp
-// in base-2 units, and the zeroed dQ accumulator row.  Memory only.
+// in base-2 units, and the zeroed dQ accumulator row.  Memory only, but for rows whose
+// log-sum-exp is a far one.
 __global__ void __launch_bounds__(128, 16) prep_kernel(const __grid_constant__ Params p) {
     const Geo& g = p.g;
     const long long T = blockIdx.x / g.heads;

@@ -43,7 +43,7 @@ __host__ __device__ constexpr int displacements(int M) { return (2 * M - 1) * (2
 // The head's table in the softmax's base-2 units.  A bucket outside the table
 // adds no bias.  Finite entries are held within +-2^126, so that log2(e) times
 // them stays finite and a row whose every entry is the type's lowest value is the
-// uniform row it is in exact arithmetic; -inf stays -inf (the pair never attends).
+// uniform row it is in any floating-point type; -inf stays -inf (the pair never attends).
 __device__ __forceinline__ float bias_entry(const __nv_bfloat16* table_h, const int* buckets, int n_buckets, int delta) {
     const int b = buckets ? __ldg(buckets + delta) : delta;
     if (b < 0 || b >= n_buckets) return 0.f;

@@ -6,9 +6,9 @@
 // The norms' rows are formed again from r and f, and the mask is drawn again, so
 // nothing but r and f is kept from the forward.  dr, dn, r, f are read and dx, df
 // written once: 64 x 256 rows of 384 channels, fp32 stream, with dropout, layer scale and
-// gate take 32 us, 3.5 TB/s: four reductions one after the other a row, with 16 warps an
-// SM to hide them, and the arithmetic of the mask; 3 x 1111 rows of 1001 channels with
-// both norms 30 us (a chunk a lane: 34).  The parameters' gradients add up over the rows of a block (a lane
+// gate take 32 us, 3.5 TB/s; 3 x 1111 rows of 1001 channels with both norms 30 us (a chunk a
+// lane: 34).  No unit is full (the first: issue slots 45 %, integer pipe 41 %, DRAM 30 %): the
+// 16 warps an SM wait, for memory most, then for their reductions.  The parameters' gradients add up over the rows of a block (a lane
 // always holds the same channels), then over the block's row groups, and a second launch
 // adds the blocks' sums in order: no atomics, the same bits every run.
 #include "resnorm.cuh"
