@@ -355,3 +355,39 @@ def test_no_second_derivative_by_mistake():
         grad = torch.autograd.grad(out.float().square().sum(), leaf, create_graph=True)[0]
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (grad.float().square().sum() + leaf.float().sum()).backward()
+
+
+def test_threads_at_once():
+    """Four host threads, a stream and tensors each, the whole layer forward and backward."""
+    from threading import Thread
+
+    sets = [draw(2, 32, 32, 2, 16, BF16, 136, seed=i) for i in range(4)]
+    cuda = [({k: v.cuda().requires_grad_() for k, v in t.items()}, dn.cuda(), dr.cuda()) for t, dn, dr in sets]
+
+    def step(i):
+        t, dn, dr = cuda[i]
+        n2, r2 = layer(t, 16, 8, 0.0, None)
+        return (n2, r2, *torch.autograd.grad([n2, r2], list(t.values()), [dn, dr]))
+
+    alone = [[x.detach().clone() for x in step(i)] for i in range(4)]
+    torch.cuda.synchronize()
+    got, raised = [None] * 4, []
+
+    def body(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = step(i)
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+
+    threads = [Thread(target=body, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not raised, raised[0]
+    for i in range(4):
+        for name, a, b in zip(("n2", "r2", *cuda[i][0]), got[i], alone[i]):  # as for two streams
+            near(name, a, b.double().cpu(), 2)
