@@ -385,3 +385,18 @@ def test_one_head_of_large_entries_among_others(copies, H, W, M, s):
             assert torch.equal(got["dtable"][h], clean["dtable"][h])
     for key in ("o", "lse", "dk", "dv", "dtable"):
         assert torch.equal(eager[key], replayed[key]), key
+
+
+@pytest.mark.parametrize("value", [-1e9, 3e7])
+@pytest.mark.parametrize("B,H,M,s", [(8, 128, 4, 0), (8, 128, 8, 4), (8, 128, 16, 8), (8, 128, 32, 0), (4, 128, 64, 32)])
+def test_one_key_of_a_large_bias_and_large_scores(B, H, M, s, value):
+    """Every query has its own token for its only key, and scores of thousands beside a bias whose steps are 4 or 128 (in
+    base 2): whichever way a score is rounded there, P is 1, o = v and dv = dout."""
+    inp = draw(B, H, H, 3, M, qk_scale=30.0)
+    inp["table"][:] = -INF
+    inp["table"][:, (2 * M - 1) ** 2 // 2] = value
+    got = run(inp, M, s)
+    assert torch.equal(got["o"].cpu(), inp["v"]) and torch.equal(got["dv"].cpu(), inp["dout"])
+    # dP - D is a rounding of two equal sums of 32 products of about 1
+    for key, size in (("dq", 30.0), ("dk", 30.0)):
+        assert got[key].float().abs().max() <= 2.0 ** -10 * size, key

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(128, 16) prep_kernel(const __grid_constant__ P
                         lse * 1.4426950408889634f);
     }
     // Rows with a second term have no probability for the main kernel; the one for far
-    // tables looks here for every row that has none.
+    // tables looks here for every row that has none (a second term of 0: no key).
     if (l.y != 0.f || l.x == -INFINITY) {
         p.far[ht * kTile + r] = l;
         l.x = -INFINITY;
@@ -943,9 +943,10 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
         };
         uint8_t* dsrow = wsm + wg * 16384 + (r >> 3) * 1024 + (r & 7) * 128;
         const uint32_t wbase = smem_u32(wsm);
-        uint32_t step = 0;
+        uint32_t step = 0, item = 0;
         bool ok = true;
-        for (long long X = X0; X < g.tiles && ok; X += stride) {
+        for (long long X = X0; X < g.tiles && ok; X += stride, ++item) {
+            const uint32_t kvb = kvs == 2 ? item & 1u : 0u;  // where the item's keys are
             const Item I = item_of(g, &bars->masks, X);
             int ki, kj;
             long long ktok;
@@ -964,12 +965,20 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                 const float* bt = brow + tile_offset(g, T, pitch);
                 const float4* neg_l = reinterpret_cast<const float4*>(stg + 2 * kTileBytes);  // of four queries each
                 const float4* neg_d = neg_l + kTile / 4;
-                if (!wwait(&wb.st_full[ph], (step >> 1) & 1u, 0x7506) || !wwait(&wb.s_full, ph, 0x7507)) {
+                if (!wwait(&wb.st_full[ph], (step >> 1) & 1u, 0x7506) || !wwait(&wb.s_full, ph, 0x7507) ||
+                    (kFarTable && !wwait(&wb.kv_full[kvb], kvs == 2 ? (item >> 1) & 1u : item & 1u, 0x750a))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float2* terms = prm.far + (item0 + I.w0 + T) * kTile;
+                // log2 P of query c from its score t: rows without one in `l` have two terms
+                auto far_exponent = [&](float t, float l, int c, float bias) -> float {
+                    if (l != -INFINITY) return t + l;
+                    const float2 f = __ldg(prm.far + (item0 + I.w0 + T) * kTile + c);
+                    if (f.y == 0.f) return t + f.x;  // no key
+                    const float d = shared_dot(stg, c, wsm + kKVOff + kvb * 2 * kTileBytes, r);
+                    return (fmaf(d, sl2, bias) + f.x) + f.y;
+                };
                 auto gradient_half = [&](auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
 #pragma unroll 1
@@ -992,12 +1001,10 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                                 const int i = e + f;
                                 float p0, p1, d0, d1;
                                 if (kFarTable) {
-                                    float2 l0 = make_float2(f ? L.z : L.x, 0.f), l1 = make_float2(f ? L.w : L.y, 0.f);
-                                    if (l0.x == -INFINITY) l0 = __ldg(terms + 16 * c16 + 2 * i);
-                                    if (l1.x == -INFINITY) l1 = __ldg(terms + 16 * c16 + 2 * i + 1);
+                                    const int c = 16 * c16 + 2 * i;
                                     unpair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]), p0, p1);
-                                    p0 = far_exponent(p0, l0.x, l0.y);
-                                    p1 = far_exponent(p1, l1.x, l1.y);
+                                    p0 = far_exponent(p0, f ? L.z : L.x, c, bias[2 * i]);
+                                    p1 = far_exponent(p1, f ? L.w : L.y, c + 1, bias[2 * i + 1]);
                                 } else {
                                     unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
                                                     f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);

@@ -81,12 +81,35 @@ __device__ __forceinline__ float grad_lse2(float lse) {
     return fabsf(v) > 1e30f ? INFINITY : v;  // a NaN stays one
 }
 
+// s + the dot product of eight channels, in an order of its own: the same bits wherever
+// the four chunks of two rows are added up.
+__device__ __forceinline__ float add_chunk(float s, const uint4& a, const uint4& b) {
+    const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        s = fmaf(bf16lo_to_f32(as[e]), bf16lo_to_f32(bs[e]), fmaf(bf16hi_to_f32(as[e]), bf16hi_to_f32(bs[e]), s));
+    return s;
+}
+// Rows of 64-byte-swizzled tiles in shared memory.
+static __device__ __noinline__ float shared_dot(const uint8_t* tile_a, int a, const uint8_t* tile_b, int b) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c)
+        s = add_chunk(s, *reinterpret_cast<const uint4*>(tile_a + a * kRowBytes + ((c ^ ((a >> 1) & 3)) << 4)),
+                      *reinterpret_cast<const uint4*>(tile_b + b * kRowBytes + ((c ^ ((b >> 1) & 3)) << 4)));
+    return s;
+}
+
 // Rows whose every key has a large bias (the type's lowest value as a mask, say) have a
 // log-sum-exp in which the sum of their exponentials is lost.  For them P = exp2((t - m) -
 // log2 l) with the maximum m and the sum l of the row's own scores, formed again here, key
-// by key on the CUDA cores: rare, so it may be slow.  The result (x, y) stands for the two
-// terms of log2 P = (t + x) + y.  A far log-sum-exp that the scores alone make (no far
-// entry) stays what it is.
+// by key on the CUDA cores: rare, so it may be slow.  The scores t that join them in P are
+// formed in the same way (add_chunk), not taken from the tensor product: beside a bias of 1e9
+// a score is rounded to multiples of 128, and where the two products round to different
+// sides of such a step, a row's one key would weigh 2^128 or nothing.
+// The result (x, y) stands for the two terms of log2 P = (t + x) + y; y < 0 marks a row that
+// has them, also where l = 1.  A far log-sum-exp that the scores alone make (no far entry)
+// stays what it is.
 // X, r: the row's tile and slot.  lse2: its log-sum-exp, far.
 static __device__ __noinline__ float2 far_row(const Geo& g, const uint8_t* q, const uint8_t* k,
                                               const __nv_bfloat16* table_h, const int* buckets, int n_buckets,
@@ -114,13 +137,7 @@ static __device__ __noinline__ float2 far_row(const Geo& g, const uint8_t* q, co
         if ((cut_i && (i >= edge) != (pi >= edge)) || (cut_j && (j >= edge) != (pj >= edge))) continue;
         const uint4* key = row_at(k, i, j);
         float s = 0.f;
-        for (int c = 0; key && c < 4; ++c) {
-            const uint4 a = __ldg(mine + c), b = __ldg(key + c);
-            const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s = fmaf(bf16lo_to_f32(as[e]), bf16lo_to_f32(bs[e]), fmaf(bf16hi_to_f32(as[e]), bf16hi_to_f32(bs[e]), s));
-        }
+        for (int c = 0; key && c < 4; ++c) s = add_chunk(s, __ldg(mine + c), __ldg(key + c));
         const float bias = bias_entry(table_h, buckets, n_buckets, (pi - i + g.M - 1) * (2 * g.M - 1) + pj - j + g.M - 1);
         far |= finite_beyond(bias, kFar / 2);
         const float t = fmaf(s, g.scale_log2, bias);
@@ -132,13 +149,8 @@ static __device__ __noinline__ float2 far_row(const Geo& g, const uint8_t* q, co
         }
     }
     if (!far) return make_float2(-grad_lse2(lse2 * 0.69314718055994530942f), 0.f);
-    return fabsf(m) > kFar ? make_float2(-m, -lg2_approx(l)) : make_float2(-(m + lg2_approx(l)), 0.f);
-}
-
-// log2 P of a far table's rows: P is at most 1, also where t rounds to another side than m did.
-__device__ __forceinline__ float far_exponent(float t, float x, float y) {
-    const float d = t + x;
-    return (d > 0.f ? 0.f : d) + y;  // a NaN stays one
+    const float y = -lg2_approx(l);
+    return fabsf(m) > kFar ? make_float2(-m, y == 0.f ? -1e-30f : y) : make_float2(y - m, 0.f);
 }
 
 // Every CTA serves one head (its table, and the table gradient it sums, belong to

@@ -597,6 +597,11 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
             if (j + 1 < n) lse = lse_of(j + 1);
             if (!wwait(&bars->s_full, ph, 0x7307)) break;
             tc_fence_after();
+            // log2 P of query q from its score t: rows with two terms have scores of their own
+            auto far_exponent = [&](float t, float l, int q, float bias) -> float {
+                if (far_y[q] == 0.f) return t + l;
+                return (fmaf(shared_dot(sl, q, sl + kTileBytes, r), g.scale_log2, bias) + l) + far_y[q];
+            };
             auto gradient = [&](auto far) {
                 constexpr bool kFarTable = decltype(far)::value;  // rows may have a second term
 #pragma unroll
@@ -620,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const __grid_constant_
                             const int i = e + f;
                             float p0, p1;
                             if (kFarTable) {
-                                const float* y = far_y + 64 * wi + 16 * c + 2 * i;
+                                const int q = 64 * wi + 16 * c + 2 * i;
                                 unpair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]), p0, p1);
-                                p0 = far_exponent(p0, f ? L.z : L.x, y[0]);
-                                p1 = far_exponent(p1, f ? L.w : L.y, y[1]);
+                                p0 = far_exponent(p0, f ? L.z : L.x, q, brow[slot_off<kBW>(16 * c + 2 * i)]);
+                                p1 = far_exponent(p1, f ? L.w : L.y, q + 1, brow[slot_off<kBW>(16 * c + 2 * i + 1)]);
                             } else {
                                 unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
                                                 f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
@@ -855,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
     const Geo& g = prm.g;
     const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
     const int h = blockIdx.x % g.heads, stream = blockIdx.x / g.heads;
-    const __nv_bfloat16* table_h = prm.table + static_cast<long long>(h) * prm.n_buckets;
-    build_bias(tab, kP4, table_h, prm.buckets, prm.n_buckets, 4, r, kThreads);
+    build_bias(tab, kP4, prm.table + static_cast<long long>(h) * prm.n_buckets, prm.buckets, prm.n_buckets, 4, r,
+               kThreads);
     __syncthreads();
     const int e_r = r & 15, flip = (lane >> 4) << 1, w0 = r & ~15;
     const float* brow = tab + ((e_r >> 2) + 3) * kP4 + (e_r & 3) + 3;
@@ -879,9 +884,7 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
         cp_async_commit();
         const float lse = valid ? __ldg(prm.lse + tok) : -INFINITY;
         const float lse2 = grad_lse2(lse);
-        float2 far = make_float2(-lse2, 0.f);
         const bool is_far = finite_beyond(lse * 1.4426950408889634f, kFar);
-        if (is_far) far = far_row(g, prm.q, prm.k, table_h, prm.buckets, prm.n_buckets, X, r, h, lse * 1.4426950408889634f);
         cp_async_wait<0>();
         __syncwarp();
         float p[16];
@@ -892,10 +895,20 @@ __global__ void __launch_bounds__(kThreads, 3) bwd_kernel(const __grid_constant_
             for (int u = 0; u < 16; ++u) {
                 const int uu = u ^ flip;
                 const float s = dot_row(tk, w0 + uu, a), b = brow[-((uu >> 2) * kP4 + (uu & 3))];
-                p[u] = ex2_approx(is_far ? far_exponent(fmaf(s, g.scale_log2, b), far.x, far.y)
-                                         : fmaf(s, g.scale_log2, b - lse2));
-                myp[e_r * kXPitch + uu] = p[u];
+                p[u] = is_far ? fmaf(s, g.scale_log2, b) : ex2_approx(fmaf(s, g.scale_log2, b - lse2));
             }
+            if (is_far) {  // the maximum and the sum of the row's scores, as in the forward
+                float m = p[0], l = 0.f;
+#pragma unroll
+                for (int u = 1; u < 16; ++u) m = fmaxf(m, p[u]);
+#pragma unroll
+                for (int u = 0; u < 16; ++u) l += p[u] = ex2_approx(p[u] - m);
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int u = 0; u < 16; ++u) p[u] *= inv;
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) myp[e_r * kXPitch + (u ^ flip)] = p[u];
         }
         float acc[32];
 #pragma unroll
