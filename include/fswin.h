@@ -208,7 +208,7 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
  * reductions whose order varies from run to run; everything else, and at M <= 8
  * every output, is the same from run to run.  workspace: at least
  * fs_winattn_relbias_bwd_workspace_bytes(shape) bytes, 256-byte aligned (M >= 16:
- * 144 bytes per token-head on the padded grid; and 4 bytes a displacement for
+ * 145 bytes per token-head on the padded grid; and 4 bytes a displacement for
  * every head and CTA).  Other arguments, layouts, ownership and errors as
  * fs_winattn_fwd / fs_winattn_bwd.  At M = 8 and M = 4, where windows share a
  * tile, values that are not finite stay inside their own window.

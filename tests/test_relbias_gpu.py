@@ -400,3 +400,21 @@ def test_one_key_of_a_large_bias_and_large_scores(B, H, M, s, value):
     # dP - D is a rounding of two equal sums of 32 products of about 1
     for key, size in (("dq", 30.0), ("dk", 30.0)):
         assert got[key].float().abs().max() <= 2.0 ** -10 * size, key
+
+
+@pytest.mark.parametrize("B,H,W,M,s", [(3, 24, 16, 8, 4), (40, 48, 80, 8, 4), (3, 48, 32, 16, 8), (40, 48, 32, 16, 8),
+                                       (2, 96, 64, 32, 16), (1, 128, 64, 64, 32)])
+def test_large_entries_that_only_some_windows_feel(B, H, W, M, s):
+    """Only keys half a window above or below are without the mask: every query of an ordinary window has one, and no
+    query of the last row of windows, which the shift cuts there."""
+    inp = draw(1, H, W, 2, M)
+    inp["table"][:, places(M)[0].abs() != M // 2] = LOWEST
+    ref, err = relbias.full(inp["q"], inp["k"], inp["v"], inp["table"], M, s, dout=inp["dout"])
+    far = ref["lse"] < -1e30
+    assert 0 < far.sum() < far.numel()
+    many = {k: t if k == "table" else t.expand(B, *t.shape[1:]).contiguous() for k, t in inp.items()}
+    got = run(many, M, s)
+    for key in ("o", "dq", "dk", "dv"):
+        x = got[key].double().cpu()
+        compare({key: x}, {key: ref[key].expand_as(x)}, {key: err[key]}, keys=(key,))
+    compare(dict(dtable=got["dtable"]), dict(dtable=B * ref["dtable"]), dict(dtable=B * err["dtable"]), keys=("dtable",))

@@ -14,7 +14,7 @@
 //
 // Times on one B200 (3 heads): forward of 32 x 128 x 128 tokens, M = 32, shifted: 537 us,
 // 294 TFLOP/s, the exponentials alone 274 us; of 2 x 200 x 334, M = 16: 80 us.  Backward of
-// 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 875 us (294 TFLOP/s), post 23 us
+// 16 x 128 x 128, M = 32: prep 34 us (6.2 TB/s), main 861 us (299 TFLOP/s), post 23 us
 // (6.6 TB/s), sums 5 us, the second launch for far tables 5 us.  M = 64, 16 x 128 x 128: forward
 // 1302 us, main 6250 us; shifted by 32: 895 and 2346 us.  No unit is full (8 x 128 x 128, M =
 // 32, forward and main: issue slots 59 and 52 %, special function 59 and 22 %, tensor 14 and
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace bwd {
 
 struct WsLayout {
-    size_t acc, rowv, far, part, disp, total;
+    size_t acc, rowv, far, flags, part, disp, total;
     int streams;  // partial sums of the table gradient a head
 };
 
@@ -520,6 +520,7 @@ __host__ inline WsLayout ws_layout(const Geo& g) {
         L.acc = o;  o += round256(ht * kTile * kHeadDim * 4);  // fp32 dQ [heads][tiles][128][32], 16-byte chunks permuted
         L.rowv = o; o += round256(ht * kTile * 8);             // per (head, tile): -lse log2(e) [128], -D [128]
         L.far = o;  o += round256(ht * kTile * 8);             // far_row's terms, of rows whose -lse log2(e) is -inf
+        L.flags = o; o += round256(ht * 16);                   // per (head, tile), a bit a row: it has two terms
         const int W = workers(g);
         L.streams = W * streams_per_head((g.tiles + W - 1) / W, g.heads, kSms);
     } else {
@@ -542,6 +543,7 @@ struct Params {
     float* acc;
     float* rowv;
     float2* far;
+    uint32_t* flags;
     float* part;
     unsigned int* status;
     unsigned long long limit_ns;
@@ -588,6 +590,8 @@ __global__ void __launch_bounds__(128, 16) prep_kernel(const __grid_constant__ P
     }
     // Rows with a second term have no probability for the main kernel; the one for far
     // tables looks here for every row that has none (a second term of 0: no key).
+    const uint32_t two = __ballot_sync(0xFFFFFFFFu, l.y != 0.f);
+    if ((r & 31) == 0) p.flags[ht * 4 + (r >> 5)] = two;
     if (l.y != 0.f || l.x == -INFINITY) {
         p.far[ht * kTile + r] = l;
         l.x = -INFINITY;
@@ -758,11 +762,12 @@ struct Diag {
     }
 };
 
-// kFarTable: a second launch, in which CTAs of heads without far entries leave at once.  It
-// takes all rows, those with a second term (prep_kernel) among them, forms dK, dV and the
-// table's sums again, and adds dQ of those rows alone.  A branch of the one kernel, or a way
-// out of it, would be simpler, but made it slower for every call (16 x 128 x 128, M = 32:
-// 875 us; with either 912 to 915, and the second launch takes 5).
+// kFarTable: a second launch for rows with two terms (prep_kernel), from which CTAs leave at
+// once whose head's table has no far entry, or whose windows no such row.  It forms dK and dV
+// again, with those rows among the others, and adds to dQ and the table's sums the part of
+// those rows alone.  A branch of the one kernel, or a way out of it, would be simpler, but
+// made it slower for every call (16 x 128 x 128, M = 32: 875 us; with either 912 to 915, and
+// the second launch takes 5).
 template <int kBW, int kWorkers, bool kFarTable>
 __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     main_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -789,6 +794,15 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     if (kFarTable &&
         !__syncthreads_or(build_bias(tab, pitch, table_h, prm.buckets, prm.n_buckets, g.M, tid, kThreads)))
         return;
+    if (kFarTable) {  // the four words of every query tile of every item
+        uint32_t some = 0;
+        const long long first = static_cast<long long>(kWorkers) * (blockIdx.x / g.heads);
+        for (int w = 0; w < kWorkers; ++w)
+            for (long long X = first + w; X < g.tiles; X += stride)
+                for (int e = tid; e < 4 * g.tpw; e += kThreads)
+                    some |= __ldg(prm.flags + (item0 + (X & ~static_cast<long long>(g.tpw - 1))) * 4 + e);
+        if (!__syncthreads_or(some != 0)) return;
+    }
 
     if (tid == 0) {
         for (int w = 0; w < kWorkers; ++w) {
@@ -971,11 +985,13 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                     break;
                 }
                 tc_fence_after();
-                // log2 P of query c from its score t: rows without one in `l` have two terms
-                auto far_exponent = [&](float t, float l, int c, float bias) -> float {
+                // log2 P of query c from its score t: rows without one in `l` have two terms, or no key
+                auto far_exponent = [&](float t, float l, int c, float bias, bool* two) -> float {
+                    *two = false;
                     if (l != -INFINITY) return t + l;
                     const float2 f = __ldg(prm.far + (item0 + I.w0 + T) * kTile + c);
-                    if (f.y == 0.f) return t + f.x;  // no key
+                    if (f.y == 0.f) return t + f.x;
+                    *two = true;
                     const float d = shared_dot(stg, c, wsm + kKVOff + kvb * 2 * kTileBytes, r);
                     return (fmaf(d, sl2, bias) + f.x) + f.y;
                 };
@@ -991,7 +1007,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                         unsigned long long t[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) t[e] = pair(bias[2 * e], bias[2 * e + 1]);
-                        uint32_t wp[8], wd[8];
+                        uint32_t wp[8], wd[8], ws[8];  // ws: what dQ and the table's sums take of wd
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
@@ -1000,11 +1016,12 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                             for (int f = 0; f < 2; ++f) {
                                 const int i = e + f;
                                 float p0, p1, d0, d1;
+                                bool two[2] = {true, true};
                                 if (kFarTable) {
                                     const int c = 16 * c16 + 2 * i;
                                     unpair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]), p0, p1);
-                                    p0 = far_exponent(p0, f ? L.z : L.x, c, bias[2 * i]);
-                                    p1 = far_exponent(p1, f ? L.w : L.y, c + 1, bias[2 * i + 1]);
+                                    p0 = far_exponent(p0, f ? L.z : L.x, c, bias[2 * i], &two[0]);
+                                    p1 = far_exponent(p1, f ? L.w : L.y, c + 1, bias[2 * i + 1], &two[1]);
                                 } else {
                                     unpair(add_pair(fma_pair(pair(sv[2 * i], sv[2 * i + 1]), sl2_2, t[i]),
                                                     f ? pair(L.z, L.w) : pair(L.x, L.y)), p0, p1);
@@ -1015,6 +1032,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                                                          f ? pair(D.z, D.w) : pair(D.x, D.y)), pair(p0, p1)), d0, d1);
                                 wp[i] = pack_bf16x2(p0, p1);
                                 wd[i] = pack_bf16x2(d0, d1);
+                                if (kFarTable) ws[i] = wd[i] & ((two[0] ? 0xFFFFu : 0u) | (two[1] ? 0xFFFF0000u : 0u));
                             }
                         }
                         if (kMasked) {
@@ -1023,6 +1041,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                             for (int e = 0; e < 8; ++e) {
                                 wp[e] = on ? wp[e] : 0u;
                                 wd[e] = on ? wd[e] : 0u;
+                                if (kFarTable) ws[e] = on ? ws[e] : 0u;
                             }
                         }
                         tmem_st8(trow + kColS + 64 * wg + 8 * hc, wp);
@@ -1030,7 +1049,8 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
 #pragma unroll
                         for (int q4 = 0; q4 < 2; ++q4)
                             *reinterpret_cast<uint4*>(dsrow + (((2 * hc + q4) ^ (r & 7)) << 4)) =
-                                make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
+                                kFarTable ? make_uint4(ws[4 * q4], ws[4 * q4 + 1], ws[4 * q4 + 2], ws[4 * q4 + 3])
+                                          : make_uint4(wd[4 * q4], wd[4 * q4 + 1], wd[4 * q4 + 2], wd[4 * q4 + 3]);
                     }
                 };
                 if (kFarTable || I.kind) gradient_half(std::true_type{});
@@ -1051,10 +1071,6 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
                     tmem_ld32(trow + (wg == 0 ? kColDV : kColDK), v);
                     tmem_ld16(trow + kColDQ + 16 * wg, q);
                     tmem_wait_ld();
-                    if (kFarTable && reinterpret_cast<const float*>(neg_l)[r] != -INFINITY) {  // added by the first launch
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) q[e] = 0u;
-                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) acc[e] = add_pair(acc[e], pair(v[2 * e], v[2 * e + 1]));
                     // half of dQ's query row over the step's Q and dO tiles, 16-byte chunks
@@ -1092,7 +1108,7 @@ __global__ void __launch_bounds__(256 * kWorkers + 128, 1)
     if (warp == 8 * kWorkers) tmem_dealloc(bars->tmem_base, 256 * kWorkers);
     if (computes) {
         float* dst = prm.part + (X0 * g.heads + h) * static_cast<long long>(side * side);
-        for (int e = tid & 255; e < side * side; e += 256) dst[e] = sums[e];
+        for (int e = tid & 255; e < side * side; e += 256) dst[e] = kFarTable ? dst[e] + sums[e] : sums[e];
     }
 }
 
@@ -1270,6 +1286,7 @@ cudaError_t launch_relbias_bwd(const Geo& g, const RelbPtrs& p, const RelbMaps& 
         prm.acc = reinterpret_cast<float*>(p.ws + L.acc);
         prm.rowv = reinterpret_cast<float*>(p.ws + L.rowv);
         prm.far = reinterpret_cast<float2*>(p.ws + L.far);
+        prm.flags = reinterpret_cast<uint32_t*>(p.ws + L.flags);
         prm.part = part;
         prm.status = status;
         prm.limit_ns = limit_ns;

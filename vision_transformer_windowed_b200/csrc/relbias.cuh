@@ -109,7 +109,9 @@ static __device__ __noinline__ float shared_dot(const uint8_t* tile_a, int a, co
 // sides of such a step, a row's one key would weigh 2^128 or nothing.
 // The result (x, y) stands for the two terms of log2 P = (t + x) + y; y < 0 marks a row that
 // has them, also where l = 1.  A far log-sum-exp that the scores alone make (no far entry)
-// stays what it is.
+// stays what it is.  Where every row is such a one a backward takes 1.6 ms in place of 0.15
+// (64 x 64 x 64 tokens, 3 heads, M = 8) or 23 in place of 0.98 (16 x 128 x 128, M = 32); with
+// large entries but no such row 0.15 in place of 0.11 and 0.96 in place of 0.94.
 // X, r: the row's tile and slot.  lse2: its log-sum-exp, far.
 static __device__ __noinline__ float2 far_row(const Geo& g, const uint8_t* q, const uint8_t* k,
                                               const __nv_bfloat16* table_h, const int* buckets, int n_buckets,
