@@ -196,8 +196,8 @@ FS_API fs_status fs_winattn_lrbias_bwd(const fs_winattn_shape* shape, const void
  * key has a large entry (the type's lowest value as a mask, say) has the softmax of its
  * biased scores as fp32 holds them, the uniform one where a step of fp32 exceeds the
  * scores (from about 1e9 on), forward and backward alike.  (The backward forms such a
- * row's maximum and sum again, key by key, which is slow.)  Where the scores q . k alone
- * make a log-sum-exp beyond 2800 in magnitude, the gradient carries fp32's step there
+ * row's maximum and sum again, key by key, which is slow.)  Where, at M >= 8, the scores
+ * q . k alone make a log-sum-exp beyond 2800 in magnitude, the gradient carries fp32's step there
  * (2^-11 of a probability, growing with it), and has no part of the query beyond 7e29.
  *
  * Forward: o and lse (lse may be NULL: inference), overwritten.
